@@ -2,7 +2,7 @@
  * kvq.h -- C ABI of libkvq: GB300 (sm_103a) kernels for the write and read
  * hot path of a paged quantized KV cache.
  *
- * Two operations:
+ * Operations:
  *
  *   kvq_store_nvfp4       bf16 K/V -> NVFP4, scattered into paged cache pages
  *                         (vLLM csrc/libtorch_stable/nvfp4_kv_cache_kernels.cu,
@@ -21,6 +21,13 @@
  *                         sequence) over the NVFP4 pages (vLLM PR #12348
  *                         "[ROCm] Faster Custom Paged Attention kernels":
  *                         the paged_attention op).
+ *   kvq_chunk_attention_nvfp4  causal attention of chunks of new tokens
+ *                         (pieces of prompts, drafts to verify, single
+ *                         tokens, in one ragged batch) over the NVFP4 pages.
+ *   kvq_extend_sequences, kvq_fork_sequences, kvq_compact_sequences,
+ *   kvq_free_sequences    the state of a paged cache on the device: page
+ *                         counts, block tables and lengths.
+ *   kvq_copy_pages, kvq_move_tokens_nvfp4  the bytes that go with them.
  *
  * Conventions shared by every entry point:
  *   - Every buffer pointer is DEVICE memory owned by the caller, on the
@@ -56,7 +63,9 @@ typedef enum {
   KVQ_ERR_CUDA = -6,    /* the CUDA runtime reported an error at launch */
   KVQ_ERR_ARG = -7,     /* unknown flag bits or inconsistent arguments */
   KVQ_ERR_SCRATCH = -8  /* kvq_paged_attention_nvfp4_noalloc: the call needs
-                           more scratch than the built-in array holds */
+                           more scratch than the built-in array holds;
+                           kvq_chunk_attention_nvfp4: the workspace is too
+                           small */
 } kvq_status;
 
 /* Size of the scratch array built into the library for
@@ -116,9 +125,13 @@ enum {
   KVQ_DEVERR_SEQ = 1 << 2,   /* position beyond max_blocks_per_seq * B, or an
                                 output row that no sequence covers, or
                                 cu_seq_lens[num_seqs] != total_tokens */
-  KVQ_DEVERR_TIMEOUT = 1 << 3 /* a bounded wait for an asynchronous copy
-                                 gave up; the affected rows were not
-                                 written */
+  KVQ_DEVERR_TIMEOUT = 1 << 3, /* a bounded wait for an asynchronous copy
+                                  gave up; the affected rows were not
+                                  written */
+  KVQ_DEVERR_REF = 1 << 4,   /* a page that other sequences share (or that
+                                nobody holds) would have been written, or a
+                                page that nobody holds was dropped */
+  KVQ_DEVERR_FULL = 1 << 5   /* not enough free pages */
 };
 
 /*
@@ -408,6 +421,259 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
     int32_t max_context_len, const float* k_scale, const float* v_scale,
     float scale, int32_t partition_size, void* out, int64_t out_stride0,
     uint32_t flags, int32_t* dev_error, void* stream);
+
+/*
+ * kvq_chunk_attention_nvfp4 -- causal attention of chunks of new tokens over
+ * the NVFP4 cache that kvq_store_nvfp4 writes, the new tokens' own K and V
+ * included (store them first).  The source material has no counterpart;
+ * this entry point is an addition of this library, the form of
+ * kvq_paged_attention_nvfp4 for any number of query tokens per sequence.
+ *
+ * Sequence b has the query rows cu_q_lens[b] .. cu_q_lens[b+1] - 1, n of
+ * them, and L = context_lens[b] tokens in the cache (the new ones are the
+ * last n of them).  Row r = cu_q_lens[b] + i is the token at position
+ * P = L - n + i and sees the tokens t = 0 .. P.  For query head h, reading
+ * KV head h / (num_q_heads / num_kv_heads), with K^ and V^ as for
+ * kvq_paged_attention_nvfp4:
+ *   s_t = scale * sum_d q[r, h, d] K^[t, d];
+ *   out[r, h, :] = sum_{t <= P} softmax(s)_t V^[t, :];
+ *   a row that sees no token (P < 0) gets zeros.
+ * A token that a row does not see cannot reach it, whatever its bytes (a
+ * group scale that is NaN makes NaN of the rows that see it, and of the
+ * columns of its group if it is a V scale).
+ * Arithmetic: as for kvq_paged_attention_nvfp4 (query rounded to fp16,
+ * e2m1 * sf exact in fp16, products accumulated in fp32 on the tensor
+ * cores, weights rounded to fp16 against a running reference, fp32 sums and
+ * merges, out rounded once), except that the denominator sums the weights
+ * before they are rounded.
+ *
+ * query          bf16 / fp16 (dtype) [total_q, num_q_heads, 128], rows
+ *                query_stride0 elements apart (multiple of 8), 16-byte
+ *                aligned; |q| < 65504 (fp16 range).  0 <= total_q <= 2^26.
+ * cu_q_lens      int32 [num_seqs + 1], cu_q_lens[0] >= 0, non-decreasing,
+ *                at most total_q (values that break this are clamped and
+ *                flagged KVQ_DEVERR_SEQ).  Rows that no sequence covers
+ *                (behind cu_q_lens[num_seqs]) are not read, and their
+ *                output is left as it was.
+ * max_q_len      the longest chunk of the batch, as known on the host.
+ *                Chooses the tile shape only: a wrong value costs time.
+ * head_size      128.   num_q_heads / num_kv_heads <= 16 (and divides),
+ *                num_q_heads <= 1024.
+ * key_cache, value_cache, page_stride, block_size, num_blocks, layout,
+ * block_table, block_table_stride, max_blocks_per_seq, k_scale, v_scale,
+ * scale          as for kvq_paged_attention_nvfp4.
+ * context_lens   int32 [num_seqs]; values above max_blocks_per_seq *
+ *                block_size (or 2^30) are clamped to it and flagged
+ *                (KVQ_DEVERR_SEQ), negative ones count as 0.
+ * workspace      workspace_bytes of device memory, 16-byte aligned; at
+ *                least kvq_chunk_attention_workspace_bytes() (the same for
+ *                every call on a device), else KVQ_ERR_SCRATCH.  Nothing in
+ *                it has to be initialised; its contents afterwards are
+ *                unspecified.  Calls that can overlap on the GPU (other
+ *                streams, graphs replayed side by side) each need their own.
+ * out            dtype [total_q, num_q_heads, 128], rows out_stride0
+ *                elements apart (multiple of 8), 16-byte aligned.
+ * flags          KVQ_F_SWIZZLE_K_SCALE, KVQ_F_PDL, or 0.
+ * dev_error      nullable (KVQ_DEVERR_BLOCK: the token is left out;
+ *                KVQ_DEVERR_SEQ; KVQ_DEVERR_TIMEOUT).
+ * total_q == 0 or num_seqs == 0 returns KVQ_OK without launching.
+ */
+kvq_status kvq_chunk_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    const float* k_scale, const float* v_scale, float scale, void* workspace,
+    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, void* stream);
+
+/* Workspace of a kvq_chunk_attention_nvfp4 call on the current device. */
+int64_t kvq_chunk_attention_workspace_bytes(void);
+
+/*
+ * The page pool: the state of a paged cache on the device, for callers that
+ * keep it there (a captured decoding loop allocates its pages without the
+ * host).  The source material has no counterpart; these entry points are
+ * additions of this library.  The state is the caller's memory:
+ *
+ *   ref_count    int32 [num_blocks], how many block-table entries hold the
+ *                page; 0 = free.  All zero to begin with.
+ *   block_table  int32 [num_rows, >= max_blocks_per_seq], rows
+ *                block_table_stride apart; entry j of a row is the page of
+ *                its tokens j * block_size ..; -1 = no page.  All -1 to
+ *                begin with.
+ *   seq_lens     int32 [num_rows], tokens of each row's sequence; 0 for an
+ *                empty row.
+ *
+ * The same table and lengths serve as the block_table and context_lens of
+ * the other calls.  One state may serve any number of caches of the same
+ * block_size (the layers of a model, an indexer cache beside the NVFP4
+ * one).  Pages are handed out lowest index first, in the order of the list,
+ * so that equal calls give equal states.  An entry of a list that cannot be
+ * carried out is refused as a whole: the state is left as if it were not in
+ * the list, and dev_error says why.  A list names a row at most once (fork:
+ * as a child); a row named more often is refused each time, with
+ * KVQ_DEVERR_SEQ -- but may be freed, which happens once.  Calls on one
+ * state must not overlap on the GPU.
+ * Limits: num_rows <= 2^18, lists of at most 4096 entries, block_size > 0,
+ * max_blocks_per_seq * block_size < 2^31 - block_size.
+ * flags: KVQ_F_PDL or 0.  A list of 0 entries returns KVQ_OK without
+ * launching.
+ */
+
+/*
+ * kvq_extend_sequences -- room for new tokens: row seq_ids[i] grows by
+ * m = cu_new[i+1] - cu_new[i] tokens, gets the pages that it needs, and
+ * slot_mapping[cu_new[i] + k] = page * block_size + offset of its k-th new
+ * token, as kvq_store_nvfp4 and kvq_store_indexer_k take it.  cu_new is
+ * also the cu_q_lens of kvq_chunk_attention_nvfp4.
+ *
+ * cu_new         int32 [num_seqs + 1], cu_new[0] == 0, non-decreasing, at
+ *                most total_new (else the whole call is refused,
+ *                KVQ_DEVERR_SEQ).
+ * slot_mapping   int64 [total_new]; -1 for the tokens of refused entries and
+ *                behind cu_new[num_seqs] (the stores skip those).
+ * Refused: a row outside [0, num_rows) or named twice, a length outside
+ * [0, max_blocks_per_seq * block_size] before or after (KVQ_DEVERR_SEQ); a
+ * partly filled last page that is not a page (KVQ_DEVERR_BLOCK) or not this
+ * row's alone (KVQ_DEVERR_REF); KVQ_DEVERR_FULL: entry i is served if the
+ * free pages cover what it and all entries before it need (entries that
+ * KVQ_DEVERR_FULL refuses still count, the others do not).
+ */
+kvq_status kvq_extend_sequences(
+    int32_t* ref_count, int64_t num_blocks, int32_t* block_table,
+    int64_t block_table_stride, int32_t num_rows, int32_t max_blocks_per_seq,
+    int32_t* seq_lens, int32_t block_size, const int32_t* seq_ids,
+    const int32_t* cu_new, int32_t num_seqs, int64_t* slot_mapping,
+    int64_t total_new, uint32_t flags, int32_t* dev_error, void* stream);
+
+/*
+ * kvq_fork_sequences -- row child_ids[i], an empty one, becomes a copy of
+ * row parent_ids[i]: it shares the parent's full pages (their counts grow)
+ * and gets a page of its own for a partly filled last one.  The bytes of
+ * that page are copied by kvq_copy_pages(..., copy_src, copy_dst, ...), once
+ * for the caches of each page size.  A parent may be named many times.
+ *
+ * copy_src, copy_dst  int32 [num_forks]: the parent's last page and the
+ *                child's, or -1 and -1 where nothing is to be copied.
+ * Refused: rows outside [0, num_rows), a child named twice or not empty
+ * (length 0 and no first page), a parent's length out of range
+ * (KVQ_DEVERR_SEQ); a parent's partly filled last page that is not a page
+ * (KVQ_DEVERR_BLOCK); KVQ_DEVERR_FULL as for kvq_extend_sequences.  A full
+ * page of the parent that is not a page becomes -1 in the child, flagged
+ * (KVQ_DEVERR_BLOCK).
+ */
+kvq_status kvq_fork_sequences(
+    int32_t* ref_count, int64_t num_blocks, int32_t* block_table,
+    int64_t block_table_stride, int32_t num_rows, int32_t max_blocks_per_seq,
+    int32_t* seq_lens, int32_t block_size, const int32_t* parent_ids,
+    const int32_t* child_ids, int32_t num_forks, int32_t* copy_src,
+    int32_t* copy_dst, uint32_t flags, int32_t* dev_error, void* stream);
+
+/*
+ * kvq_compact_sequences -- row seq_ids[i] keeps the tokens at the positions
+ * keep[cu_keep[i]] < keep[cu_keep[i] + 1] < ... and drops the others: the
+ * j-th kept token's place becomes position j, the length the number kept,
+ * and the pages behind it are dropped (freed where nobody else holds them).
+ * The bytes move by kvq_move_tokens_nvfp4(..., src_slots, dst_slots,
+ * cu_keep, ...), which must run before the dropped pages are handed out
+ * again.
+ *
+ * keep           int32 [total_keep]; cu_keep int32 [num_seqs + 1] as cu_new
+ *                above.
+ * src_slots, dst_slots  int64 [total_keep]: each kept token's place before
+ *                and after (equal where it stays), -1 for refused entries
+ *                and behind cu_keep[num_seqs].
+ * Refused: rows as above, positions that do not rise or lie outside the
+ * sequence (KVQ_DEVERR_SEQ), a kept token's page that is not a page
+ * (KVQ_DEVERR_BLOCK), a page that would receive a moved token and is not
+ * this row's alone (KVQ_DEVERR_REF; kept tokens may stay in, and move out
+ * of, shared pages).
+ */
+kvq_status kvq_compact_sequences(
+    int32_t* ref_count, int64_t num_blocks, int32_t* block_table,
+    int64_t block_table_stride, int32_t num_rows, int32_t max_blocks_per_seq,
+    int32_t* seq_lens, int32_t block_size, const int32_t* seq_ids,
+    const int32_t* keep, const int32_t* cu_keep, int32_t num_seqs,
+    int64_t* src_slots, int64_t* dst_slots, int64_t total_keep,
+    uint32_t flags, int32_t* dev_error, void* stream);
+
+/*
+ * kvq_free_sequences -- rows seq_ids[i] become empty: every page that they
+ * hold is dropped once per entry (free when nobody else holds it), the
+ * entries become -1 and the lengths 0.  A row outside [0, num_rows) is
+ * skipped (KVQ_DEVERR_SEQ); so is an entry that is not a page
+ * (KVQ_DEVERR_BLOCK, it becomes -1) and a count that is already 0
+ * (KVQ_DEVERR_REF, it stays 0).
+ */
+kvq_status kvq_free_sequences(int32_t* ref_count, int64_t num_blocks,
+                              int32_t* block_table,
+                              int64_t block_table_stride, int32_t num_rows,
+                              int32_t max_blocks_per_seq, int32_t* seq_lens,
+                              const int32_t* seq_ids, int32_t num_seqs,
+                              uint32_t flags, int32_t* dev_error,
+                              void* stream);
+
+/*
+ * kvq_copy_pages -- page dst_pages[i] := page src_pages[i], in each of the
+ * caches (any layout: the bytes are copied).
+ *
+ * caches         HOST array of num_caches device pointers, page 0 of each,
+ *                16-byte aligned; read during the call.
+ * page_bytes     bytes of a page, page_stride bytes from page to page;
+ *                multiples of 16, 0 < page_bytes <= page_stride.
+ * src_pages, dst_pages  int32 [num_pairs], device.  A pair with a negative
+ *                page, or with src == dst, copies nothing; a page >=
+ *                num_blocks skips the pair (KVQ_DEVERR_BLOCK).  A page that
+ *                is written must not occur in another pair; if it does,
+ *                the bytes of the pages written are unspecified.
+ * flags          KVQ_F_PDL or 0.
+ * num_caches == 0 or num_pairs == 0 returns KVQ_OK without launching.
+ */
+kvq_status kvq_copy_pages(uint8_t* const* caches, int32_t num_caches,
+                          int64_t page_stride, int64_t page_bytes,
+                          int64_t num_blocks, const int32_t* src_pages,
+                          const int32_t* dst_pages, int32_t num_pairs,
+                          uint32_t flags, int32_t* dev_error, void* stream);
+
+/*
+ * kvq_move_tokens_nvfp4 -- copy single tokens (the bytes of K and V data and
+ * scales of every head, exactly) from slot to slot in each of the NVFP4
+ * caches.  Bytes of other tokens are left as they are.
+ *
+ * caches         HOST array of num_caches device pointers, page 0 of the K
+ *                side of each, 16-byte aligned; read during the call.
+ * value_offset   bytes from a cache's K side to its V side (multiple of 16,
+ *                >= H*B*(D/2 + S)); page_stride, num_blocks, block_size,
+ *                layout, num_heads, head_size (<= 8192) as for
+ *                kvq_store_nvfp4.
+ * src_slots, dst_slots  int64 [total_moves], device, in num_lists lists:
+ *                list i is cu_moves[i] .. cu_moves[i+1] - 1 (a list out of
+ *                order or beyond total_moves is skipped, KVQ_DEVERR_SEQ).
+ *                A move with a negative slot, or with src == dst, does
+ *                nothing; one with a slot >= num_blocks * block_size is
+ *                skipped (KVQ_DEVERR_SLOT).  Within a list a slot that one
+ *                move has written must not be read by a later one (a slot
+ *                may be written after it was read); slots of different
+ *                lists that write them must be disjoint, and no slot may be
+ *                written twice.  Where this is broken the bytes of the slots
+ *                written are unspecified.  The lists of
+ *                kvq_compact_sequences satisfy it.
+ * flags          KVQ_F_SWIZZLE_K_SCALE, KVQ_F_PDL, or 0.
+ * num_caches, num_lists or total_moves == 0 returns KVQ_OK without
+ * launching.  One list is walked in order by one thread block per cache,
+ * head and side: long work comes as several lists or caches.
+ */
+kvq_status kvq_move_tokens_nvfp4(
+    uint8_t* const* caches, int32_t num_caches, int64_t value_offset,
+    int64_t page_stride, int64_t num_blocks, int32_t block_size,
+    int32_t layout, int32_t num_heads, int32_t head_size,
+    const int64_t* src_slots, const int64_t* dst_slots, int64_t total_moves,
+    const int32_t* cu_moves, int32_t num_lists, uint32_t flags,
+    int32_t* dev_error, void* stream);
 
 /* Static text for a status code. */
 const char* kvq_status_string(kvq_status status);

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libkvq.so")
 
 SOURCES = ["kvq_api.cu", "store_nvfp4.cu", "gather_indexer_k.cu",
            "load_nvfp4.cu", "store_indexer_k.cu", "attention_noalloc.cu",
-           "paged_attention_mma.cu"]
+           "paged_attention_mma.cu", "chunk_attention.cu", "page_pool.cu",
+           "page_move.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-Wall", f"-I{INCLUDE}", f"-I{CSRC}"]

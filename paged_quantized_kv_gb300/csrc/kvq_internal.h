@@ -162,6 +162,107 @@ kvq_status attention_check(
     float scale, int32_t partition_size, const void* out, int64_t out_stride0,
     uint32_t flags);
 
+// ---------------------------------------------------------------------------
+// Attention of a chunk of new tokens over the NVFP4 cache
+// ---------------------------------------------------------------------------
+struct ChunkParams {
+  const uint16_t* q;       // [total_q, Hq, D] bf16/fp16 bits
+  int64_t q_stride0;       // elements
+  const uint8_t* side[2];  // page 0 of the K side / V side
+  int64_t page_stride;
+  int64_t num_blocks;
+  int64_t scale_off;       // H * B * D/2: offset of a side's scale region
+  int64_t dhs, dts, shs, sts;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  const int32_t* cu;       // cu_q_lens [num_seqs + 1]
+  const int32_t* lens;     // context_lens [num_seqs]
+  const float* k_scale;    // device scalars
+  const float* v_scale;
+  float scale;             // softmax scale
+  uint8_t* workspace;
+  uint16_t* out;           // [total_q, Hq, D], rows out_stride0 apart
+  int64_t out_stride0;
+  int32_t* dev_error;      // nullable
+  int64_t total_q;
+  int32_t num_seqs, Hq, Hkv, G, B, b_shift;
+  int32_t max_q_len;
+  int32_t len_cap;         // max_blocks * B
+  bool swizzle_k;
+  bool f16;
+  bool pdl;
+};
+
+constexpr int kChunkMaxSeqs = 1 << 20;
+// longest context (positions and tile counts stay in 32 bits)
+constexpr int kChunkMaxContext = 1 << 30;
+
+cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t stream);
+// Workspace bytes of a call on a device of `sms` multiprocessors.
+int64_t chunk_workspace_bytes(int sms);
+
+// ---------------------------------------------------------------------------
+// Page pool: growing, forking, compacting and freeing sequences
+// ---------------------------------------------------------------------------
+struct PoolParams {
+  int32_t* ref;            // ref_count [num_blocks]
+  int64_t num_blocks;
+  int32_t* table;          // block_table rows, `stride` entries apart
+  int64_t stride;
+  int32_t* lens;           // seq_lens [rows]
+  int32_t rows, width, B;
+  int32_t n;               // entries of the list
+  const int32_t* ids;      // rows of the list (fork: parents)
+  const int32_t* ids2;     // fork: children
+  const int32_t* cu;       // extend: new tokens; compact: kept tokens
+  const int32_t* keep;     // compact
+  int64_t total;           // extend: slots; compact: kept tokens
+  int64_t* slots;          // extend: slot_mapping; compact: src_slots
+  int64_t* slots2;         // compact: dst_slots
+  int32_t *src, *dst;      // fork: pages to copy
+  int32_t* err;            // nullable
+  bool pdl;
+};
+constexpr int kPoolMaxList = 4096;
+constexpr int kPoolMaxRows = 1 << 18;
+
+cudaError_t launch_extend(const PoolParams& p, cudaStream_t stream);
+cudaError_t launch_fork(const PoolParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const PoolParams& p, cudaStream_t stream);
+cudaError_t launch_free(const PoolParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Moving pages and tokens
+// ---------------------------------------------------------------------------
+constexpr int kMaxCaches = 128;  // caches of one launch
+
+struct CopyParams {
+  uint8_t* caches[kMaxCaches];
+  int64_t page_stride, page_bytes, num_blocks;
+  const int32_t *src, *dst;
+  int32_t* err;
+  int32_t num_caches, num_pairs;
+  int32_t pieces;          // warps per (pair, cache)
+  bool pdl;
+};
+// Bytes a warp copies.
+int copy_piece_bytes(bool vec32);
+cudaError_t launch_copy_pages(const CopyParams& p, bool vec32,
+                              cudaStream_t stream);
+
+struct MoveParams {
+  uint8_t* caches[kMaxCaches];
+  int64_t value_offset, page_stride, num_slots, scale_off;
+  int64_t dhs, dts, shs, sts;
+  const int64_t *src, *dst;
+  const int32_t* cu;
+  int64_t total;
+  int32_t* err;
+  int32_t num_caches, num_lists, H, D, S, B;
+  bool swizzle_k, pdl;
+};
+cudaError_t launch_move_tokens(const MoveParams& p, cudaStream_t stream);
+
 // The partition merge of the attention (PDL launch).
 cudaError_t launch_attention_merge(const AttnParams& p, cudaStream_t stream);
 

@@ -22,6 +22,16 @@ one:
   k_scale, v_scale, key_out, value_out)`` -- the read side of the store.
 * ``kvq_store_indexer_k(k, kv_cache, slot_mapping)`` -- the write side of
   the indexer cache the gather reads.
+
+Additions of this library (no counterpart in the pages):
+
+* ``kvq_chunk_attention_nvfp4`` -- causal attention of chunks of new tokens
+  over the NVFP4 pages.
+* ``kvq_extend_sequences``, ``kvq_fork_sequences``,
+  ``kvq_compact_sequences``, ``kvq_free_sequences`` -- the state of a paged
+  cache (``alloc_page_pool``) on the device.
+* ``kvq_copy_pages``, ``kvq_move_tokens_nvfp4`` -- the bytes that go with
+  them.
 """
 from __future__ import annotations
 
@@ -57,6 +67,8 @@ KVQ_DEVERR_SLOT = 1
 KVQ_DEVERR_BLOCK = 2
 KVQ_DEVERR_SEQ = 4
 KVQ_DEVERR_TIMEOUT = 8
+KVQ_DEVERR_REF = 16
+KVQ_DEVERR_FULL = 32
 
 _lock = threading.Lock()
 _lib = None
@@ -111,6 +123,37 @@ def lib() -> ctypes.CDLL:
             c.c_int64, c.c_int32, P, c.c_int32, P, P, c.c_float, c.c_int32,
             P, c.c_int64, c.c_uint32, P, P]
         L.kvq_paged_attention_nvfp4_noalloc.restype = c.c_int
+        L.kvq_chunk_attention_nvfp4.argtypes = [
+            P, c.c_int64, c.c_int32, c.c_int64, c.c_int32, P, c.c_int32,
+            c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int64, c.c_int32,
+            c.c_int64, c.c_int32, P, c.c_int64, c.c_int32, P, P, P,
+            c.c_float, P, c.c_int64, P, c.c_int64, c.c_uint32, P, P]
+        L.kvq_chunk_attention_nvfp4.restype = c.c_int
+        L.kvq_chunk_attention_workspace_bytes.argtypes = []
+        L.kvq_chunk_attention_workspace_bytes.restype = c.c_int64
+        pool = [P, c.c_int64, P, c.c_int64, c.c_int32, c.c_int32, P]
+        L.kvq_extend_sequences.argtypes = pool + [
+            c.c_int32, P, P, c.c_int32, P, c.c_int64, c.c_uint32, P, P]
+        L.kvq_extend_sequences.restype = c.c_int
+        L.kvq_fork_sequences.argtypes = pool + [
+            c.c_int32, P, P, c.c_int32, P, P, c.c_uint32, P, P]
+        L.kvq_fork_sequences.restype = c.c_int
+        L.kvq_compact_sequences.argtypes = pool + [
+            c.c_int32, P, P, P, c.c_int32, P, P, c.c_int64, c.c_uint32, P,
+            P]
+        L.kvq_compact_sequences.restype = c.c_int
+        L.kvq_free_sequences.argtypes = pool + [
+            P, c.c_int32, c.c_uint32, P, P]
+        L.kvq_free_sequences.restype = c.c_int
+        L.kvq_copy_pages.argtypes = [
+            P, c.c_int32, c.c_int64, c.c_int64, c.c_int64, P, P, c.c_int32,
+            c.c_uint32, P, P]
+        L.kvq_copy_pages.restype = c.c_int
+        L.kvq_move_tokens_nvfp4.argtypes = [
+            P, c.c_int32, c.c_int64, c.c_int64, c.c_int64, c.c_int32,
+            c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int64, P, c.c_int32,
+            c.c_uint32, P, P]
+        L.kvq_move_tokens_nvfp4.restype = c.c_int
         L.kvq_status_string.argtypes = [c.c_int]
         L.kvq_status_string.restype = c.c_char_p
         L.kvq_version.argtypes = []
@@ -380,6 +423,350 @@ def kvq_paged_attention_nvfp4_noalloc(query: torch.Tensor,
         out.data_ptr(), out.stride(0), int(flags), _ptr(dev_error),
         _stream_of(query) if stream is None else stream)
     _check("kvq_paged_attention_nvfp4_noalloc", st)
+
+
+def _same_device(fn: str, *tensors) -> None:
+    """Every tensor given is on the current CUDA device (whose stream the
+    call runs on), else KVQ_ERR_ARG: a host or foreign pointer must not
+    reach a kernel."""
+    if any(t is not None and not t.is_cuda for t in tensors):
+        raise KvqError(fn, KVQ_ERR_ARG)
+    here = torch.cuda.current_device()
+    if any(t is not None and t.device.index != here for t in tensors):
+        raise KvqError(fn, KVQ_ERR_ARG)
+
+
+def _int32_vector(fn: str, *tensors) -> None:
+    for t in tensors:
+        if t.dtype != torch.int32:
+            raise KvqError(fn, KVQ_ERR_DTYPE)
+        if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+
+
+def _dev_error_ok(fn: str, t) -> None:
+    if t is not None and (t.dtype != torch.int32 or t.numel() < 1):
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+
+
+def _page_views(fn: str, key_cache, value_cache) -> int:
+    """Checks the store's 4-D page views; returns their layout."""
+    for t in (key_cache, value_cache):
+        if t.dtype != torch.uint8:
+            raise KvqError(fn, KVQ_ERR_DTYPE)
+        if t.dim() != 4 or t.stride(3) != 1:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+    n, B, H, full = key_cache.shape
+    if (tuple(value_cache.shape) != (n, B, H, full)
+            or value_cache.stride() != key_cache.stride()):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _, sb, sh, _ = key_cache.stride()
+    if sb == full and (sh == B * full or H == 1):
+        return KVQ_LAYOUT_HND  # (with one head both layouts are the same)
+    if sh == full and sb == H * full:
+        return KVQ_LAYOUT_NHD
+    raise KvqError(fn, KVQ_ERR_SHAPE)
+
+
+def chunk_attention_workspace(device="cuda") -> torch.Tensor:
+    """Workspace of kvq_chunk_attention_nvfp4 (the same for every call on a
+    device; calls that may overlap each need their own)."""
+    with torch.cuda.device(device):
+        n = lib().kvq_chunk_attention_workspace_bytes()
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
+                              value_cache: torch.Tensor,
+                              block_table: torch.Tensor,
+                              cu_q_lens: torch.Tensor,
+                              context_lens: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor,
+                              scale: float, out: torch.Tensor,
+                              max_q_len: int,
+                              workspace: torch.Tensor | None = None,
+                              flags: int = 0,
+                              dev_error: torch.Tensor | None = None,
+                              stream: int | None = None) -> None:
+    """Causal attention of chunks of new tokens over the NVFP4 cache (see
+    ``include/kvq.h``).
+
+    query / out: bf16 or fp16 [total_q, Hq, 128] (last two dims contiguous);
+    sequence b's new tokens are rows cu_q_lens[b] .. cu_q_lens[b+1] - 1 and
+    the last of its context_lens[b] cached tokens.  key_cache / value_cache:
+    the store's 4-D page views; block_table int32 [num_seqs, max_blocks];
+    cu_q_lens int32 [num_seqs + 1]; context_lens int32 [num_seqs];
+    max_q_len: the longest chunk.  The workspace
+    (``chunk_attention_workspace``) is allocated here when it is not
+    given."""
+    fn = "kvq_chunk_attention_nvfp4"
+    dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
+    if query.dtype not in dtypes or out.dtype != query.dtype:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if query.dim() != 3 or out.shape != query.shape:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    total, Hq, D = query.shape
+    if (query.stride(2) != 1 or query.stride(1) != D or out.stride(2) != 1
+            or out.stride(1) != D):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    layout = _page_views(fn, key_cache, value_cache)
+    _int32_vector(fn, cu_q_lens, context_lens)
+    n = context_lens.numel()
+    if block_table.dtype != torch.int32:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if (cu_q_lens.numel() != n + 1 or block_table.dim() != 2
+            or block_table.size(0) < n
+            or (block_table.numel() > 1 and block_table.size(1) > 1
+                and block_table.stride(1) != 1)
+            or key_cache.size(3) != D // 2 + D // 16):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    _dev_error_ok(fn, dev_error)
+    _same_device(fn, query, out, key_cache, value_cache, block_table,
+                 cu_q_lens, context_lens, k_scale, v_scale, workspace,
+                 dev_error)
+    if workspace is None:
+        workspace = chunk_attention_workspace(query.device)
+    if not workspace.is_contiguous():
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    st = lib().kvq_chunk_attention_nvfp4(
+        query.data_ptr(), query.stride(0) if total > 1 else Hq * D,
+        dtypes[query.dtype], total, n, cu_q_lens.data_ptr(), int(max_q_len),
+        Hq, key_cache.size(2), D, key_cache.data_ptr(),
+        value_cache.data_ptr(), key_cache.stride(0), key_cache.size(1),
+        key_cache.size(0), layout, block_table.data_ptr(),
+        block_table.stride(0) if n > 1 else block_table.size(1),
+        block_table.size(1), context_lens.data_ptr(), k_scale.data_ptr(),
+        v_scale.data_ptr(), float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.data_ptr(), out.stride(0) if total > 1 else Hq * D, int(flags),
+        _ptr(dev_error), _stream_of(query) if stream is None else stream)
+    _check(fn, st)
+
+
+def alloc_page_pool(num_blocks: int, num_rows: int, max_blocks_per_seq: int,
+                    device="cuda"):
+    """An empty page pool: (ref_count, block_table, seq_lens)."""
+    return (torch.zeros(num_blocks, dtype=torch.int32, device=device),
+            torch.full((num_rows, max_blocks_per_seq), -1,
+                       dtype=torch.int32, device=device),
+            torch.zeros(num_rows, dtype=torch.int32, device=device))
+
+
+def _pool_args(fn: str, ref_count, block_table, seq_lens, dev_error,
+               *others):
+    """The state's checks, and its leading C arguments."""
+    _int32_vector(fn, ref_count, seq_lens)
+    if block_table.dtype != torch.int32:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if (block_table.dim() != 2 or block_table.size(0) != seq_lens.numel()
+            or (block_table.numel() > 1 and block_table.size(1) > 1
+                and block_table.stride(1) != 1)):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    # rows that overlap (an expanded table) would be written by several
+    if (block_table.size(0) > 1 and block_table.size(1) > 0
+            and block_table.stride(0) < block_table.size(1)):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _dev_error_ok(fn, dev_error)
+    _same_device(fn, ref_count, block_table, seq_lens, dev_error, *others)
+    rows, width = block_table.shape
+    return (ref_count.data_ptr(), ref_count.numel(), block_table.data_ptr(),
+            block_table.stride(0) if rows > 1 else width, rows, width,
+            seq_lens.data_ptr())
+
+
+def _int64_vector(fn: str, *tensors) -> None:
+    for t in tensors:
+        if t.dtype != torch.int64:
+            raise KvqError(fn, KVQ_ERR_DTYPE)
+        if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+
+
+def kvq_extend_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, seq_ids: torch.Tensor,
+                         cu_new: torch.Tensor, slot_mapping: torch.Tensor,
+                         block_size: int, flags: int = 0,
+                         dev_error: torch.Tensor | None = None,
+                         stream: int | None = None) -> None:
+    """Pages and slots for cu_new[i+1] - cu_new[i] new tokens of each row
+    seq_ids[i] (see ``include/kvq.h``).  ref_count, block_table, seq_lens:
+    ``alloc_page_pool``; seq_ids int32 [n]; cu_new int32 [n + 1];
+    slot_mapping int64 [total], written whole."""
+    fn = "kvq_extend_sequences"
+    _int32_vector(fn, seq_ids, cu_new)
+    _int64_vector(fn, slot_mapping)
+    n = seq_ids.numel()
+    if cu_new.numel() != n + 1:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                       seq_ids, cu_new, slot_mapping)
+    st = lib().kvq_extend_sequences(
+        *state, int(block_size), seq_ids.data_ptr(), cu_new.data_ptr(), n,
+        slot_mapping.data_ptr(), slot_mapping.numel(), int(flags),
+        _ptr(dev_error), _stream_of(ref_count) if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_fork_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
+                       seq_lens: torch.Tensor, parent_ids: torch.Tensor,
+                       child_ids: torch.Tensor, copy_src: torch.Tensor,
+                       copy_dst: torch.Tensor, block_size: int,
+                       flags: int = 0, dev_error: torch.Tensor | None = None,
+                       stream: int | None = None) -> None:
+    """Empty rows child_ids[i] become copies of rows parent_ids[i] (see
+    ``include/kvq.h``); ``kvq_copy_pages(caches, copy_src, copy_dst)`` then
+    copies the partly filled last pages.  All four lists int32 [n]."""
+    fn = "kvq_fork_sequences"
+    _int32_vector(fn, parent_ids, child_ids, copy_src, copy_dst)
+    n = parent_ids.numel()
+    if any(t.numel() != n for t in (child_ids, copy_src, copy_dst)):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                       parent_ids, child_ids, copy_src, copy_dst)
+    st = lib().kvq_fork_sequences(
+        *state, int(block_size), parent_ids.data_ptr(),
+        child_ids.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
+        int(flags), _ptr(dev_error),
+        _stream_of(ref_count) if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_compact_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
+                          seq_lens: torch.Tensor, seq_ids: torch.Tensor,
+                          keep: torch.Tensor, cu_keep: torch.Tensor,
+                          src_slots: torch.Tensor, dst_slots: torch.Tensor,
+                          block_size: int, flags: int = 0,
+                          dev_error: torch.Tensor | None = None,
+                          stream: int | None = None) -> None:
+    """Rows seq_ids[i] keep the tokens at the rising positions
+    keep[cu_keep[i] : cu_keep[i+1]] (see ``include/kvq.h``);
+    ``kvq_move_tokens_nvfp4(caches, src_slots, dst_slots, cu_keep)`` then
+    moves their bytes.  keep int32 [total]; src_slots, dst_slots int64
+    [total], written whole."""
+    fn = "kvq_compact_sequences"
+    _int32_vector(fn, seq_ids, keep, cu_keep)
+    _int64_vector(fn, src_slots, dst_slots)
+    n = seq_ids.numel()
+    if (cu_keep.numel() != n + 1 or src_slots.numel() != keep.numel()
+            or dst_slots.numel() != keep.numel()):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                       seq_ids, keep, cu_keep, src_slots, dst_slots)
+    st = lib().kvq_compact_sequences(
+        *state, int(block_size), seq_ids.data_ptr(), keep.data_ptr(),
+        cu_keep.data_ptr(), n, src_slots.data_ptr(), dst_slots.data_ptr(),
+        keep.numel(), int(flags), _ptr(dev_error),
+        _stream_of(ref_count) if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_free_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
+                       seq_lens: torch.Tensor, seq_ids: torch.Tensor,
+                       flags: int = 0, dev_error: torch.Tensor | None = None,
+                       stream: int | None = None) -> None:
+    """Rows seq_ids[i] become empty, their pages are dropped (see
+    ``include/kvq.h``)."""
+    fn = "kvq_free_sequences"
+    _int32_vector(fn, seq_ids)
+    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                       seq_ids)
+    st = lib().kvq_free_sequences(
+        *state, seq_ids.data_ptr(), seq_ids.numel(), int(flags),
+        _ptr(dev_error), _stream_of(ref_count) if stream is None else stream)
+    _check(fn, st)
+
+
+def _cache_list(fn: str, caches, dims: int):
+    """(tensors' common shape and strides of one cache, a C array of their
+    addresses, how many, a tensor): caches is a list of uint8 tensors
+    [num_blocks, ...] of one shape, or one tensor with the caches stacked in
+    front."""
+    if isinstance(caches, torch.Tensor):
+        if caches.dtype != torch.uint8:
+            raise KvqError(fn, KVQ_ERR_DTYPE)
+        if caches.dim() < dims + 1 or caches.size(0) == 0:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+        n, first = caches.size(0), caches[0]
+        if n > 1 and caches.stride(0) < first.size(0) * first.stride(0):
+            raise KvqError(fn, KVQ_ERR_SHAPE)  # caches would overlap
+        base, step = caches.data_ptr(), caches.stride(0)
+        ptrs = [base + k * step for k in range(n)]
+        tensors = [caches]
+    else:
+        tensors = list(caches)
+        if not tensors:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+        first = tensors[0]
+        for t in tensors:
+            if t.dtype != torch.uint8:
+                raise KvqError(fn, KVQ_ERR_DTYPE)
+            if t.shape != first.shape or t.stride() != first.stride():
+                raise KvqError(fn, KVQ_ERR_SHAPE)
+        if first.dim() < dims:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+        ptrs = [t.data_ptr() for t in tensors]
+    if first.size(0) > 0 and not first[0].is_contiguous():
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    return first, (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), tensors
+
+
+def kvq_copy_pages(caches, src_pages: torch.Tensor, dst_pages: torch.Tensor,
+                   flags: int = 0, dev_error: torch.Tensor | None = None,
+                   stream: int | None = None) -> None:
+    """Page dst_pages[i] := page src_pages[i] in every cache (see
+    ``include/kvq.h``).  caches: a list of uint8 tensors [num_blocks, ...] of
+    one shape, each page contiguous, or one tensor [n, num_blocks, ...];
+    src_pages, dst_pages int32 [pairs], negative = skip."""
+    fn = "kvq_copy_pages"
+    first, ptrs, n, tensors = _cache_list(fn, caches, 2)
+    _int32_vector(fn, src_pages, dst_pages)
+    if src_pages.numel() != dst_pages.numel():
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _dev_error_ok(fn, dev_error)
+    _same_device(fn, *tensors, src_pages, dst_pages, dev_error)
+    if first.size(0) == 0:
+        return
+    st = lib().kvq_copy_pages(
+        ptrs, n, first.stride(0), first[0].numel(), first.size(0),
+        src_pages.data_ptr(), dst_pages.data_ptr(), src_pages.numel(),
+        int(flags), _ptr(dev_error),
+        _stream_of(src_pages) if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_move_tokens_nvfp4(kv_caches, src_slots: torch.Tensor,
+                          dst_slots: torch.Tensor, cu_moves: torch.Tensor,
+                          layout: int = KVQ_LAYOUT_HND, flags: int = 0,
+                          dev_error: torch.Tensor | None = None,
+                          stream: int | None = None) -> None:
+    """Tokens from slot to slot in every NVFP4 cache (see
+    ``include/kvq.h``).  kv_caches: a list of ``alloc_nvfp4_cache``'s raw
+    tensors [num_blocks, 2, H, B, D/2 + D/16] (HND; NHD has B before H), or
+    one such tensor with the caches stacked in front; src_slots, dst_slots
+    int64 [moves], negative = skip; cu_moves int32 [lists + 1]."""
+    fn = "kvq_move_tokens_nvfp4"
+    first, ptrs, n, tensors = _cache_list(fn, kv_caches, 5)
+    if first.dim() != 5 or first.size(1) != 2 or first.size(4) % 9 != 0:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    if layout not in (KVQ_LAYOUT_HND, KVQ_LAYOUT_NHD):
+        raise KvqError(fn, KVQ_ERR_LAYOUT)
+    H, B = first.size(2), first.size(3)
+    if layout == KVQ_LAYOUT_NHD:
+        H, B = B, H
+    _int64_vector(fn, src_slots, dst_slots)
+    _int32_vector(fn, cu_moves)
+    if src_slots.numel() != dst_slots.numel() or cu_moves.numel() < 1:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _dev_error_ok(fn, dev_error)
+    _same_device(fn, *tensors, src_slots, dst_slots, cu_moves, dev_error)
+    st = lib().kvq_move_tokens_nvfp4(
+        ptrs, n, first.stride(1), first.stride(0), first.size(0), B,
+        int(layout), H, first.size(4) // 9 * 16, src_slots.data_ptr(),
+        dst_slots.data_ptr(), src_slots.numel(), cu_moves.data_ptr(),
+        cu_moves.numel() - 1, int(flags), _ptr(dev_error),
+        _stream_of(src_slots) if stream is None else stream)
+    _check(fn, st)
 
 
 def alloc_nvfp4_cache(num_blocks: int, block_size: int, num_heads: int,
