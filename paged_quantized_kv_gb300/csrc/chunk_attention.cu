@@ -26,14 +26,14 @@ constexpr float kLag = 8.0f;               // see the softmax
 // ---------------------------------------------------------------------------
 // Shared-memory matrix descriptors of a tile whose rows are 128 bytes (64
 // fp16) with their 16-byte chunks XOR-swizzled by the row's low three bits
-// (the hardware's 128-byte swizzle): `lbo` from one 64-element half to the
-// next (used by the MN-major operand), 1024 bytes from one group of 8 rows
-// to the next.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) |
-         (static_cast<uint64_t>(lbo >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (uint64_t{1} << 46) |
-         (uint64_t{2} << 61);
+// (the hardware's 128-byte swizzle): `kLbo` bytes from one 64-element half to
+// the next (used by the MN-major operand), 1024 bytes from one group of 8
+// rows to the next.  The low word holds the address and kLbo, the high word
+// is a constant.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+template <uint32_t kLbo>
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFu) | ((kLbo >> 4) << 16);
 }
 
 // kind::f16, fp16 operands, fp32 accumulator, M = N = 128.
@@ -41,23 +41,30 @@ constexpr uint32_t kIdesc =
     (1u << 4) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
 constexpr uint32_t kIdescBmn = kIdesc | (1u << 16);  // B is MN-major
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b,
+// D[tmem] (+)= A[smem] B[smem]; a, b: low descriptor words.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b,
                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{ .reg .pred p;\n"
+      "  .reg .b64 da, db;\n"
       "  setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      "  mov.b64 da, {%1, %5};\n"
+      "  mov.b64 db, {%2, %5};\n"
+      "  tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b,
+// D[tmem] (+)= A[tmem] B[smem].
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b,
                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{ .reg .pred p;\n"
+      "  .reg .b64 db;\n"
       "  setp.ne.b32 p, %4, 0;\n"
-      "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "  mov.b64 db, {%2, %5};\n"
+      "  tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p; }" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 
@@ -102,6 +109,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
       "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
       "%29, %30, %31};" ::KVQ_I8(r, 0),
       KVQ_I8(r, 8), KVQ_I8(r, 16), KVQ_I8(r, 24), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];"
+      : KVQ_R8(r, 0), KVQ_R8(r, 8)
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15};" ::KVQ_I8(r, 0),
+      KVQ_I8(r, 8), "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -163,12 +186,46 @@ __device__ __forceinline__ uint4 ldg128(const void* p) {
                : "l"(p));
   return v;
 }
-__device__ __forceinline__ uint2 ldg64(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];"
-               : "=r"(v.x), "=r"(v.y)
-               : "l"(p));
-  return v;
+// One lane of the (converged) warp: the same one every time.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p;\n"
+      "  elect.sync _|p, 0xFFFFFFFF;\n"
+      "  selp.u32 %0, 1, 0, p; }"
+      : "=r"(r));
+  return r != 0;
+}
+
+// A value that every lane holds, told to the compiler as such.
+__device__ __forceinline__ int uniform(int x) {
+  return __shfl_sync(0xFFFFFFFFu, x, 0);
+}
+
+// Two fp32 at once: a * b + c, a + b.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b,
+                                         uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -309,6 +366,12 @@ struct Walk {
   }
 };
 
+// CTAs that get a share of U units.
+__device__ __forceinline__ int ctas_of(int64_t U) {
+  return static_cast<int>(
+      min(static_cast<int64_t>(gridDim.x), max(U, int64_t{1})));
+}
+
 // What the merge kernel needs of an item that begins in a CTA's share and
 // goes on in the next ones': partial results in this CTA's slot `slot` and
 // in slot 0 of the `more` CTAs behind it.
@@ -330,6 +393,7 @@ __device__ __forceinline__ float* slot_of(const ChunkParams& p, int cta,
 // Shared memory
 // ---------------------------------------------------------------------------
 constexpr int kStages = 2;
+constexpr int kWalkBytes = 80;
 
 template <int kTiles>
 struct Smem {
@@ -338,19 +402,31 @@ struct Smem {
   static constexpr int kV = kK + kStages * kTile;           // kStages tiles
   static constexpr int kBar = kV + kStages * kTile;
   static constexpr int kBars = 4 * kStages + 4 * kTiles;
-  static constexpr int kValid = kBar + 8 * 18;  // [4][4] words
-  static constexpr int kNan = kValid + 64;      // [4][8][4] ints
-  static constexpr int kMisc = kNan + 512;      // 16 ints
-  static constexpr int kScan = kMisc + 64;      // 32 int64
-  static constexpr int kBytes = kScan + 256 + 1024;  // 1024: alignment
+  // Per tile and quarter: the tokens that are not left out.  A filler is at
+  // most a few tiles ahead of the softmax: K of tile k + 3 waits for the
+  // products of tile k + 1, which wait for the weights of tile k.
+  static constexpr int kValid = kBar + 8 * 18;  // [8][4] words
+  // Per segment, group and quarter: the first token whose V scale is NaN.
+  // V of tile k waits for the products of tile k - 2, so when segment s is
+  // filled the epilogues of the segments up to s - 3 are over.
+  static constexpr int kNan = kValid + 128;     // [8][8][4] ints
+  static constexpr int kMisc = kNan + 1024;     // 16 ints
+  static constexpr int kScan = kMisc + 64;      // 36 int64
+  // The softmax warps' positions, kept out of their registers.
+  static constexpr int kWalk = kScan + 288;
+  static constexpr int kBytes =
+      kWalk + 4 * kTiles * kWalkBytes + 1024;   // 1024: alignment
   static_assert(kBars < 18 && kValid % 16 == 0, "");
 };
 
 // Roles of the warps: kTiles softmax warpgroups (one query tile each, one
-// row per thread), one dequantising warpgroup (one token per thread), one
-// warpgroup of which one thread issues the products.
+// row per thread), then one warp that issues the products and seven that
+// dequantise (one token's K or V row per thread).  An SM quarter holds the
+// registers of four warps of 128, so a 17th warp would cost every warp a
+// quarter of its registers.
 template <int kTiles>
 constexpr int kThreadsOf = 128 * (kTiles + 2);
+constexpr int kFillers = 7;
 
 template <int kTiles, bool kF16>
 __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
@@ -403,7 +479,7 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
     misc[2] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (tid < 128) nan_at[tid] = INT32_MAX;
+  if (tid < 256) nan_at[tid] = INT32_MAX;
   if (tid == 0)  // nothing to join, unless the end of this CTA says so
     (reinterpret_cast<Cut*>(p.workspace) + blockIdx.x)->more = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -444,9 +520,7 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
   };
   for (int r = 0; r < rounds; ++r) scan_round(r, true);
   const int64_t U = total;
-  const int ctas = static_cast<int>(
-      min(static_cast<int64_t>(gridDim.x), max(U, int64_t{1})));
-  const int cta = blockIdx.x;
+  const int cta = blockIdx.x, ctas = ctas_of(U);
   const int64_t u0 = cta < ctas ? U * cta / ctas : U;
   const int64_t u1 = cta < ctas ? U * (cta + 1) / ctas : U;
   if (rounds > 1) total = 0;
@@ -467,75 +541,92 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
       misc[5] = static_cast<int>(rem % w);
     }
   }
+  if (tid == 0) {
+    scan[32] = U;
+    scan[33] = u0;
+    scan[34] = u1;
+  }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+  volatile int64_t* kept_units = scan + 32;  // U, u0, u1
   Walk<kRows> walk;
   walk.b = misc[2];
   walk.block = misc[3];
   walk.h = misc[4];
   walk.kv0 = misc[5];
-  walk.left = u1 - u0;
+  walk.left = kept_units[2] - kept_units[1];
   const bool any = walk.b >= 0;
   if (any) walk.load(p);
-
-  const float c0 = p.scale * __ldg(p.k_scale);
 
   if (wg < kTiles) {
     // --- softmax: tile m, one row per thread --------------------------------
     if constexpr (kTiles == 2)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
     const int m = wg, row = tid & 127;
+    const float c0 = p.scale * __ldg(p.k_scale);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lanes + 128 * m;
     const uint32_t o_col = tmem + lanes + 128 * kTiles + 128 * m;
     // (c0 == 0: a query of zeros, and any c > 0)
     const float c = c0 != 0.0f ? fabsf(c0) * kLog2e : 1.0f;
-    const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
-    const float v_scale = __ldg(p.v_scale);
-    Cut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
-    uint32_t cnt = 0;    // tiles of this warpgroup so far
-    uint32_t tiles = 0;  // tiles of the CTA so far
-    int seg = 0;
-    int64_t u = u0;
+    // A tile's logits take 128 registers.  The warp's position waits in
+    // shared memory meanwhile.
+    struct Kept {
+      Walk<kRows> walk;
+      int seg;
+    };
+    static_assert(sizeof(Kept) <= kWalkBytes, "");
+    Kept* kept = reinterpret_cast<Kept*>(smem + L::kWalk + warp * kWalkBytes);
+    if (lane == 0) *kept = {walk, 0};
+    __syncwarp();
+    uint32_t cnt = 0;  // tiles of this warpgroup so far
     bool go = any;
     while (go) {
-      const int n_rows = walk.rows - 128 * m;  // rows of this tile
-      if (n_rows > 0) {
-        const int r = walk.row0 + 128 * m + row;   // row of the sequence
+      int kv0, kv1, pos, tiles, rows;
+      {
+        const Walk<kRows> w = kept->walk;
+        kv0 = w.kv0;
+        kv1 = w.kv1;
+        rows = w.rows - 128 * m;  // rows of this tile
+        // (tile kt of this segment is the CTA's (tiles + kt)-th)
+        tiles = static_cast<int>(kept_units[2] - kept_units[1] - w.left) - kv0;
+        const int r = w.row0 + 128 * m + row;  // row of the sequence
         const int tok = r / p.G;
-        const bool live = row < n_rows;
-        const int64_t q_row = walk.s.q0 + tok;
-        const int head = walk.h * p.G + (r - tok * p.G);
-        const int pos = live ? walk.s.L - walk.s.n + tok : -1;
-        // the query row, rounded to fp16, its sign folded with the scale's
-        {
-          const uint16_t* src = p.q + q_row * p.q_stride0 + head * kD;
+        const bool live = row < rows;
+        pos = live ? w.s.L - w.s.n + tok : -1;
+        if (rows > 0) {
+          // the query row, rounded to fp16, its sign folded with the scale's
+          const uint16_t* src = p.q + (w.s.q0 + tok) * p.q_stride0 +
+                                (w.h * p.G + (r - tok * p.G)) * kD;
           const uint32_t dst = base + L::kQ + m * kTile + row * 128;
+          const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
             uint4 v = make_uint4(0, 0, 0, 0);
             if (live && c0 != 0.0f) v = ldg128(src + 8 * g);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              w[k] = (kF16 ? w[k] : bf16x2_to_f16x2(w[k])) ^ flip;
-            sts128(dst + (g >> 3) * kHalf + (((g & 7) ^ (row & 7)) << 4), w);
+              x[k] = (kF16 ? x[k] : bf16x2_to_f16x2(x[k])) ^ flip;
+            sts128(dst + (g >> 3) * kHalf + (((g & 7) ^ (row & 7)) << 4), x);
           }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(q_full(m));
         }
+      }
+      if (rows > 0) {
         float ref = -INFINITY, sum = 0.0f;
-        for (int kt = walk.kv0; kt < walk.kv1; ++kt) {
+        for (int kt = kv0; kt < kv1; ++kt) {
           if (!warp_wait(s_full(m), cnt & 1, abort)) goto done;
           fence_after();
           uint32_t s[128];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32(s_col + 32 * k, s + 32 * k);
           const uint32_t* valid = reinterpret_cast<const uint32_t*>(
-              smem + L::kValid + ((tiles + kt - walk.kv0) & 3) * 16);
+              smem + L::kValid + ((tiles + kt) & 7) * 16);
           const uint32_t v0 = valid[0], v1 = valid[1], v2 = valid[2],
                          v3 = valid[3];
           tmem_wait_ld();
@@ -550,8 +641,10 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int k = 0; k < 128; ++k)
-            mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(s[k]));
+          for (int k = 0; k < 128; k += 2)
+            mx[(k >> 1) & 3] =
+                max3(mx[(k >> 1) & 3], __uint_as_float(s[k]),
+                     __uint_as_float(s[k + 1]));
           const float top =
               fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
           // The reference follows the maximum only when it lags by more
@@ -563,32 +656,37 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
               ref = top;
               sum *= f;
             }
-            if (kt > walk.kv0) {
+            if (kt > kv0) {
               if (!warp_wait(o_done(m), (cnt - 1) & 1, abort)) goto done;
               fence_after();
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                uint32_t o[32];
-                tmem_ld32(o_col + 32 * k, o);
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                uint32_t o[16];
+                tmem_ld16(o_col + 16 * k, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 16; ++j)
                   o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st32(o_col + 32 * k, o);
+                tmem_st16(o_col + 16 * k, o);
               }
             }
           }
           const float low = ref == -INFINITY ? 0.0f : ref;
-          float add[4] = {0, 0, 0, 0};
+          const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
+          uint64_t add[2] = {0, 0};
 #pragma unroll
           for (int k = 0; k < 128; k += 2) {
-            const float a = ex2(fmaf(__uint_as_float(s[k]), c, -low));
-            const float b = ex2(fmaf(__uint_as_float(s[k + 1]), c, -low));
-            add[k & 3] += a;
-            add[(k & 3) + 1] += b;
+            float a, b;
+            unpack2(fma2(pack2(__uint_as_float(s[k]),
+                               __uint_as_float(s[k + 1])), cc, ll), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            add[(k >> 1) & 1] = add2(add[(k >> 1) & 1], pack2(a, b));
             s[k >> 1] = pack_f16x2(a, b);
           }
-          sum += (add[0] + add[1]) + (add[2] + add[3]);
+          float e, o;
+          unpack2(add2(add[0], add[1]), e, o);
+          sum += e + o;
           tmem_st32(s_col, s);
           tmem_st32(s_col + 32, s + 32);
           tmem_wait_st();
@@ -600,13 +698,18 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
         // --- epilogue -------------------------------------------------------
         if (!warp_wait(o_done(m), (cnt - 1) & 1, abort)) goto done;
         fence_after();
+        const Walk<kRows> w = kept->walk;
+        const int seg = kept->seg;
         const int4* nan_row =
-            reinterpret_cast<const int4*>(nan_at + (seg & 3) * 32);
-        const bool whole = walk.kv0 == 0 && walk.kv1 == walk.W;
-        const float inv =
-            sum > 0.0f ? v_scale / sum : (sum == 0.0f ? 0.0f : sum);
-        float* slot = slot_of(p, cta, seg > 0);
-        uint16_t* dst = p.out + q_row * p.out_stride0 + head * kD;
+            reinterpret_cast<const int4*>(nan_at + (seg & 7) * 32);
+        const bool live = row < rows;
+        const bool whole = kv0 == 0 && kv1 == w.W;
+        const float inv = sum > 0.0f ? __ldg(p.v_scale) / sum
+                                     : (sum == 0.0f ? 0.0f : sum);
+        float* slot = slot_of(p, blockIdx.x, seg > 0);
+        const int r = w.row0 + 128 * m + row, tok = r / p.G;
+        uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
+                        (w.h * p.G + (r - tok * p.G)) * kD;
         float* part = slot + (128 * m + row) * kD;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -650,95 +753,111 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
         }
         fence_before();
       }
-      u += walk.kv1 - walk.kv0;
-      tiles += walk.kv1 - walk.kv0;
-      if (walk.kv0 == 0 && walk.kv1 < walk.W) {
+      Walk<kRows> w = kept->walk;
+      const int seg = kept->seg;
+      if (tid == 0 && kv0 == 0 && kv1 < w.W) {
         // goes on in the next CTAs' shares
-        const int64_t end = u + (walk.W - walk.kv1);
+        const int64_t all = kept_units[0];
+        const int64_t end = kept_units[2] - w.left + w.W;
+        const int cta = blockIdx.x, ctas = ctas_of(all);
         int more = 1;
-        while (cta + more + 1 < ctas && U * (cta + more + 1) / ctas < end)
+        while (cta + more + 1 < ctas && all * (cta + more + 1) / ctas < end)
           ++more;
-        cut = {walk.b, walk.block, walk.h, seg > 0, more, {0, 0, 0}};
+        *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
+            w.b, w.block, w.h, seg > 0, more, {0, 0, 0}};
       }
-      ++seg;
-      go = walk.next(p);
+      go = w.next(p);
+      __syncwarp();
+      if (lane == 0) *kept = {w, seg + 1};
+      __syncwarp();
     }
-    if (tid == 0)
-      *(reinterpret_cast<Cut*>(p.workspace) + cta) = cut;
-  } else if (wg == kTiles) {
-    // --- dequantise: one token of a tile per thread --------------------------
+  } else {
     if constexpr (kTiles == 2)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    const int t = tid & 127;
-    const uint32_t row_at = t * 128, sw = t & 7;
-    // the tile ahead: coordinates, then raw bytes
+  }
+  if (wg >= kTiles && warp != 4 * kTiles) {
+    // --- dequantise: a quarter (32 tokens) of a tile's K or V at a time ------
+    // The quarters K 0..3, V 0..3 of the share's tiles, in order, are dealt
+    // round-robin to the warps.  A warp has three in hand: the one whose raw
+    // bytes are in registers, the next one, whose page is known, and the one
+    // behind it, whose block id is on its way (`job`, `kt` and `walk` are at
+    // that one).
+    int job = warp - 4 * kTiles - 1;  // 0..3: K quarters, 4..7: V quarters
     int kt = walk.kv0, seg = 0;
-    bool have = any;
-    uint4 kd[4], vd[4];
-    uint2 ksc, vsc;
-    bool k_ok = false, v_ok = false;  // token to be read
-    uint32_t mask = 0;                // ballot: not to be left out
-    const uint8_t *k_page = nullptr, *v_page = nullptr;
-    int off = 0;
-    // page of this thread's token of tile (walk, kt)
-    auto locate = [&]() {
-      const int pos = kt * kKeys + t;
-      const bool in = pos < walk.s.L;
-      const bool quad = (pos & ~3) < walk.s.L;  // (a quad is in one page)
-      bool bad = false;
-      k_ok = false;
+    uint32_t cnt = 0;      // tile of the share
+    bool more = any;       // there is a tile at (walk, kt)
+    int32_t blk = -1;      // the block id of this thread's token
+    int pos = 0, off = 0;  // the token, and its place in the page
+    bool quad = false;     // its 4-token band is inside the context
+    auto look_up = [&]() {
+      pos = kt * kKeys + 32 * (job & 3) + lane;
+      quad = more && (pos & ~3) < walk.s.L;  // (a band is in one page)
       if (quad) {
         const int j = p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B;
         off = pos - j * p.B;
-        const int32_t blk = __ldg(p.block_table + walk.b * p.bt_stride + j);
+        blk = __ldg(p.block_table + walk.b * p.bt_stride + j);
+      }
+    };
+    // The next job.  Tokens that are not to be read load the query's first
+    // bytes instead, and scale them by 0: loads without a branch need no
+    // moves at the end of the loop, where they would wait for the data.
+    const uint8_t *data = nullptr, *scales = nullptr;
+    bool next_some = false, next_first = false, next_in = false;
+    int next_pos = 0, next_job = 0;
+    uint32_t next_mask = 0, next_cnt = 0, next_seg = 0;
+    auto step = [&]() {
+      bool bad = false;
+      data = scales = reinterpret_cast<const uint8_t*>(p.q);
+      next_in = false;
+      next_some = more;
+      next_pos = pos;
+      next_job = job;
+      next_cnt = cnt;
+      next_seg = seg;
+      next_first = kt == walk.kv0;
+      const bool v = job >= 4;
+      if (quad) {
         bad = blk < 0 || blk >= p.num_blocks;
+        const bool in = pos < walk.s.L;
         if (!bad) {
-          k_ok = true;
-          k_page = p.side[0] + blk * p.page_stride;
-          v_page = p.side[1] + blk * p.page_stride;
-        } else if (in) {
+          const uint8_t* page =
+              (v ? p.side[1] : p.side[0]) + blk * p.page_stride;
+          data = page + walk.h * p.dhs + off * p.dts;
+          // swizzled: row off % 4 of the band, other lanes' scales too
+          scales = page + p.scale_off + walk.h * p.shs + off * p.sts;
+          next_in = in;
+        } else if (in && !v) {
           flag(p.dev_error, KVQ_DEVERR_BLOCK);
         }
       }
-      mask = __ballot_sync(0xFFFFFFFFu, !bad);
-    };
-    auto load_side = [&](const uint8_t* page, bool ok, bool in, bool swz,
-                         uint4 (&d)[4], uint2& sc) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = make_uint4(0, 0, 0, 0);
-      sc = make_uint2(0, 0);
-      if (!ok) return;
-      if (in) {
-        const uint8_t* src = page + walk.h * p.dhs + off * p.dts;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[i] = ldg128(src + 16 * i);
-      }
-      // swizzled: row off % 4 of the 4-token band (other lanes' scales too)
-      if (in || swz)
-        sc = ldg64(page + p.scale_off + walk.h * p.shs + off * p.sts);
-    };
-    // dequantise a row into a tile; scale words in group order
-    auto put = [&](const uint4 (&d)[4], uint32_t lo, uint32_t hi,
-                   bool linear, uint32_t dst) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {  // groups 2g, 2g + 1
-        const uint32_t pair =
-            linear ? (g < 2 ? lo : hi) >> (16 * (g & 1))
-                   : prmt(lo, hi, g | ((g + 4) << 4));
-        const uint32_t sf = e4m3x2_to_f16x2(pair & 0xFFFFu);
-        const uint32_t se = prmt(sf, sf, 0x1010u), so = prmt(sf, sf, 0x3232u);
-        const uint32_t w[4] = {d[g].x, d[g].y, d[g].z, d[g].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t o[4];
-          dequant_word(w[i], i < 2 ? se : so, o);
-          const int ch = 4 * g + i;  // 16-byte chunk of the row
-          sts128(dst + (ch >> 3) * kHalf + row_at + (((ch & 7) ^ sw) << 4),
-                 o);
+      next_mask = __ballot_sync(0xFFFFFFFFu, !bad);
+      if (more) {
+        job += kFillers;
+        if (job >= 8) {
+          job -= 8;
+          ++cnt;
+          if (++kt == walk.kv1) {
+            more = walk.next(p);
+            kt = walk.kv0;
+            ++seg;
+          }
         }
+        look_up();
       }
     };
-    // swizzled scales: 4 x 4 byte transposition over the quad's lanes, to
+    uint4 d[4];
+    uint2 sc;
+    auto load = [&](int i) {
+      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
+                   : "l"(data + 16 * i));
+    };
+    auto load_scales = [&]() {
+      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(sc.x), "=r"(sc.y)
+                   : "l"(scales));
+    };
+    // swizzled scales: 4 x 4 byte transposition over the band's lanes, to
     // words of the even and the odd groups of this thread's token
     auto untwist = [&](uint32_t w) {
       const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
@@ -747,146 +866,132 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
       return prmt(z, x, (lane & 2) ? 0x3276u : 0x5410u);
     };
 
-    uint32_t cnt = 0;
-    bool in = false, in_v = false;
-    if (have) {
-      locate();
-      in = k_ok && kt * kKeys + t < walk.s.L;
-      load_side(k_page, k_ok, in, p.swizzle_k, kd, ksc);
-      load_side(v_page, k_ok, in, true, vd, vsc);
-      v_ok = k_ok;
-      in_v = in;
-    }
-    while (have) {
-      const int stage = cnt & 1;
-      const uint32_t phase = (cnt >> 1) & 1;
-      const int cur_kt = kt, cur_seg = seg;
-      const bool first = kt == walk.kv0;
-      const uint32_t cur_mask = mask;
-      // K
-      if (!warp_wait(k_empty(stage), phase ^ 1, abort)) goto done;
-      {
-        uint32_t lo = ksc.x, hi = ksc.y;
-        if (p.swizzle_k) {
-          lo = untwist(lo);
-          hi = untwist(hi);
-          if (!in) lo = hi = 0;
-        }
-        put(kd, lo, hi, !p.swizzle_k, base + L::kK + stage * kTile);
-        if (lane == 0)
-          reinterpret_cast<volatile uint32_t*>(
-              smem + L::kValid)[(cnt & 3) * 4 + (warp & 3)] = cur_mask;
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full(stage));
-      }
-      const bool in_now = in_v;
-      // the next tile's K (its latency passes while V is converted)
-      if (++kt == walk.kv1) {
-        have = walk.next(p);
-        kt = walk.kv0;
-        ++seg;
-      }
-      if (have) {
-        locate();
-        in = k_ok && kt * kKeys + t < walk.s.L;
-        load_side(k_page, k_ok, in, p.swizzle_k, kd, ksc);
-      }
-      // V
-      if (!warp_wait(v_empty(stage), phase ^ 1, abort)) goto done;
-      {
-        // this warp's list of the segment's NaN places (last used four
-        // segments ago)
-        int* nan_row = nan_at + (cur_seg & 3) * 32 + (warp & 3);
-        if (first) {
-          if (lane < 8) nan_row[4 * lane] = INT32_MAX;
-          __syncwarp();
-        }
-        uint32_t lo = untwist(vsc.x), hi = untwist(vsc.y);
-        if (!in_now) lo = hi = 0;
-        if ((nan_bytes(lo) | nan_bytes(hi)) != 0u) {
-          // 0 * NaN would reach rows that do not see the token: its place
-          // goes on the list, zeros into the tile
-          uint32_t w[2] = {lo, hi};
+    look_up();
+    step();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int sh = 8 * (j >> 1);
-            if (((w[j & 1] >> sh) & 0x7Fu) == 0x7Fu) {
-              atomicMin(nan_row + 4 * j, cur_kt * kKeys + t);
-              w[j & 1] &= ~(0xFFu << sh);
-            }
+    for (int i = 0; i < 4; ++i) load(i);
+    load_scales();
+    while (next_some) {
+      const int stage = next_cnt & 1;
+      const uint32_t phase = (next_cnt >> 1) & 1;
+      const bool is_v = next_job >= 4, in = next_in;
+      const int quarter = next_job & 3, cur_pos = next_pos;
+      const bool swz = is_v || p.swizzle_k;
+      const uint32_t mask = next_mask, cur = next_cnt, cur_seg = next_seg;
+      const bool first = next_first;
+      step();
+      if (!warp_wait(is_v ? v_empty(stage) : k_empty(stage), phase ^ 1,
+                     abort))
+        goto done;
+      if (!is_v && lane == 0)
+        reinterpret_cast<volatile uint32_t*>(
+            smem + L::kValid)[(cur & 7) * 4 + quarter] = mask;
+      // this quarter's list of NaN places for the segment four ahead (its
+      // last user, four back, is done: see kNan)
+      if (is_v && first && lane < 8)
+        nan_at[((cur_seg + 4) & 7) * 32 + 4 * lane + quarter] = INT32_MAX;
+      uint32_t lo = sc.x, hi = sc.y;
+      if (swz) {
+        lo = untwist(lo);
+        hi = untwist(hi);
+      }
+      if (!in) lo = hi = 0;
+      if (is_v && (nan_bytes(lo) | nan_bytes(hi)) != 0u) {
+        // 0 * NaN would reach rows that do not see the token: its place goes
+        // on the list, zeros into the tile
+        uint32_t w[2] = {lo, hi};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int sh = 8 * (j >> 1);
+          if (((w[j & 1] >> sh) & 0x7Fu) == 0x7Fu) {
+            atomicMin(nan_at + (cur_seg & 7) * 32 + 4 * j + quarter, cur_pos);
+            w[j & 1] &= ~(0xFFu << sh);
           }
-          lo = w[0];
-          hi = w[1];
         }
-        put(vd, lo, hi, false, base + L::kV + stage * kTile);
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(stage));
+        lo = w[0];
+        hi = w[1];
       }
-      if (have) {
-        load_side(v_page, k_ok, in, true, vd, vsc);
-        in_v = in;
+      const uint32_t dst = base + (is_v ? L::kV : L::kK) + stage * kTile +
+                           (32 * quarter + lane) * 128;
+      const uint32_t sw = lane & 7;
+      load_scales();
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {  // groups 2g, 2g + 1
+        const uint32_t pair = swz ? prmt(lo, hi, g | ((g + 4) << 4))
+                                  : (g < 2 ? lo : hi) >> (16 * (g & 1));
+        const uint32_t sf = e4m3x2_to_f16x2(pair & 0xFFFFu);
+        const uint32_t se = prmt(sf, sf, 0x1010u), so = prmt(sf, sf, 0x3232u);
+        const uint32_t w[4] = {d[g].x, d[g].y, d[g].z, d[g].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t o[4];
+          dequant_word(w[i], i < 2 ? se : so, o);
+          const int ch = 4 * g + i;  // 16-byte chunk of the row
+          sts128(dst + (ch >> 3) * kHalf + (((ch & 7) ^ sw) << 4), o);
+        }
+        load(g);  // the next job's bytes into the registers just used
       }
-      ++cnt;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(is_v ? v_full(stage) : k_full(stage));
     }
-  } else {
-    if constexpr (kTiles == 2)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-    if (tid == (kTiles + 1) * 128 && any) {
-      // --- products -----------------------------------------------------------
-      uint32_t cnt = 0;  // KV tiles
-      uint32_t q_phase[kTiles] = {}, done[kTiles] = {};
-      auto qk = [&](int m, uint32_t n) {
-        const uint32_t q = base + L::kQ + m * kTile;
-        const uint32_t k = base + L::kK + (n & 1) * kTile;
+  } else if (warp == 4 * kTiles && any) {
+    // --- products: the warp waits, one lane issues ---------------------------
+    uint32_t cnt = 0;  // KV tiles
+    uint32_t q_phase[kTiles] = {}, p_phase[kTiles] = {};
+    auto qk = [&](int m, uint32_t n, bool last) {
+      const uint32_t q = desc_lo<16>(base + L::kQ + m * kTile);
+      const uint32_t k = desc_lo<16>(base + L::kK + (n & 1) * kTile);
+      if (elect()) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const uint32_t at = (i >> 2) * kHalf + (i & 3) * 32;
-          mma_ss(tmem + 128 * m, smem_desc(q + at, 16),
-                 smem_desc(k + at, 16), kIdesc, i > 0);
+          const uint32_t at = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
+          mma_ss(tmem + 128 * m, q + at, k + at, kIdesc, i > 0);
         }
         mma_commit(s_full(m));
-      };
-      bool go = true;
-      while (go) {
-        const int T = kTiles == 2 && walk.rows > 128 ? 2 : 1;
-        const int n = walk.kv1 - walk.kv0;
-        if (!wait(k_full(cnt & 1), (cnt >> 1) & 1, abort)) goto done;
+        if (last) mma_commit(k_empty(n & 1));
+      }
+      __syncwarp();
+    };
+    bool go = true;
+    while (go) {
+      const int T = kTiles == 2 && uniform(walk.rows) > 128 ? 2 : 1;
+      const int n = uniform(walk.kv1 - walk.kv0);
+      if (!warp_wait(k_full(cnt & 1), (cnt >> 1) & 1, abort)) goto done;
+      for (int m = 0; m < T; ++m) {
+        if (!warp_wait(q_full(m), q_phase[m] & 1, abort)) goto done;
+        ++q_phase[m];
+        fence_after();
+        qk(m, cnt, m == T - 1);
+      }
+      for (int j = 0; j < n; ++j, ++cnt) {
         for (int m = 0; m < T; ++m) {
-          if (!wait(q_full(m), q_phase[m] & 1, abort)) goto done;
-          ++q_phase[m];
+          if (m == 0 && !warp_wait(v_full(cnt & 1), (cnt >> 1) & 1, abort))
+            goto done;
+          if (!warp_wait(p_full(m), p_phase[m] & 1, abort)) goto done;
+          ++p_phase[m];
           fence_after();
-          qk(m, cnt);
-        }
-        mma_commit(k_empty(cnt & 1));
-        for (int j = 0; j < n; ++j, ++cnt) {
-          for (int m = 0; m < T; ++m) {
-            if (m == 0 &&
-                !wait(v_full(cnt & 1), (cnt >> 1) & 1, abort))
-              goto done;
-            if (!wait(p_full(m), done[m] & 1, abort)) goto done;
-            ++done[m];
-            fence_after();
-            const uint32_t v = base + L::kV + (cnt & 1) * kTile;
+          const uint32_t v =
+              desc_lo<kHalf>(base + L::kV + (cnt & 1) * kTile);
+          if (elect()) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               mma_ts(tmem + 128 * kTiles + 128 * m, tmem + 128 * m + 8 * i,
-                     smem_desc(v + i * 2048, kHalf), kIdescBmn,
-                     j > 0 || i > 0);
+                     v + i * (2048 >> 4), kIdescBmn, j > 0 || i > 0);
             mma_commit(o_done(m));
             if (m == T - 1) mma_commit(v_empty(cnt & 1));
-            if (j + 1 < n) {
-              if (m == 0 && !wait(k_full((cnt + 1) & 1),
-                                  ((cnt + 1) >> 1) & 1, abort))
-                goto done;
-              qk(m, cnt + 1);
-              if (m == T - 1) mma_commit(k_empty((cnt + 1) & 1));
-            }
+          }
+          __syncwarp();
+          if (j + 1 < n) {
+            if (m == 0 && !warp_wait(k_full((cnt + 1) & 1),
+                                     ((cnt + 1) >> 1) & 1, abort))
+              goto done;
+            fence_after();
+            qk(m, cnt + 1, m == T - 1);
           }
         }
-        go = walk.next(p);
       }
+      go = walk.next(p);
     }
   }
 done:
@@ -894,7 +999,7 @@ done:
   if (*abort != 0) {
     // products in flight end by themselves; wait for them before the tensor
     // memory goes
-    if (tid == (kTiles + 1) * 128) {
+    if (warp == 4 * kTiles && elect()) {
       mbar_init(bar(L::kBars), 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       mma_commit(bar(L::kBars));
