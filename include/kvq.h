@@ -449,7 +449,7 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  *
  * query          bf16 / fp16 (dtype) [total_q, num_q_heads, 128], rows
  *                query_stride0 elements apart (multiple of 8), 16-byte
- *                aligned; |q| < 65504 (fp16 range).  0 <= total_q <= 2^26.
+ *                aligned; |q| < 65504 (fp16 range).  0 <= total_q <= 2^25.
  * cu_q_lens      int32 [num_seqs + 1], cu_q_lens[0] >= 0, non-decreasing,
  *                at most total_q (values that break this are clamped and
  *                flagged KVQ_DEVERR_SEQ).  Rows that no sequence covers
@@ -463,7 +463,7 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  * block_table, block_table_stride, max_blocks_per_seq, k_scale, v_scale,
  * scale          as for kvq_paged_attention_nvfp4.
  * context_lens   int32 [num_seqs]; values above max_blocks_per_seq *
- *                block_size (or 2^30) are clamped to it and flagged
+ *                block_size (or 2^26) are clamped to it and flagged
  *                (KVQ_DEVERR_SEQ), negative ones count as 0.
  * workspace      workspace_bytes of device memory, 16-byte aligned; at
  *                least kvq_chunk_attention_workspace_bytes() (the same for

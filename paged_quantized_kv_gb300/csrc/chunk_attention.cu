@@ -153,18 +153,27 @@ __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
 }
 
 // Wait for phase `parity`, for at most KVQ_WAIT_LIMIT_NS (and 2^24 polls),
-// or until another thread of the CTA has given up.  False: give up.
+// or until another thread of the CTA has given up.  False: give up.  The
+// timer is looked at only every 64th poll: reading it takes
+// longer than most of these waits.
+__device__ __forceinline__ bool keep_waiting(uint32_t polls, uint64_t* start,
+                                          volatile int* abort) {
+  if (*abort != 0) return false;
+  const uint64_t now = dev::global_ns();
+  if (*start == 0) *start = now;
+  if (now - *start <= KVQ_WAIT_LIMIT_NS && polls < (1u << 24)) return true;
+  *abort = 1;
+  return false;
+}
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity,
                                      volatile int* abort) {
   if (mbar_try(bar, parity)) return true;
-  const uint64_t start = dev::global_ns();
-  for (uint32_t polls = 0; polls < (1u << 24); ++polls) {
+  uint64_t start = 0;
+#pragma unroll 1
+  for (uint32_t polls = 1;; ++polls) {
     if (mbar_try(bar, parity)) return true;
-    if (*abort != 0) return false;
-    if (dev::global_ns() - start > KVQ_WAIT_LIMIT_NS) break;
+    if (polls % 64 == 0 && !keep_waiting(polls, &start, abort)) return false;
   }
-  *abort = 1;
-  return false;
 }
 
 // The same for a whole warp: true in every lane or in none.
@@ -173,10 +182,38 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity,
   return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort));
 }
 
+// The same with every register of a tile live: no call, bounded by the count
+// alone (of polls that do not suspend the warp).
+__device__ __forceinline__ bool warp_spin(uint32_t bar, uint32_t parity,
+                                          volatile int* abort) {
+  uint32_t done = 0;
+#pragma unroll 1
+  for (uint32_t polls = 0; polls < (1u << 24) && !done; ++polls) {
+    asm volatile(
+        "{ .reg .pred p;\n"
+        "  mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        "  selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (polls % 256 == 255 && *abort != 0) break;
+  }
+  if (!done) *abort = 1;
+  return __all_sync(0xFFFFFFFFu, done);
+}
+
 __device__ __forceinline__ void sts128(uint32_t a, const uint32_t (&v)[4]) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v[0]),
                "r"(v[1]), "r"(v[2]), "r"(v[3])
                : "memory");
+}
+
+// Named barriers of warps that share TMEM lanes.
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 __device__ __forceinline__ uint4 ldg128(const void* p) {
@@ -284,15 +321,67 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Four scales of every other group: zeros for those that are NaN, their
+// token on the groups' lists (8 apart).
+__device__ __noinline__ uint32_t drop_nan(uint32_t w, int* at, int pos) {
+  for (int j = 0; j < 4; ++j)
+    if (((w >> (8 * j)) & 0x7Fu) == 0x7Fu) {
+      atomicMin(at + 8 * j, pos);
+      w &= ~(0xFFu << (8 * j));
+    }
+  return w;
+}
+
+// -inf for the logits whose bit is not set.
+__device__ __forceinline__ void mask32(uint32_t* s, uint32_t bits) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if ((bits & (1u << k)) == 0u) s[k] = 0xFF800000u;
+}
+// The first lim + 1 of 32 bits.
+__device__ __forceinline__ uint32_t first_bits(int lim) {
+  return lim >= 31 ? ~0u : lim < 0 ? 0u : (2u << lim) - 1u;
+}
+
+__device__ __forceinline__ float max64(const uint32_t* s) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < 64; k += 2)
+    mx[(k >> 1) & 3] = max3(mx[(k >> 1) & 3], __uint_as_float(s[k]),
+                            __uint_as_float(s[k + 1]));
+  return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+}
+
+// The output of this warp's rows, times each row's f.
+__device__ __forceinline__ void rescale(uint32_t col, float f) {
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    uint32_t o[16];
+    tmem_ld16(col + 16 * k, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+    tmem_st16(col + 16 * k, o);
+  }
+}
+
 // ---------------------------------------------------------------------------
 // The schedule
 // ---------------------------------------------------------------------------
-// Work is counted in units of one KV tile of one item; an item is a block of
-// kRows rows (token, head of the KV head) of one sequence and KV head and
-// spans the tiles up to its last row's position (one at least, so that rows
-// that see nothing are written too).  The units of all items, in the order
-// sequence, block, KV head, tile, are cut into equal shares, one per CTA; an
-// item that is cut leaves partial results, which the merge kernel joins.
+// An item is a block of up to kRows = 256 rows (token, head of the KV head)
+// of one sequence and KV head; it spans the KV tiles up to its last row's
+// position (one at least, so that rows that see nothing are written too).  It
+// counts as kItemUnits units and, for each tile, two units if it has more
+// than 128 rows, else one.  The units of all items, in the order sequence,
+// block, KV head, tile, are cut into equal shares, one per CTA; an item that
+// is cut leaves partial results, which the merge kernel joins.  A cut inside
+// a tile's two units falls behind the tile, one inside an item's own units
+// before its first tile; every share has at least kItemUnits + 2 units, so
+// that no share in the middle of an item is without a tile.
+constexpr int kRows = 256;
+constexpr int kItemUnits = 2;
+
 struct Seq {
   int q0, n, L;
 };
@@ -306,70 +395,123 @@ __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
   return s;
 }
 
-template <int kRows>
-struct Schedule {
-  // tiles of block i of a sequence
-  static __device__ __forceinline__ int width(const ChunkParams& p,
-                                              const Seq& s, int i) {
-    const int last = min((i + 1) * kRows, s.n * p.G) - 1;  // last row
-    const int seen = s.L - s.n + last / p.G + 1;
-    return seen <= 0 ? 1 : (seen + kKeys - 1) / kKeys;
+// The blocks of a sequence, one after the other.  Block i ends with row
+// min(256 (i + 1), n G) - 1, whose token sees L - n + row / G + 1 tokens:
+// floor((row + G (L - n + 128)) / (128 G)) tiles.  From block to block the
+// row grows by 256, and the quotient is carried along.  (Rows are below 2^29,
+// contexts at most 2^26 tokens, groups at most 16: 32 bits.)
+struct Blocks {
+  int left;   // rows from this block on
+  int step;   // 128 G
+  int tiles;  // of the block, were it full
+  int rest;   // of that division
+
+  __device__ __forceinline__ void begin(const ChunkParams& p, const Seq& s,
+                                        int i) {
+    step = 128 * p.G;
+    left = s.n * p.G - i * kRows;
+    const int top = i * kRows + kRows - 1 + p.G * (s.L - s.n + 128);
+    tiles = max(top, 0) / step;
+    rest = top - tiles * step;
   }
-  static __device__ __forceinline__ int blocks(const ChunkParams& p,
-                                               const Seq& s) {
-    return (s.n * p.G + kRows - 1) / kRows;
+  __device__ __forceinline__ void next() {
+    left -= kRows;
+    rest += kRows;
+    while (rest >= step) {
+      rest -= step;
+      ++tiles;
+    }
   }
-  static __device__ __forceinline__ int64_t units(const ChunkParams& p,
-                                                  const Seq& s) {
-    int64_t u = 0;
-    for (int i = 0, n = blocks(p, s); i < n; ++i) u += width(p, s, i);
-    return u * p.Hkv;
+  // Tiles of this block (a last block that is not full ends earlier).
+  __device__ __forceinline__ int width() const {
+    const int short_by = max(kRows - left, 0) - rest;
+    return max(tiles - (short_by > 0) - (short_by > step), 1);
+  }
+  __device__ __forceinline__ int weight() const { return left > 128 ? 2 : 1; }
+  __device__ __forceinline__ int units() const {
+    return kItemUnits + width() * weight();
   }
 };
 
-// A share's position: the next segment (one item's tiles kv0 .. kv1).
-template <int kRows>
-struct Walk {
-  int b, block, h, kv0;
-  int64_t left;  // units of the share from here on
-  Seq s;
-  int W, kv1;    // tiles of the item; end of this segment
-  int row0, rows;
+// Shares of U units: the first ones are one unit longer than the others.
+__device__ __noinline__ int64_t share_begin(int64_t U, int cta, int* ctas) {
+  const int64_t most = U / (kItemUnits + 2);
+  const int n = static_cast<int>(
+      min(static_cast<int64_t>(gridDim.x), max(most, int64_t{1})));
+  *ctas = n;
+  if (cta >= n) return U;
+  const int64_t size = U / n;
+  return size * cta + min(static_cast<int64_t>(cta), U - size * n);
+}
 
-  __device__ __forceinline__ void load(const ChunkParams& p) {
-    s = seq_of(p, b);
-    enter(p);
+// A position in a share: one segment, the tiles kv0 .. kv1 - 1 of one item.
+struct Walk {
+  int b, block, h;
+  int rem, end;   // the segment's units, from the item's first one
+  int64_t left;   // units of the share from here on
+  Seq s;
+  int W, weight;  // tiles of the item
+  int kv0, kv1;
+  int seg, tiles;  // segments and tiles of the share before this one
+  int there;       // (in the ring) this segment exists
+
+  __device__ __forceinline__ static int tile(int unit, int weight) {
+    return max(unit - kItemUnits + weight - 1, 0) / weight;
   }
   __device__ __forceinline__ void enter(const ChunkParams& p) {
-    W = Schedule<kRows>::width(p, s, block);
-    kv1 = static_cast<int>(min(static_cast<int64_t>(W), kv0 + left));
-    row0 = block * kRows;
-    rows = min(kRows, s.n * p.G - row0);
+    Blocks k;
+    k.begin(p, s, block);
+    W = k.width();
+    weight = k.weight();
+    end = static_cast<int>(min(static_cast<int64_t>(k.units()), rem + left));
+    kv0 = tile(rem, weight);
+    kv1 = tile(end, weight);
   }
-  // To the next segment; false at the end of the share.
-  __device__ __forceinline__ bool next(const ChunkParams& p) {
-    left -= kv1 - kv0;
-    if (left <= 0) return false;
-    kv0 = 0;
-    if (++h == p.Hkv) {
-      h = 0;
-      if (++block == Schedule<kRows>::blocks(p, s)) {
-        block = 0;
-        do {
-          if (++b >= p.num_seqs) return false;
-          s = seq_of(p, b);
-        } while (s.n == 0);
-      }
+  // To the next segment that has a tile (the first one: from a position with
+  // rem set and kv0 == kv1); false: there is none.
+  __device__ __forceinline__ bool next(const ChunkParams& p, bool first) {
+    if (!first) {
+      ++seg;
+      tiles += kv1 - kv0;
     }
-    enter(p);
+    do {
+      if (!first) {
+        left -= end - rem;
+        rem = 0;
+        if (left <= 0) return false;
+        if (++h == p.Hkv) {
+          h = 0;
+          if (++block * kRows >= s.n * p.G) {
+            block = 0;
+            do {
+              if (++b >= p.num_seqs) return false;
+              s = seq_of(p, b);
+            } while (s.n == 0);
+          }
+        }
+      }
+      first = false;
+      enter(p);
+    } while (kv0 >= kv1);
     return true;
   }
 };
 
-// CTAs that get a share of U units.
-__device__ __forceinline__ int ctas_of(int64_t U) {
-  return static_cast<int>(
-      min(static_cast<int64_t>(gridDim.x), max(U, int64_t{1})));
+// The position of the product warp and of each filler is in shared memory,
+// moved on by the warp's first lane, out of line: a copy of this code in
+// each role would be larger than the loops it serves.  True for the whole
+// warp if there is another segment.  (The softmax warps take theirs from the
+// product warp, through a ring: a call would cost them registers.)
+__device__ __noinline__ bool advance(const ChunkParams& p, Walk* walk) {
+  bool more = false;
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) {
+    Walk w = *walk;
+    more = w.next(p, false);
+    *walk = w;
+  }
+  __syncwarp();
+  return __shfl_sync(0xFFFFFFFFu, more, 0);
 }
 
 // What the merge kernel needs of an item that begins in a CTA's share and
@@ -380,8 +522,7 @@ struct Cut {
 };
 constexpr int kMaxCtas = 512;
 constexpr int64_t kCutBytes = kMaxCtas * sizeof(Cut);
-constexpr int kSlotRows = 256;
-constexpr int64_t kSlotFloats = kSlotRows * (kD + 2);
+constexpr int64_t kSlotFloats = kRows * (kD + 2);  // output, reference, sum
 
 __device__ __forceinline__ float* slot_of(const ChunkParams& p, int cta,
                                           int slot) {
@@ -389,224 +530,263 @@ __device__ __forceinline__ float* slot_of(const ChunkParams& p, int cta,
          (2 * static_cast<int64_t>(cta) + slot) * kSlotFloats;
 }
 
-// ---------------------------------------------------------------------------
-// Shared memory
-// ---------------------------------------------------------------------------
-constexpr int kStages = 2;
-constexpr int kWalkBytes = 80;
+// A segment that begins an item and does not end it: which CTAs go on with
+// it, up to the one whose share has the unit that its last tile begins with.
+__device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
+                                      int64_t U, int64_t share_end) {
+  const int64_t last = share_end - w.left - w.rem + kItemUnits +
+                       static_cast<int64_t>(w.W) * w.weight - w.weight;
+  const int cta = blockIdx.x;
+  int more = 0, ctas;
+  do {
+    ++more;
+  } while (share_begin(U, cta + more + 1, &ctas) <= last);
+  *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
+      w.b, w.block, w.h, w.seg > 0, more, {0, 0, 0}};
+}
 
-template <int kTiles>
-struct Smem {
-  static constexpr int kQ = 0;                              // kTiles tiles
-  static constexpr int kK = kQ + kTiles * kTile;            // kStages tiles
-  static constexpr int kV = kK + kStages * kTile;           // kStages tiles
-  static constexpr int kBar = kV + kStages * kTile;
-  static constexpr int kBars = 4 * kStages + 4 * kTiles;
-  // Per tile and quarter: the tokens that are not left out.  A filler is at
-  // most a few tiles ahead of the softmax: K of tile k + 3 waits for the
-  // products of tile k + 1, which wait for the weights of tile k.
-  static constexpr int kValid = kBar + 8 * 18;  // [8][4] words
-  // Per segment, group and quarter: the first token whose V scale is NaN.
-  // V of tile k waits for the products of tile k - 2, so when segment s is
-  // filled the epilogues of the segments up to s - 3 are over.
-  static constexpr int kNan = kValid + 128;     // [8][8][4] ints
-  static constexpr int kMisc = kNan + 1024;     // 16 ints
-  static constexpr int kScan = kMisc + 64;      // 36 int64
-  // The softmax warps' positions, kept out of their registers.
-  static constexpr int kWalk = kScan + 288;
-  static constexpr int kBytes =
-      kWalk + 4 * kTiles * kWalkBytes + 1024;   // 1024: alignment
-  static_assert(kBars < 18 && kValid % 16 == 0, "");
+// ---------------------------------------------------------------------------
+// Roles, barriers, shared memory
+// ---------------------------------------------------------------------------
+// Warps 0 .. 7: softmax, a warpgroup for each slot (query tile), one row per
+// thread.  Warps 8 and 9 issue the products of slot 0 and 1: the tensor cores
+// queue hardly more than one instruction, so what a warp spends between two
+// batches of them (waits, commits) is hidden only by the other warp's.  Warps
+// 10 .. 15 (fillers) dequantise.
+// (An SM quarter holds the registers of four warps of 128: a 17th warp would
+// cost every warp a quarter of its registers.)
+constexpr int kSoftWarps = 8;
+constexpr int kFillers = 6;
+constexpr int kThreads = 32 * (kSoftWarps + 2 + kFillers);
+constexpr int kStages = 2;
+
+enum Bar {
+  kKFull = 0,                  // [stage] a tile of K is in shared memory
+  kKEmpty = kKFull + kStages,  // [stage] its products are done
+  kVFull = kKEmpty + kStages,
+  kVEmpty = kVFull + kStages,
+  kQFull = kVEmpty + kStages,  // [slot] the query rows are in shared memory
+  kSFull = kQFull + 2,         // [slot] logits are in tensor memory
+  kPFull = kSFull + 2,         // [slot] weights are in tensor memory
+  kODone = kPFull + 2,         // [slot] they are multiplied with V
+  kTurn = kODone + 2,          // [slot] the tensor cores are this slot's
+  kOFree = kTurn + 2,          // the segment's output has been read
+  kSegment = kOFree + 1,       // the next segment is in the ring
+  kLast = kSegment + 1,          // (a wait that gave up: products in flight)
+  kBars = kLast + 1
 };
 
-// Roles of the warps: kTiles softmax warpgroups (one query tile each, one
-// row per thread), then one warp that issues the products and seven that
-// dequantise (one token's K or V row per thread).  An SM quarter holds the
-// registers of four warps of 128, so a 17th warp would cost every warp a
-// quarter of its registers.
-template <int kTiles>
-constexpr int kThreadsOf = 128 * (kTiles + 2);
-constexpr int kFillers = 7;
+constexpr int kQAt = 0;                       // 2 tiles
+constexpr int kKAt = kQAt + 2 * kTile;        // kStages tiles
+constexpr int kVAt = kKAt + kStages * kTile;  // kStages tiles
+constexpr int kBarAt = kVAt + kStages * kTile;
+// Per tile and quarter: the tokens that are not left out ([8][4] words).  K
+// of tile k waits for the logits of tile k - 2, whose product is issued after
+// the weights of tile k - 4 at the latest: eight entries are enough.
+constexpr int kValidAt = kBarAt + 8 * 22;
+// Per segment, group and quarter: the first token whose V scale is NaN
+// ([8][8][4] ints).  V of tile k waits for tile k - 2's product with V, and
+// that one for the epilogues of all segments before its own: when segment s
+// is filled, those up to s - 3 are over.
+constexpr int kNanAt = kValidAt + 128;
+constexpr int kMiscAt = kNanAt + 1024;   // 16 ints
+constexpr int kScanAt = kMiscAt + 64;    // 32 int64
+constexpr int kUnitsAt = kScanAt + 256;  // 3 int64: all units, share's ends
+constexpr int kSumAt = kUnitsAt + 32;    // [slot][row] floats
+constexpr int kRefAt = kSumAt + 1024;    // [slot][row] floats
+// The segments for the softmax warps ([segment % 4]; when segment s begins,
+// weights of segment s - 1 have been multiplied, so s - 3 is over), then the
+// other warps' positions.
+constexpr int kRingAt = kRefAt + 1024;
+constexpr int kWalkAt = kRingAt + 4 * static_cast<int>(sizeof(Walk));
+constexpr int kSmemBytes =
+    kWalkAt + (kFillers + 2) * static_cast<int>(sizeof(Walk)) + 1024;
+static_assert(kBars <= 22 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
+                  sizeof(Walk) % 8 == 0,
+              "");
+// Tensor memory: logits (and, over them, weights) of the two slots, outputs
+// of the two slots.
+constexpr uint32_t kOCol = 256;
 
-template <int kTiles, bool kF16>
-__global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
+template <bool kF16>
+__global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams p) {
-  using L = Smem<kTiles>;
-  constexpr int kRows = 128 * kTiles;
-  constexpr int kThreads = kThreadsOf<kTiles>;
   extern __shared__ __align__(16) uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
   const uint32_t base = smem_addr(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int wg = warp >> 2;
-  volatile int* misc = reinterpret_cast<volatile int*>(smem + L::kMisc);
-  volatile int* abort = misc;                    // a wait gave up
-  int* nan_at = reinterpret_cast<int*>(smem + L::kNan);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + L::kScan);
-
-  auto bar = [&](int i) { return base + L::kBar + 8 * i; };
-  auto k_full = [&](int s) { return bar(s); };
-  auto k_empty = [&](int s) { return bar(kStages + s); };
-  auto v_full = [&](int s) { return bar(2 * kStages + s); };
-  auto v_empty = [&](int s) { return bar(3 * kStages + s); };
-  auto q_full = [&](int m) { return bar(4 * kStages + m); };
-  auto s_full = [&](int m) { return bar(4 * kStages + kTiles + m); };
-  auto p_full = [&](int m) { return bar(4 * kStages + 2 * kTiles + m); };
-  auto o_done = [&](int m) { return bar(4 * kStages + 3 * kTiles + m); };
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + kMiscAt);
+  volatile int* abort = misc;  // a wait gave up
+  int* nan_at = reinterpret_cast<int*>(smem + kNanAt);
+  volatile int64_t* units_kept =
+      reinterpret_cast<volatile int64_t*>(smem + kUnitsAt);
+  auto bar = [&](int i) { return base + kBarAt + 8 * i; };
 
   if (warp == 0) {
     asm volatile(
-        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::
-            "r"(base + L::kMisc + 4),
-        "r"(256u * kTiles)
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+        ::"r"(base + kMiscAt + 4)
         : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(k_full(s), 4);
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_full(s), 4);
-      mbar_init(v_empty(s), 1);
+      mbar_init(bar(kKFull + s), 4);
+      mbar_init(bar(kKEmpty + s), 2);
+      mbar_init(bar(kVFull + s), 4);
+      mbar_init(bar(kVEmpty + s), 2);
     }
-    for (int m = 0; m < kTiles; ++m) {
-      mbar_init(q_full(m), 4);
-      mbar_init(s_full(m), 1);
-      mbar_init(p_full(m), 4);
-      mbar_init(o_done(m), 1);
+    for (int m = 0; m < 2; ++m) {
+      mbar_init(bar(kQFull + m), 4);
+      mbar_init(bar(kSFull + m), 1);
+      mbar_init(bar(kPFull + m), 4);
+      mbar_init(bar(kTurn + m), 1);
+      mbar_init(bar(kODone + m), 1);
     }
+    mbar_init(bar(kOFree), kSoftWarps);
+    mbar_init(bar(kSegment), 2);
+    mbar_init(bar(kLast), 2);
     misc[0] = 0;
-    misc[2] = -1;
+    misc[2] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < 256) nan_at[tid] = INT32_MAX;
-  if (tid == 0)  // nothing to join, unless the end of this CTA says so
-    (reinterpret_cast<Cut*>(p.workspace) + blockIdx.x)->more = 0;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0)  // nothing to join, unless the end of this CTA says so
+    (reinterpret_cast<Cut*>(p.workspace) + blockIdx.x)->more = 0;
 
   // --- this CTA's share -----------------------------------------------------
   // inclusive scan of the sequences' units, kThreads of them at a time; with
   // no more sequences than threads each is looked at once
-  const int rounds = (p.num_seqs + kThreads - 1) / kThreads;
-  int64_t units = 0, incl = 0, total = 0;
-  auto scan_round = [&](int r, bool check) {
-    const int b = r * kThreads + tid;
-    units = 0;
-    if (b < p.num_seqs) {
-      const Seq s = seq_of(p, b);
-      units = Schedule<kRows>::units(p, s);
-      if (check && blockIdx.x == 0 &&
-          (s.q0 != __ldg(p.cu + b) || s.q0 + s.n != __ldg(p.cu + b + 1) ||
-           __ldg(p.lens + b) > s.L))
-        flag(p.dev_error, KVQ_DEVERR_SEQ);
-    }
-    int64_t x = units;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-      if (lane >= d) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = x;
-    __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) before += scan[w];
-      all += scan[w];
-    }
-    incl = total + before + x;
-    total += all;
-  };
-  for (int r = 0; r < rounds; ++r) scan_round(r, true);
-  const int64_t U = total;
-  const int cta = blockIdx.x, ctas = ctas_of(U);
-  const int64_t u0 = cta < ctas ? U * cta / ctas : U;
-  const int64_t u1 = cta < ctas ? U * (cta + 1) / ctas : U;
-  if (rounds > 1) total = 0;
-  for (int r = 0; r < rounds; ++r) {
-    if (rounds > 1) scan_round(r, false);
-    if (units > 0 && u0 < u1 && incl - units <= u0 && u0 < incl) {
-      const int b = r * kThreads + tid;
-      const Seq s = seq_of(p, b);
-      int64_t rem = u0 - (incl - units);
-      int i = 0, w = Schedule<kRows>::width(p, s, 0);
-      while (rem >= static_cast<int64_t>(w) * p.Hkv) {
-        rem -= static_cast<int64_t>(w) * p.Hkv;
-        w = Schedule<kRows>::width(p, s, ++i);
+  Walk* ring = reinterpret_cast<Walk*>(smem + kRingAt);
+  {
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + kScanAt);
+    const int rounds = (p.num_seqs + kThreads - 1) / kThreads;
+    int64_t units = 0, incl = 0, U = 0, u0 = 0, u1 = 0;
+    Seq s;
+#pragma unroll 1
+    for (int r = 0; r < (rounds > 1 ? 2 * rounds : 1); ++r) {
+      if (r == rounds) U = 0;  // (second time over: the totals again)
+      const int b = r % rounds * kThreads + tid;
+      units = 0;
+      if (b < p.num_seqs) {
+        s = seq_of(p, b);
+        if (s.n > 0) {
+          Blocks k;
+          k.begin(p, s, 0);
+#pragma unroll 1
+          for (; k.left > 0; k.next()) units += k.units();
+        }
+        units *= p.Hkv;
+        if (r < rounds && blockIdx.x == 0 &&
+            (s.q0 != __ldg(p.cu + b) || s.q0 + s.n != __ldg(p.cu + b + 1) ||
+             __ldg(p.lens + b) > s.L))
+          flag(p.dev_error, KVQ_DEVERR_SEQ);
       }
-      misc[2] = b;
-      misc[3] = i;
-      misc[4] = static_cast<int>(rem / w);
-      misc[5] = static_cast<int>(rem % w);
+      int64_t x = units;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      incl = U + x;
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) incl += scan[w];
+        U += scan[w];
+      }
+      if (r == rounds - 1) {  // the sum is known
+        int ctas;
+        u0 = share_begin(U, blockIdx.x, &ctas);
+        u1 = share_begin(U, blockIdx.x + 1, &ctas);
+        if (tid == 0) {
+          units_kept[0] = U;
+          units_kept[1] = u1;
+        }
+      }
+      // (r >= rounds - 1: u0 and u1 are known)
+      if (r >= rounds - 1 && (rounds == 1 || r >= rounds) && units > 0 &&
+          u0 < u1 && incl - units <= u0 && u0 < incl) {
+        int64_t rem = u0 - (incl - units);
+        Blocks k;
+        k.begin(p, s, 0);
+        int i = 0;
+#pragma unroll 1
+        for (; rem >= static_cast<int64_t>(k.units()) * p.Hkv; k.next()) {
+          rem -= static_cast<int64_t>(k.units()) * p.Hkv;
+          ++i;
+        }
+        Walk w = {};
+        w.b = b;
+        w.block = i;
+        w.h = static_cast<int>(rem) / k.units();
+        w.rem = static_cast<int>(rem) - w.h * k.units();
+        w.left = u1 - u0;
+        w.s = s;
+        w.there = w.next(p, true);
+        ring[0] = w;
+        misc[2] = w.there;
+      }
     }
-  }
-  if (tid == 0) {
-    scan[32] = U;
-    scan[33] = u0;
-    scan[34] = u1;
   }
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-  volatile int64_t* kept_units = scan + 32;  // U, u0, u1
-  Walk<kRows> walk;
-  walk.b = misc[2];
-  walk.block = misc[3];
-  walk.h = misc[4];
-  walk.kv0 = misc[5];
-  walk.left = kept_units[2] - kept_units[1];
-  const bool any = walk.b >= 0;
-  if (any) walk.load(p);
+  const bool any = misc[2] != 0;
+  Walk* walk = reinterpret_cast<Walk*>(smem + kWalkAt) +
+               (warp < kSoftWarps ? 0 : warp - kSoftWarps);
+  if (any && warp >= kSoftWarps && lane == 0) *walk = ring[0];
+  __syncwarp();
 
-  if (wg < kTiles) {
-    // --- softmax: tile m, one row per thread --------------------------------
-    if constexpr (kTiles == 2)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-    const int m = wg, row = tid & 127;
+  if (warp < kSoftWarps) {
+    // --- softmax ----------------------------------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    const int m = warp >> 2, row = tid & 127;
+    const uint32_t lanes =
+        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_col = lanes + 128 * m, o_col = lanes + kOCol + 128 * m;
     const float c0 = p.scale * __ldg(p.k_scale);
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_col = tmem + lanes + 128 * m;
-    const uint32_t o_col = tmem + lanes + 128 * kTiles + 128 * m;
     // (c0 == 0: a query of zeros, and any c > 0)
     const float c = c0 != 0.0f ? fabsf(c0) * kLog2e : 1.0f;
-    // A tile's logits take 128 registers.  The warp's position waits in
-    // shared memory meanwhile.
-    struct Kept {
-      Walk<kRows> walk;
-      int seg;
-    };
-    static_assert(sizeof(Kept) <= kWalkBytes, "");
-    Kept* kept = reinterpret_cast<Kept*>(smem + L::kWalk + warp * kWalkBytes);
-    if (lane == 0) *kept = {walk, 0};
-    __syncwarp();
-    uint32_t cnt = 0;  // tiles of this warpgroup so far
-    bool go = any;
-    while (go) {
+    uint32_t cnt0 = 0, cnt1 = 0;  // tiles of the slots so far
+    for (uint32_t seg = 0; any; ++seg) {
+      if (seg > 0 && !warp_wait(bar(kSegment), (seg - 1) & 1, abort))
+        goto done;
+      if (seg > 0 && !ring[seg & 3].there) break;
       int kv0, kv1, pos, tiles, rows;
       {
-        const Walk<kRows> w = kept->walk;
+        const Walk& w = ring[seg & 3];
         kv0 = w.kv0;
         kv1 = w.kv1;
-        rows = w.rows - 128 * m;  // rows of this tile
+        rows = min(kRows, w.s.n * p.G - w.block * kRows);
         // (tile kt of this segment is the CTA's (tiles + kt)-th)
-        tiles = static_cast<int>(kept_units[2] - kept_units[1] - w.left) - kv0;
-        const int r = w.row0 + 128 * m + row;  // row of the sequence
+        tiles = w.tiles - kv0;
+        // two query tiles, or one whose KV tiles the slots share out
+        const int at = (rows > 128 ? 128 * m : 0) + row;
+        const int r = w.block * kRows + at;  // row of the sequence
         const int tok = r / p.G;
-        const bool live = row < rows;
-        pos = live ? w.s.L - w.s.n + tok : -1;
-        if (rows > 0) {
+        // (a row that is none sees all, so that it does not slow the others)
+        pos = at < rows ? w.s.L - w.s.n + tok : INT32_MAX;
+        if (m == 0 || rows > 128) {
           // the query row, rounded to fp16, its sign folded with the scale's
           const uint16_t* src = p.q + (w.s.q0 + tok) * p.q_stride0 +
                                 (w.h * p.G + (r - tok * p.G)) * kD;
-          const uint32_t dst = base + L::kQ + m * kTile + row * 128;
+          const uint32_t dst = base + kQAt + m * kTile + row * 128;
           const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
+          uint4 v[16];
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (live && c0 != 0.0f) v = ldg128(src + 8 * g);
-            uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            v[g] = make_uint4(0, 0, 0, 0);
+            if (at < rows && c0 != 0.0f) v[g] = ldg128(src + 8 * g);
+          }
+#pragma unroll
+          for (int g = 0; g < 16; ++g) {
+            uint32_t x[4] = {v[g].x, v[g].y, v[g].z, v[g].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[k] = (kF16 ? x[k] : bf16x2_to_f16x2(x[k])) ^ flip;
@@ -614,68 +794,62 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(q_full(m));
+          if (lane == 0) mbar_arrive(bar(kQFull + m));
         }
       }
-      if (rows > 0) {
-        float ref = -INFINITY, sum = 0.0f;
-        for (int kt = kv0; kt < kv1; ++kt) {
-          if (!warp_wait(s_full(m), cnt & 1, abort)) goto done;
-          fence_after();
-          uint32_t s[128];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(s_col + 32 * k, s + 32 * k);
-          const uint32_t* valid = reinterpret_cast<const uint32_t*>(
-              smem + L::kValid + ((tiles + kt) & 7) * 16);
-          const uint32_t v0 = valid[0], v1 = valid[1], v2 = valid[2],
-                         v3 = valid[3];
-          tmem_wait_ld();
-          const int lim = pos - kt * kKeys;  // columns 0 .. lim are seen
-          const bool all = lim >= kKeys - 1 && (v0 & v1 & v2 & v3) == ~0u;
-          if (!__all_sync(0xFFFFFFFFu, all)) {
-            const uint32_t vs[4] = {v0, v1, v2, v3};
-#pragma unroll
-            for (int k = 0; k < 128; ++k)
-              if (k > lim || !((vs[k >> 5] >> (k & 31)) & 1u))
-                s[k] = 0xFF800000u;  // -inf
-          }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int k = 0; k < 128; k += 2)
-            mx[(k >> 1) & 3] =
-                max3(mx[(k >> 1) & 3], __uint_as_float(s[k]),
-                     __uint_as_float(s[k + 1]));
-          const float top =
-              fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-          // The reference follows the maximum only when it lags by more
-          // than kLag, so weights stay below 2^kLag and few tiles rescale.
-          const bool move = top > ref + kLag;
-          if (__any_sync(0xFFFFFFFFu, move)) {
-            const float f = move ? ex2(ref - top) : 1.0f;
-            if (move) {
-              ref = top;
-              sum *= f;
-            }
-            if (kt > kv0) {
-              if (!warp_wait(o_done(m), (cnt - 1) & 1, abort)) goto done;
-              fence_after();
+      const bool two = rows > 128;
+      float ref = -INFINITY, sum = 0.0f;
+      uint32_t cnt = m == 0 ? cnt0 : cnt1;
+      const int kt0 = two ? kv0 : kv0 + m, step = two ? 1 : 2;
 #pragma unroll 1
-              for (int k = 0; k < 8; ++k) {
-                uint32_t o[16];
-                tmem_ld16(o_col + 16 * k, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                tmem_st16(o_col + 16 * k, o);
-              }
-            }
+      for (int kt = kt0; kt < kv1; kt += step, ++cnt) {
+        if (!warp_wait(bar(kSFull + m), cnt & 1, abort)) goto done;
+        fence_after();
+        const uint4 valid = *reinterpret_cast<const uint4*>(
+            smem + kValidAt + ((tiles + kt) & 7) * 16);
+        uint32_t s[128];
+        tmem_ld32(s_col, s);
+        tmem_ld32(s_col + 32, s + 32);
+        tmem_wait_ld();
+        tmem_ld32(s_col + 64, s + 64);
+        tmem_ld32(s_col + 96, s + 96);
+        float top = max64(s);
+        tmem_wait_ld();
+        top = fmaxf(top, max64(s + 64)) * c;
+        // (looked at only now: the products keep shared memory busy, and
+        // what is read from it comes late)
+        const int lim = pos - kt * kKeys;  // the row sees columns 0 .. lim
+        const bool all = lim >= kKeys - 1 &&
+                         (valid.x & valid.y & valid.z & valid.w) == ~0u;
+        if (!__all_sync(0xFFFFFFFFu, all)) {
+          mask32(s, valid.x & first_bits(lim));
+          mask32(s + 32, valid.y & first_bits(lim - 32));
+          mask32(s + 64, valid.z & first_bits(lim - 64));
+          mask32(s + 96, valid.w & first_bits(lim - 96));
+          top = fmaxf(max64(s), max64(s + 64)) * c;
+        }
+        // The reference follows the maximum only when it lags by more than
+        // kLag, so weights stay below 2^kLag and few tiles rescale.
+        const bool move = top > ref + kLag;
+        if (__any_sync(0xFFFFFFFFu, move)) {
+          const float f = move ? ex2(ref - top) : 1.0f;
+          if (move) {
+            ref = top;
+            sum *= f;
           }
-          const float low = ref == -INFINITY ? 0.0f : ref;
-          const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
-          uint64_t add[2] = {0, 0};
+          if (kt > kt0) {
+            if (!warp_spin(bar(kODone + m), (cnt - 1) & 1, abort)) goto done;
+            fence_after();
+            rescale(o_col, f);
+          }
+        }
+        const float low = ref == -INFINITY ? 0.0f : ref;
+        const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
+        uint64_t add[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < 128; k += 2) {
+        for (int half = 0; half < 2; ++half) {
+#pragma unroll
+          for (int k = 64 * half; k < 64 * half + 64; k += 2) {
             float a, b;
             unpack2(fma2(pack2(__uint_as_float(s[k]),
                                __uint_as_float(s[k + 1])), cc, ll), a, b);
@@ -684,118 +858,138 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
             add[(k >> 1) & 1] = add2(add[(k >> 1) & 1], pack2(a, b));
             s[k >> 1] = pack_f16x2(a, b);
           }
-          float e, o;
-          unpack2(add2(add[0], add[1]), e, o);
-          sum += e + o;
-          tmem_st32(s_col, s);
-          tmem_st32(s_col + 32, s + 32);
-          tmem_wait_st();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(m));
-          ++cnt;
+          tmem_st32(s_col + 32 * half, s + 32 * half);
         }
-        // --- epilogue -------------------------------------------------------
-        if (!warp_wait(o_done(m), (cnt - 1) & 1, abort)) goto done;
-        fence_after();
-        const Walk<kRows> w = kept->walk;
-        const int seg = kept->seg;
-        const int4* nan_row =
-            reinterpret_cast<const int4*>(nan_at + (seg & 7) * 32);
-        const bool live = row < rows;
-        const bool whole = kv0 == 0 && kv1 == w.W;
-        const float inv = sum > 0.0f ? __ldg(p.v_scale) / sum
-                                     : (sum == 0.0f ? 0.0f : sum);
-        float* slot = slot_of(p, blockIdx.x, seg > 0);
-        const int r = w.row0 + 128 * m + row, tok = r / p.G;
-        uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
-                        (w.h * p.G + (r - tok * p.G)) * kD;
-        float* part = slot + (128 * m + row) * kD;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint32_t o[32];
-          __syncwarp();
-          tmem_ld32(o_col + 32 * k, o);
+        tmem_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + m));
+        float e, o;
+        unpack2(add2(add[0], add[1]), e, o);
+        sum += e + o;
+      }
+      // --- epilogue ---------------------------------------------------------------
+      const int n = kv1 - kv0;
+      cnt0 += two ? n : (n + 1) >> 1;
+      cnt1 += two ? n : n >> 1;
+      float w0 = 1.0f, w1 = 0.0f;
+      if (two) {
+        if (!warp_wait(bar(kODone + m), (cnt - 1) & 1, abort)) goto done;
+      } else {
+        // the slots' sums and references (a product of this segment with V
+        // is done, so every warp has read those of the last segment)
+        float* x_sum = reinterpret_cast<float*>(smem + kSumAt) + row;
+        float* x_ref = reinterpret_cast<float*>(smem + kRefAt) + row;
+        if (!warp_wait(bar(kODone), (cnt0 - 1) & 1, abort)) goto done;
+        if (n > 1 && !warp_wait(bar(kODone + 1), (cnt1 - 1) & 1, abort))
+          goto done;
+        x_sum[128 * m] = sum;
+        x_ref[128 * m] = ref;
+        bar_sync(1 + (warp & 3), 64);
+        const float r0 = x_ref[0], r1 = x_ref[128];
+        ref = fmaxf(r0, r1);
+        w0 = r0 == ref ? 1.0f : ex2(r0 - ref);
+        w1 = r1 == ref ? 1.0f : ex2(r1 - ref);
+        sum = x_sum[0] * w0 + x_sum[128] * w1;
+      }
+      fence_after();
+      const Walk& w = ring[seg & 3];
+      const int4* nan_row =
+          reinterpret_cast<const int4*>(nan_at + (seg & 7) * 32);
+      const int at = (two ? 128 * m : 0) + row;
+      const bool whole = kv0 == 0 && kv1 == w.W;
+      const float inv = sum > 0.0f ? __ldg(p.v_scale) / sum
+                                   : (sum == 0.0f ? 0.0f : sum);
+      float* slot = slot_of(p, blockIdx.x, seg > 0);
+      const int r = w.block * kRows + at, tok = r / p.G;
+      uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
+                      (w.h * p.G + (r - tok * p.G)) * kD;
+      float* part = slot + at * kD;
+      // columns: the row of the slot's own output, or half a row of the two
+      // slots' joined ones
+#pragma unroll 1
+      for (int k = 0; k < (two ? 4 : 2); ++k) {
+        const int col = two ? 32 * k : 64 * m + 32 * k;
+        uint32_t o[32];
+        __syncwarp();
+        tmem_ld32(lanes + kOCol + (two ? 128 * m : 0) + col, o);
+        if (!two && n > 1) {
+          uint32_t o1[32];
+          tmem_ld32(lanes + kOCol + 128 + col, o1);
           tmem_wait_ld();
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            const int4 at = nan_row[2 * k + g];
-            if (min(min(at.x, at.y), min(at.z, at.w)) <= pos) {
+          for (int j = 0; j < 32; ++j)
+            o[j] = __float_as_uint(__uint_as_float(o[j]) * w0 +
+                                   __uint_as_float(o1[j]) * w1);
+        } else {
+          tmem_wait_ld();
+        }
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[16 * g + j] = 0x7FFFFFFFu;
-            }
-          }
-          if (live && whole) {
+        for (int g = 0; g < 2; ++g) {
+          const int4 x = nan_row[col / 16 + g];
+          if (min(min(x.x, x.y), min(x.z, x.w)) <= pos) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float x = __uint_as_float(o[8 * g + 2 * j]) * inv;
-                const float y = __uint_as_float(o[8 * g + 2 * j + 1]) * inv;
-                w[j] = kF16 ? pack_f16x2(x, y) : pack_bf16x2(x, y);
-              }
-              *reinterpret_cast<uint4*>(dst + 32 * k + 8 * g) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (live) {
-#pragma unroll
-            for (int g = 0; g < 8; ++g)
-              *reinterpret_cast<uint4*>(part + 32 * k + 4 * g) =
-                  make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2],
-                             o[4 * g + 3]);
+            for (int j = 0; j < 16; ++j) o[16 * g + j] = 0x7FFFFFFFu;
           }
         }
-        __syncwarp();
-        if (!whole && live) {
-          slot[kSlotRows * kD + 128 * m + row] = ref;
-          slot[kSlotRows * (kD + 1) + 128 * m + row] = sum;
+        if (at < rows && whole) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t x[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float a = __uint_as_float(o[8 * g + 2 * j]) * inv;
+              const float b = __uint_as_float(o[8 * g + 2 * j + 1]) * inv;
+              x[j] = kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+            }
+            *reinterpret_cast<uint4*>(dst + col + 8 * g) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        } else if (at < rows) {
+#pragma unroll
+          for (int g = 0; g < 8; ++g)
+            *reinterpret_cast<uint4*>(part + col + 4 * g) =
+                make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2],
+                           o[4 * g + 3]);
         }
-        fence_before();
       }
-      Walk<kRows> w = kept->walk;
-      const int seg = kept->seg;
-      if (tid == 0 && kv0 == 0 && kv1 < w.W) {
-        // goes on in the next CTAs' shares
-        const int64_t all = kept_units[0];
-        const int64_t end = kept_units[2] - w.left + w.W;
-        const int cta = blockIdx.x, ctas = ctas_of(all);
-        int more = 1;
-        while (cta + more + 1 < ctas && all * (cta + more + 1) / ctas < end)
-          ++more;
-        *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
-            w.b, w.block, w.h, seg > 0, more, {0, 0, 0}};
+      if (!whole && at < rows && (two || m == 0)) {
+        slot[kRows * kD + at] = ref;
+        slot[kRows * (kD + 1) + at] = sum;
       }
-      go = w.next(p);
+      fence_before();
       __syncwarp();
-      if (lane == 0) *kept = {w, seg + 1};
-      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kOFree));
     }
   } else {
-    if constexpr (kTiles == 2)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   }
-  if (wg >= kTiles && warp != 4 * kTiles) {
+  if (warp >= kSoftWarps + 2) {
     // --- dequantise: a quarter (32 tokens) of a tile's K or V at a time ------
     // The quarters K 0..3, V 0..3 of the share's tiles, in order, are dealt
     // round-robin to the warps.  A warp has three in hand: the one whose raw
     // bytes are in registers, the next one, whose page is known, and the one
     // behind it, whose block id is on its way (`job`, `kt` and `walk` are at
     // that one).
-    int job = warp - 4 * kTiles - 1;  // 0..3: K quarters, 4..7: V quarters
-    int kt = walk.kv0, seg = 0;
+    int job = warp - kSoftWarps - 2;  // 0..3: K quarters, 4..7: V quarters
+    // (this segment: its sequence's length and table row, its head, its end)
+    int kt = walk->kv0, kv1 = walk->kv1, len = walk->s.L, seg = 0;
+    const int32_t* table = p.block_table + walk->b * p.bt_stride;
+    int64_t data_h = walk->h * p.dhs;
+    int64_t scale_h = p.scale_off + walk->h * p.shs;
     uint32_t cnt = 0;      // tile of the share
-    bool more = any;       // there is a tile at (walk, kt)
+    bool more = any;       // there is a tile at kt
+    bool first = true;     // it is the segment's first
     int32_t blk = -1;      // the block id of this thread's token
     int pos = 0, off = 0;  // the token, and its place in the page
     bool quad = false;     // its 4-token band is inside the context
     auto look_up = [&]() {
       pos = kt * kKeys + 32 * (job & 3) + lane;
-      quad = more && (pos & ~3) < walk.s.L;  // (a band is in one page)
+      quad = more && (pos & ~3) < len;  // (a band is in one page)
       if (quad) {
         const int j = p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B;
         off = pos - j * p.B;
-        blk = __ldg(p.block_table + walk.b * p.bt_stride + j);
+        blk = __ldg(table + j);
       }
     };
     // The next job.  Tokens that are not to be read load the query's first
@@ -814,17 +1008,17 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
       next_job = job;
       next_cnt = cnt;
       next_seg = seg;
-      next_first = kt == walk.kv0;
+      next_first = first;
       const bool v = job >= 4;
       if (quad) {
         bad = blk < 0 || blk >= p.num_blocks;
-        const bool in = pos < walk.s.L;
+        const bool in = pos < len;
         if (!bad) {
           const uint8_t* page =
               (v ? p.side[1] : p.side[0]) + blk * p.page_stride;
-          data = page + walk.h * p.dhs + off * p.dts;
+          data = page + data_h + off * p.dts;
           // swizzled: row off % 4 of the band, other lanes' scales too
-          scales = page + p.scale_off + walk.h * p.shs + off * p.sts;
+          scales = page + scale_h + off * p.sts;
           next_in = in;
         } else if (in && !v) {
           flag(p.dev_error, KVQ_DEVERR_BLOCK);
@@ -836,10 +1030,17 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
         if (job >= 8) {
           job -= 8;
           ++cnt;
-          if (++kt == walk.kv1) {
-            more = walk.next(p);
-            kt = walk.kv0;
+          first = false;
+          if (++kt == kv1) {
+            more = advance(p, walk);
+            first = true;
             ++seg;
+            kt = walk->kv0;
+            kv1 = walk->kv1;
+            len = walk->s.L;
+            table = p.block_table + walk->b * p.bt_stride;
+            data_h = walk->h * p.dhs;
+            scale_h = p.scale_off + walk->h * p.shs;
           }
         }
         look_up();
@@ -880,12 +1081,12 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
       const uint32_t mask = next_mask, cur = next_cnt, cur_seg = next_seg;
       const bool first = next_first;
       step();
-      if (!warp_wait(is_v ? v_empty(stage) : k_empty(stage), phase ^ 1,
+      if (!warp_wait(bar((is_v ? kVEmpty : kKEmpty) + stage), phase ^ 1,
                      abort))
         goto done;
       if (!is_v && lane == 0)
         reinterpret_cast<volatile uint32_t*>(
-            smem + L::kValid)[(cur & 7) * 4 + quarter] = mask;
+            smem + kValidAt)[(cur & 7) * 4 + quarter] = mask;
       // this quarter's list of NaN places for the segment four ahead (its
       // last user, four back, is done: see kNan)
       if (is_v && first && lane < 8)
@@ -899,21 +1100,13 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
       if (is_v && (nan_bytes(lo) | nan_bytes(hi)) != 0u) {
         // 0 * NaN would reach rows that do not see the token: its place goes
         // on the list, zeros into the tile
-        uint32_t w[2] = {lo, hi};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int sh = 8 * (j >> 1);
-          if (((w[j & 1] >> sh) & 0x7Fu) == 0x7Fu) {
-            atomicMin(nan_at + (cur_seg & 7) * 32 + 4 * j + quarter, cur_pos);
-            w[j & 1] &= ~(0xFFu << sh);
-          }
-        }
-        lo = w[0];
-        hi = w[1];
+        lo = drop_nan(lo, nan_at + (cur_seg & 7) * 32 + quarter, cur_pos);
+        hi = drop_nan(hi, nan_at + (cur_seg & 7) * 32 + 4 + quarter, cur_pos);
       }
-      const uint32_t dst = base + (is_v ? L::kV : L::kK) + stage * kTile +
-                           (32 * quarter + lane) * 128;
-      const uint32_t sw = lane & 7;
+      // (a row is 128-byte aligned: its swizzled chunks by XOR)
+      const uint32_t dst =
+          (base + (is_v ? kVAt : kKAt) + stage * kTile +
+           (32 * quarter + lane) * 128) | ((lane & 7) << 4);
       load_scales();
 #pragma unroll
       for (int g = 0; g < 4; ++g) {  // groups 2g, 2g + 1
@@ -927,94 +1120,146 @@ __global__ void __launch_bounds__(kThreadsOf<kTiles>, 1)
           uint32_t o[4];
           dequant_word(w[i], i < 2 ? se : so, o);
           const int ch = 4 * g + i;  // 16-byte chunk of the row
-          sts128(dst + (ch >> 3) * kHalf + (((ch & 7) ^ sw) << 4), o);
+          sts128((dst ^ ((ch & 7) << 4)) + (ch >> 3) * kHalf, o);
         }
         load(g);  // the next job's bytes into the registers just used
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(is_v ? v_full(stage) : k_full(stage));
+      if (lane == 0) mbar_arrive(bar((is_v ? kVFull : kKFull) + stage));
     }
-  } else if (warp == 4 * kTiles && any) {
-    // --- products: the warp waits, one lane issues ---------------------------
-    uint32_t cnt = 0;  // KV tiles
-    uint32_t q_phase[kTiles] = {}, p_phase[kTiles] = {};
-    auto qk = [&](int m, uint32_t n, bool last) {
-      const uint32_t q = desc_lo<16>(base + L::kQ + m * kTile);
-      const uint32_t k = desc_lo<16>(base + L::kK + (n & 1) * kTile);
-      if (elect()) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t at = ((i >> 2) * kHalf + (i & 3) * 32) >> 4;
-          mma_ss(tmem + 128 * m, q + at, k + at, kIdesc, i > 0);
-        }
-        mma_commit(s_full(m));
-        if (last) mma_commit(k_empty(n & 1));
-      }
-      __syncwarp();
-    };
+  } else if (warp >= kSoftWarps && any) {
+    // --- products of slot m: the warp waits, one lane issues -----------------
+    // In order: logits of the slot's first tile, then its output with a tile
+    // and its logits of the next one, so that the tensor cores work for this
+    // slot while the other's weights come.  Both slots release a stage of K
+    // or V; where they share one query tile, the slot that used it does so
+    // twice.
+    const int m = warp - kSoftWarps;
+    uint32_t cnt = 0;                    // KV tiles before this segment
+    uint32_t q1 = 0, p_cnt = 0;          // phases of query 1, of the weights
+    uint32_t segs = 0, turns = 0;
     bool go = true;
     while (go) {
-      const int T = kTiles == 2 && uniform(walk.rows) > 128 ? 2 : 1;
-      const int n = uniform(walk.kv1 - walk.kv0);
-      if (!warp_wait(k_full(cnt & 1), (cnt >> 1) & 1, abort)) goto done;
-      for (int m = 0; m < T; ++m) {
-        if (!warp_wait(q_full(m), q_phase[m] & 1, abort)) goto done;
-        ++q_phase[m];
-        fence_after();
-        qk(m, cnt, m == T - 1);
-      }
-      for (int j = 0; j < n; ++j, ++cnt) {
-        for (int m = 0; m < T; ++m) {
-          if (m == 0 && !warp_wait(v_full(cnt & 1), (cnt >> 1) & 1, abort))
+      const bool two = uniform(walk->weight) == 2;
+      const int n = uniform(walk->kv1 - walk->kv0);
+      const int step = two ? 1 : 2, first = two ? 0 : m;
+      const int q = two ? m : 0;
+      // Both warps wait for slot 0's query, whether they use it or not: once
+      // it is there, slot 0 is done with the last segment, and every tile of
+      // it has come and gone.  Without that, a warp that had no tile in a
+      // segment could run two phases ahead of a barrier, and take the phase
+      // before the last for the one that it waits for.
+      if (!warp_wait(bar(kQFull), segs & 1, abort)) goto done;
+      if (q == 1 && !warp_wait(bar(kQFull + 1), q1 & 1, abort)) goto done;
+      // product i - step with V, then the logits of tile i: everything is
+      // waited for first, then the batch is issued in one go
+#pragma unroll 1
+      for (int i = first; i < n + step; i += step) {
+        const bool pv = i >= first + step, qk = i < n;
+        const uint32_t tv = cnt + i - step, tk = cnt + i;  // their tiles
+        // (the weights last: they come last, and every test on the way from
+        // them to the products would add to the slot's round)
+        if (pv && !warp_wait(bar(kVFull + (tv & 1)), (tv >> 1) & 1, abort))
+          goto done;
+        if (qk && !warp_wait(bar(kKFull + (tk & 1)), (tk >> 1) & 1, abort))
+          goto done;
+        // Two query tiles take turns: batches that ran side by side would
+        // end side by side, and leave the tensor cores idle while both
+        // slots make their weights.
+        if (two && pv) {
+          if (turns + m > 0 &&
+              !warp_wait(bar(kTurn + m), (turns + m - 1) & 1, abort))
             goto done;
-          if (!warp_wait(p_full(m), p_phase[m] & 1, abort)) goto done;
-          ++p_phase[m];
-          fence_after();
-          const uint32_t v =
-              desc_lo<kHalf>(base + L::kV + (cnt & 1) * kTile);
-          if (elect()) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              mma_ts(tmem + 128 * kTiles + 128 * m, tmem + 128 * m + 8 * i,
-                     v + i * (2048 >> 4), kIdescBmn, j > 0 || i > 0);
-            mma_commit(o_done(m));
-            if (m == T - 1) mma_commit(v_empty(cnt & 1));
+          ++turns;
+        }
+        const uint32_t a = desc_lo<16>(base + kQAt + q * kTile);
+        const uint32_t k = desc_lo<16>(base + kKAt + (tk & 1) * kTile);
+        const uint32_t v = desc_lo<kHalf>(base + kVAt + (tv & 1) * kTile);
+        const uint32_t s_at = tmem + 128 * m, o_at = s_at + kOCol;
+        if (pv) {
+          // the output's columns are free once the last segment's are read
+          if (i == first + step && segs > 0) {
+            if (!warp_wait(bar(kPFull + m), p_cnt & 1, abort)) goto done;
+            if (!warp_wait(bar(kOFree), (segs - 1) & 1, abort)) goto done;
           }
-          __syncwarp();
-          if (j + 1 < n) {
-            if (m == 0 && !warp_wait(k_full((cnt + 1) & 1),
-                                     ((cnt + 1) >> 1) & 1, abort))
-              goto done;
-            fence_after();
-            qk(m, cnt + 1, m == T - 1);
+          if (!warp_wait(bar(kPFull + m), p_cnt & 1, abort)) goto done;
+          ++p_cnt;
+        }
+        fence_after();
+        if (elect()) {
+          if (pv) {
+            mma_ts(o_at, s_at, v, kIdescBmn, i > first + step);
+#pragma unroll
+            for (int x = 1; x < 8; ++x)
+              mma_ts(o_at, s_at + 8 * x, v + x * (2048 >> 4), kIdescBmn, 1);
+            mma_commit(bar(kODone + m));
+            mma_commit(bar(kVEmpty + (tv & 1)));
+            if (!two) mma_commit(bar(kVEmpty + (tv & 1)));
+            if (two && !qk) mbar_arrive(bar(kTurn + 1 - m));
+          }
+          if (qk) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const uint32_t at = ((x >> 2) * kHalf + (x & 3) * 32) >> 4;
+              mma_ss(s_at, a + at, k + at, kIdesc, x > 0);
+              // (what is left takes as long as the other warp to begin)
+              if (x == 4 && two && pv) mbar_arrive(bar(kTurn + 1 - m));
+            }
+            mma_commit(bar(kSFull + m));
+            mma_commit(bar(kKEmpty + (tk & 1)));
+            if (!two) mma_commit(bar(kKEmpty + (tk & 1)));
           }
         }
+        __syncwarp();
+        if (i == first) {
+          // while the first weights are made: the next segment (slot 0: for
+          // the softmax warps too)
+          if (m == 0 && lane == 0 && walk->kv0 == 0 && walk->kv1 < walk->W)
+            note_cut(p, *walk, units_kept[0], units_kept[1]);
+          go = advance(p, walk);
+          if (lane == 0) {
+            if (m == 0) {
+              Walk* next = ring + ((segs + 1) & 3);
+              *next = *walk;
+              next->there = go;
+            }
+            // (from both warps: no query of the next segment is announced
+            // before both have seen this one's)
+            mbar_arrive(bar(kSegment));
+          }
+          __syncwarp();
+        }
       }
-      go = walk.next(p);
+      if (two) ++q1;
+      cnt += n;
+      ++segs;
     }
   }
 done:
   __syncwarp();
   if (*abort != 0) {
+    // whoever waits for this warp's rows goes on, to its own wait that gives
+    // up
+    if (warp < kSoftWarps) bar_arrive(1 + (warp & 3), 64);
     // products in flight end by themselves; wait for them before the tensor
     // memory goes
-    if (warp == 4 * kTiles && elect()) {
-      mbar_init(bar(L::kBars), 1);
-      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      mma_commit(bar(L::kBars));
-      for (int i = 0; i < 1 << 20 && !mbar_try(bar(L::kBars), 0); ++i) {
+    if (warp == kSoftWarps || warp == kSoftWarps + 1) {
+      if (elect()) {
+        mma_commit(bar(kLast));
+        for (int i = 0; i < 1 << 20 && !mbar_try(bar(kLast), 0); ++i) {
+        }
+        flag(p.dev_error, KVQ_DEVERR_TIMEOUT);
       }
-      flag(p.dev_error, KVQ_DEVERR_TIMEOUT);
+      __syncwarp();
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
   if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(
-                     tmem),
-                 "r"(256u * kTiles));
+    asm volatile(
+        "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 // ---------------------------------------------------------------------------
@@ -1022,10 +1267,9 @@ done:
 // ---------------------------------------------------------------------------
 constexpr int kMergeRows = 32;  // rows of a CTA, four to a warp
 
-template <int kTiles, bool kF16>
+template <bool kF16>
 __global__ void __launch_bounds__(256)
     chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int kRows = 128 * kTiles;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int cta = blockIdx.x;
@@ -1042,14 +1286,14 @@ __global__ void __launch_bounds__(256)
     float top = -INFINITY;
     for (int k = 0; k <= cut.more; ++k)
       top = fmaxf(top, slot_of(p, cta + k,
-                               k == 0 ? cut.slot : 0)[kSlotRows * kD + row]);
+                               k == 0 ? cut.slot : 0)[kRows * kD + row]);
     float sum = 0.0f;
     float4 o = make_float4(0, 0, 0, 0);
     for (int k = 0; k <= cut.more; ++k) {
       const float* slot = slot_of(p, cta + k, k == 0 ? cut.slot : 0);
-      const float ref = slot[kSlotRows * kD + row];
+      const float ref = slot[kRows * kD + row];
       const float w = ref == top ? 1.0f : ex2(ref - top);
-      sum += slot[kSlotRows * (kD + 1) + row] * w;
+      sum += slot[kRows * (kD + 1) + row] * w;
       const float4 x =
           *reinterpret_cast<const float4*>(slot + row * kD + 4 * lane);
       o.x += x.x * w;
@@ -1071,22 +1315,21 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <int kTiles, bool kF16>
+template <bool kF16>
 cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
-  constexpr int kSmem = Smem<kTiles>::kBytes;
   const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<kTiles, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      kSmem);
+      chunk_kernel<kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      kSmemBytes);
   if (set != cudaSuccess) return set;
   const unsigned ctas = static_cast<unsigned>(sm_count());
   if (ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
-  const cudaError_t err =
-      launch_kernel(chunk_kernel<kTiles, kF16>, dim3(ctas),
-                    kThreadsOf<kTiles>, kSmem, stream, p.pdl, p);
+  const cudaError_t err = launch_kernel(chunk_kernel<kF16>, dim3(ctas),
+                                        kThreads, kSmemBytes, stream, p.pdl,
+                                        p);
   if (err != cudaSuccess) return err;
-  return launch_kernel(chunk_merge_kernel<kTiles, kF16>,
-                       dim3(ctas, 128 * kTiles / kMergeRows), 256, 0, stream,
-                       true, p);
+  return launch_kernel(chunk_merge_kernel<kF16>,
+                       dim3(ctas, kRows / kMergeRows), 256, 0, stream, true,
+                       p);
 }
 
 }  // namespace
@@ -1097,7 +1340,7 @@ int64_t chunk_workspace_bytes(int sms) {
 
 cudaError_t launch_chunk_attention(const ChunkParams& p,
                                    cudaStream_t stream) {
-  return p.f16 ? launch<2, true>(p, stream) : launch<2, false>(p, stream);
+  return p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
 }
 
 }  // namespace kvq

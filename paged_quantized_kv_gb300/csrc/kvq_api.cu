@@ -526,8 +526,7 @@ kvq_status kvq_chunk_attention_nvfp4(
   if (page_stride < H * B * (D / 2 + S)) return KVQ_ERR_SHAPE;
   if (query_stride0 < num_q_heads * D || out_stride0 < num_q_heads * D)
     return KVQ_ERR_SHAPE;
-  // rows of (token, head of a KV head) and token positions are 32-bit
-  if (total_q > (int64_t{1} << 26) || num_seqs > kChunkMaxSeqs)
+  if (total_q > kChunkMaxRows || num_seqs > kChunkMaxSeqs)
     return KVQ_ERR_SHAPE;
   if (total_q == 0 || num_seqs == 0) return KVQ_OK;
   if (query == nullptr || cu_q_lens == nullptr || key_cache == nullptr ||

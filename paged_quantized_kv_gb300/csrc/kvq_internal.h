@@ -194,8 +194,9 @@ struct ChunkParams {
 };
 
 constexpr int kChunkMaxSeqs = 1 << 20;
-// longest context (positions and tile counts stay in 32 bits)
-constexpr int kChunkMaxContext = 1 << 30;
+// longest context, most query rows (the schedule counts in 32 bits)
+constexpr int kChunkMaxContext = 1 << 26;
+constexpr int kChunkMaxRows = 1 << 25;
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t stream);
 // Workspace bytes of a call on a device of `sms` multiprocessors.
