@@ -19,7 +19,7 @@ constexpr int kKeys = 128;                 // tokens of a KV tile
 constexpr int kHalf = 128 * 128;           // bytes of half a tile (64 dims)
 constexpr int kTile = 2 * kHalf;           // a [128 x 128] fp16 tile
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLag = 8.0f;               // see the softmax
+constexpr float kMost = 32768.0f;          // see the softmax
 
 // ---------------------------------------------------------------------------
 // tcgen05 helpers
@@ -805,51 +805,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kt = kt0; kt < kv1; kt += step, ++cnt) {
         if (!warp_wait(bar(kSFull + m), cnt & 1, abort)) goto done;
         fence_after();
-        const uint4 valid = *reinterpret_cast<const uint4*>(
-            smem + kValidAt + ((tiles + kt) & 7) * 16);
+        // Weights are exp2 of the scaled logits minus a reference: the
+        // maximum of the first tile.  Later tiles do without their maximum:
+        // as long as a row's weights sum up to less than kMost, none is out
+        // of fp16's range.  Where that fails the tile is done over, with the
+        // maximum for the new reference.
+        bool look = kt == kt0;
         uint32_t s[128];
-        tmem_ld32(s_col, s);
-        tmem_ld32(s_col + 32, s + 32);
-        tmem_wait_ld();
-        tmem_ld32(s_col + 64, s + 64);
-        tmem_ld32(s_col + 96, s + 96);
-        float top = max64(s);
-        tmem_wait_ld();
-        top = fmaxf(top, max64(s + 64)) * c;
-        // (looked at only now: the products keep shared memory busy, and
-        // what is read from it comes late)
-        const int lim = pos - kt * kKeys;  // the row sees columns 0 .. lim
-        const bool all = lim >= kKeys - 1 &&
-                         (valid.x & valid.y & valid.z & valid.w) == ~0u;
-        if (!__all_sync(0xFFFFFFFFu, all)) {
-          mask32(s, valid.x & first_bits(lim));
-          mask32(s + 32, valid.y & first_bits(lim - 32));
-          mask32(s + 64, valid.z & first_bits(lim - 64));
-          mask32(s + 96, valid.w & first_bits(lim - 96));
-          top = fmaxf(max64(s), max64(s + 64)) * c;
-        }
-        // The reference follows the maximum only when it lags by more than
-        // kLag, so weights stay below 2^kLag and few tiles rescale.
-        const bool move = top > ref + kLag;
-        if (__any_sync(0xFFFFFFFFu, move)) {
-          const float f = move ? ex2(ref - top) : 1.0f;
-          if (move) {
-            ref = top;
+        float ts;
+        for (;;) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32(s_col + 32 * k, s + 32 * k);
+          tmem_wait_ld();
+          // (looked at only now: the products keep shared memory busy, and
+          // what is read from it comes late)
+          const uint4 valid = *reinterpret_cast<const uint4*>(
+              smem + kValidAt + ((tiles + kt) & 7) * 16);
+          const int lim = pos - kt * kKeys;  // the row sees columns 0 .. lim
+          const bool all = lim >= kKeys - 1 &&
+                           (valid.x & valid.y & valid.z & valid.w) == ~0u;
+          if (!__all_sync(0xFFFFFFFFu, all)) {
+            mask32(s, valid.x & first_bits(lim));
+            mask32(s + 32, valid.y & first_bits(lim - 32));
+            mask32(s + 64, valid.z & first_bits(lim - 64));
+            mask32(s + 96, valid.w & first_bits(lim - 96));
+          }
+          if (look) {
+            const float top = fmaxf(max64(s), max64(s + 64)) * c;
+            const float f = top > ref ? ex2(ref - top) : 1.0f;
+            ref = fmaxf(ref, top);
             sum *= f;
+            if (kt > kt0) {
+              if (!warp_spin(bar(kODone + m), (cnt - 1) & 1, abort))
+                goto done;
+              fence_after();
+              rescale(o_col, f);
+            }
           }
-          if (kt > kt0) {
-            if (!warp_spin(bar(kODone + m), (cnt - 1) & 1, abort)) goto done;
-            fence_after();
-            rescale(o_col, f);
-          }
-        }
-        const float low = ref == -INFINITY ? 0.0f : ref;
-        const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
-        uint64_t add[2] = {0, 0};
+          const float low = ref == -INFINITY ? 0.0f : ref;
+          const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
+          uint64_t add[2] = {0, 0};
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-#pragma unroll
-          for (int k = 64 * half; k < 64 * half + 64; k += 2) {
+          for (int k = 0; k < 128; k += 2) {
             float a, b;
             unpack2(fma2(pack2(__uint_as_float(s[k]),
                                __uint_as_float(s[k + 1])), cc, ll), a, b);
@@ -858,15 +855,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             add[(k >> 1) & 1] = add2(add[(k >> 1) & 1], pack2(a, b));
             s[k >> 1] = pack_f16x2(a, b);
           }
-          tmem_st32(s_col + 32 * half, s + 32 * half);
+          float e, o;
+          unpack2(add2(add[0], add[1]), e, o);
+          ts = e + o;
+          // (a row that has seen nothing has no reference yet)
+          const bool again = !(ts < kMost) || ref == -INFINITY;
+          if (look || !__any_sync(0xFFFFFFFFu, again)) break;
+          look = true;
         }
+        tmem_st32(s_col, s);
+        tmem_st32(s_col + 32, s + 32);
+        sum += ts;
         tmem_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kPFull + m));
-        float e, o;
-        unpack2(add2(add[0], add[1]), e, o);
-        sum += e + o;
       }
       // --- epilogue ---------------------------------------------------------------
       const int n = kv1 - kv0;
