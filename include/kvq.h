@@ -444,8 +444,9 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  * Arithmetic: as for kvq_paged_attention_nvfp4 (query rounded to fp16,
  * e2m1 * sf exact in fp16, products accumulated in fp32 on the tensor
  * cores, weights rounded to fp16 against a running reference, fp32 sums and
- * merges, out rounded once), except that the denominator sums the weights
- * before they are rounded.
+ * merges, out rounded once), except that for longer chunks the denominator
+ * sums the weights before they are rounded, and the reference may lag behind
+ * the maximum by up to 15 (in log2).
  *
  * query          bf16 / fp16 (dtype) [total_q, num_q_heads, 128], rows
  *                query_stride0 elements apart (multiple of 8), 16-byte
@@ -455,16 +456,21 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  *                flagged KVQ_DEVERR_SEQ).  Rows that no sequence covers
  *                (behind cu_q_lens[num_seqs]) are not read, and their
  *                output is left as it was.
- * max_q_len      the longest chunk of the batch, as known on the host.
- *                Chooses the tile shape only: a wrong value costs time.
+ * max_q_len      the longest chunk of the batch, as known on the host (a
+ *                larger value costs time; a smaller one may leave the rows
+ *                of longer chunks unwritten, flagged KVQ_DEVERR_SEQ).
  * head_size      128.   num_q_heads / num_kv_heads <= 16 (and divides),
  *                num_q_heads <= 1024.
  * key_cache, value_cache, page_stride, block_size, num_blocks, layout,
  * block_table, block_table_stride, max_blocks_per_seq, k_scale, v_scale,
  * scale          as for kvq_paged_attention_nvfp4.
- * context_lens   int32 [num_seqs]; values above max_blocks_per_seq *
- *                block_size (or 2^26) are clamped to it and flagged
- *                (KVQ_DEVERR_SEQ), negative ones count as 0.
+ * context_lens   int32 [num_seqs]; values above min(max_context_len,
+ *                max_blocks_per_seq * block_size, 2^26) are clamped to it
+ *                and flagged (KVQ_DEVERR_SEQ), negative ones count as 0.
+ * max_context_len  the batch's longest context, as known on the host, or 0
+ *                for the block table's width.  Sizes the launch for chunks
+ *                of a few tokens (as for kvq_paged_attention_nvfp4: a loose
+ *                bound costs time).
  * workspace      workspace_bytes of device memory, 16-byte aligned; at
  *                least kvq_chunk_attention_workspace_bytes() (the same for
  *                every call on a device), else KVQ_ERR_SCRATCH.  Nothing in
@@ -486,7 +492,8 @@ kvq_status kvq_chunk_attention_nvfp4(
     int32_t block_size, int64_t num_blocks, int32_t layout,
     const int32_t* block_table, int64_t block_table_stride,
     int32_t max_blocks_per_seq, const int32_t* context_lens,
-    const float* k_scale, const float* v_scale, float scale, void* workspace,
+    int32_t max_context_len, const float* k_scale, const float* v_scale,
+    float scale, void* workspace,
     int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
     int32_t* dev_error, void* stream);
 

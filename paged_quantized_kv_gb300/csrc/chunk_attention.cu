@@ -392,6 +392,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
   s.q0 = min(max(__ldg(p.cu + b), 0), total);
   s.n = min(max(__ldg(p.cu + b + 1), s.q0), total) - s.q0;
   s.L = min(max(__ldg(p.lens + b), 0), p.len_cap);
+  if (s.n <= p.skip) s.n = 0;
   return s;
 }
 
@@ -679,10 +680,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (; k.left > 0; k.next()) units += k.units();
         }
         units *= p.Hkv;
-        if (r < rounds && blockIdx.x == 0 &&
-            (s.q0 != __ldg(p.cu + b) || s.q0 + s.n != __ldg(p.cu + b + 1) ||
-             __ldg(p.lens + b) > s.L))
-          flag(p.dev_error, KVQ_DEVERR_SEQ);
+        if (r < rounds && blockIdx.x == 0) {
+          const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
+          if (c0 < 0 || c1 < c0 || c1 > p.total_q ||
+              __ldg(p.lens + b) > p.len_cap)
+            flag(p.dev_error, KVQ_DEVERR_SEQ);
+        }
       }
       int64_t x = units;
 #pragma unroll
@@ -1341,9 +1344,73 @@ int64_t chunk_workspace_bytes(int sms) {
   return kCutBytes + static_cast<int64_t>(sms) * 2 * kSlotFloats * 4;
 }
 
-cudaError_t launch_chunk_attention(const ChunkParams& p,
+// Short chunks go token by token through the decode kernel, which walks the
+// context once for every token, but at three times the speed of a tile of
+// 128 rows that is mostly padding, and with nothing to set up.
+static int short_chunk(const ChunkParams& p) {
+  if (p.max_q_len <= 4) return p.max_q_len > 1 ? p.max_q_len : 1;
+  const bool few = static_cast<int64_t>(p.num_seqs) * p.Hkv <= sm_count();
+  return few && p.max_q_len <= 8 ? p.max_q_len : 1;
+}
+
+cudaError_t launch_chunk_attention(const ChunkParams& caller,
                                    cudaStream_t stream) {
-  return p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
+  ChunkParams p = caller;
+  p.skip = short_chunk(p);
+  // the decode kernel's scratch: output, sum and maximum of each stretch
+  constexpr int kPart = 512;
+  const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.skip;
+  const int64_t parts = (static_cast<int64_t>(p.len_cap) + kPart - 1) / kPart;
+  const int64_t cells = rows * p.Hq * parts;
+  if (rows * p.Hkv * (parts > 0 ? parts : 1) >= INT32_MAX ||
+      (parts > 1 && cells * (kD + 2) * 4 > chunk_workspace_bytes(sm_count())))
+    p.skip = 0;
+  cudaError_t err = cudaSuccess;
+  const bool tiles = p.max_q_len > p.skip;
+  if (tiles)
+    err = p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
+  if (err != cudaSuccess || p.skip == 0) return err;
+  AttnParams a{};
+  a.q = p.q;
+  a.q_stride0 = p.q_stride0;
+  a.side[0] = p.side[0];
+  a.side[1] = p.side[1];
+  a.page_stride = p.page_stride;
+  a.num_blocks = p.num_blocks;
+  a.scale_off = p.scale_off;
+  a.dhs = p.dhs;
+  a.dts = p.dts;
+  a.shs = p.shs;
+  a.sts = p.sts;
+  a.block_table = p.block_table;
+  a.bt_stride = p.bt_stride;
+  a.lens = p.lens;
+  a.k_scale = p.k_scale;
+  a.v_scale = p.v_scale;
+  a.scale = p.scale;
+  a.tmp_out = reinterpret_cast<float*>(p.workspace);
+  a.exp_sums = a.tmp_out + cells * kD;
+  a.max_logits = a.exp_sums + cells;
+  a.out = p.out;
+  a.out_stride0 = p.out_stride0;
+  a.dev_error = p.dev_error;
+  a.num_seqs = static_cast<int32_t>(rows);
+  a.Hq = p.Hq;
+  a.Hkv = p.Hkv;
+  a.G = p.G;
+  a.B = p.B;
+  a.b_shift = p.b_shift;
+  a.part = kPart;
+  a.max_parts = static_cast<int32_t>(parts > 0 ? parts : 1);
+  a.len_cap = p.len_cap;
+  a.swizzle_k = p.swizzle_k;
+  a.f16 = p.f16;
+  a.pdl = tiles || p.pdl;
+  a.cu = p.cu;
+  a.total_q = p.total_q;
+  a.per_seq = p.skip;
+  a.only_short = !tiles;
+  return launch_paged_attention_mma(a, stream);
 }
 
 }  // namespace kvq

@@ -500,7 +500,8 @@ kvq_status kvq_chunk_attention_nvfp4(
     int32_t block_size, int64_t num_blocks, int32_t layout,
     const int32_t* block_table, int64_t block_table_stride,
     int32_t max_blocks_per_seq, const int32_t* context_lens,
-    const float* k_scale, const float* v_scale, float scale, void* workspace,
+    int32_t max_context_len, const float* k_scale, const float* v_scale,
+    float scale, void* workspace,
     int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
     int32_t* dev_error, void* stream) {
   using namespace kvq;
@@ -510,7 +511,8 @@ kvq_status kvq_chunk_attention_nvfp4(
   if ((flags & ~static_cast<uint32_t>(KVQ_F_SWIZZLE_K_SCALE | KVQ_F_PDL)) !=
       0u)
     return KVQ_ERR_ARG;
-  if (total_q < 0 || num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 ||
+  if (total_q < 0 || num_seqs < 0 || max_q_len < 0 || max_context_len < 0 ||
+      num_q_heads <= 0 ||
       num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 ||
       num_blocks < 0 || max_blocks_per_seq < 0 ||
       block_table_stride < max_blocks_per_seq)
@@ -583,7 +585,9 @@ kvq_status kvq_chunk_attention_nvfp4(
   p.b_shift = ilog2_exact(B);
   p.max_q_len = max_q_len;
   p.len_cap = static_cast<int32_t>(std::min<int64_t>(
-      static_cast<int64_t>(max_blocks_per_seq) * B, kChunkMaxContext));
+      std::min<int64_t>(static_cast<int64_t>(max_blocks_per_seq) * B,
+                        kChunkMaxContext),
+      max_context_len > 0 ? max_context_len : kChunkMaxContext));
   p.swizzle_k = (flags & KVQ_F_SWIZZLE_K_SCALE) != 0u;
   p.f16 = dtype == KVQ_DTYPE_FP16;
   p.pdl = (flags & KVQ_F_PDL) != 0u;

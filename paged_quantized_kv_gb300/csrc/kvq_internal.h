@@ -144,6 +144,13 @@ struct AttnParams {
   bool f16;                // query / out are fp16 (else bf16)
   bool pdl;
   bool early_meta;         // lengths, block ids, query read before the wait
+  // Short chunks (kvq_chunk_attention_nvfp4; cu == nullptr otherwise): row
+  // b of num_seqs is new token b % per_seq of sequence b / per_seq, if that
+  // one has at most per_seq of them; its context ends with the token.
+  const int32_t* cu;       // cu_q_lens
+  int64_t total_q;
+  int32_t per_seq;
+  bool only_short;         // a longer chunk is an error
 };
 
 cudaError_t launch_paged_attention_mma(const AttnParams& p,
@@ -187,7 +194,8 @@ struct ChunkParams {
   int64_t total_q;
   int32_t num_seqs, Hq, Hkv, G, B, b_shift;
   int32_t max_q_len;
-  int32_t len_cap;         // max_blocks * B
+  int32_t len_cap;         // min(max_context_len, max_blocks * B)
+  int32_t skip;            // chunks of up to this many tokens are left out
   bool swizzle_k;
   bool f16;
   bool pdl;

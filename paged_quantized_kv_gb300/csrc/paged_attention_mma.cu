@@ -182,6 +182,48 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 
 // ---------------------------------------------------------------------------
+// Rows
+// ---------------------------------------------------------------------------
+// Row b of a launch: its query and output row, its sequence (block-table
+// row) and its context length.  A decode step's row b is sequence b.  With
+// p.cu it is new token b % per_seq of sequence b / per_seq, which sees the
+// context up to itself; a token that the sequence does not have, or whose
+// sequence has more than per_seq of them, is none (live false).
+struct Row {
+  int64_t q;
+  int seq, L;
+  bool live, bad;  // bad: lengths or offsets out of range
+};
+
+__device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
+  Row r = {b, b, 0, true, false};
+  if (p.cu == nullptr) {
+    r.L = __ldg(p.lens + b);
+    r.bad = r.L < 0 || r.L > p.len_cap;
+    r.L = max(0, min(r.L, p.len_cap));
+    return r;
+  }
+  r.seq = b / p.per_seq;
+  const int i = b - r.seq * p.per_seq;
+  const int c0 = __ldg(p.cu + r.seq), c1 = __ldg(p.cu + r.seq + 1);
+  const int len = __ldg(p.lens + r.seq);
+  const int total = static_cast<int>(p.total_q);
+  const int q0 = min(max(c0, 0), total);
+  const int n = min(max(c1, q0), total) - q0;
+  r.bad = i == 0 && (q0 != c0 || q0 + n != c1 || len > p.len_cap ||
+                     (p.only_short && n > p.per_seq));
+  r.live = i < n && n <= p.per_seq;
+  r.q = q0 + i;
+  r.L = max(0, max(0, min(len, p.len_cap)) - n + i + 1);
+  return r;
+}
+
+// Whether a row has weights: a row of a chunk whose weights are NaN has.
+__device__ __forceinline__ bool has_weights(const AttnParams& p, float den) {
+  return den > 0.f || (p.cu != nullptr && den != den);
+}
+
+// ---------------------------------------------------------------------------
 // Small device helpers
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -385,6 +427,8 @@ constexpr float kLazy = 8.0f;
 // bands); 9, 10 = 1, 3 with block_size 8 (linear K scales): 8-token piece
 // j of step i is block 4i + j, and a stretch is kPartB8 tokens long, so
 // that a warp's range spans at most 64 blocks.
+// Chunks of a few new tokens run here too (p.cu set), each token as a row of
+// its own: see row_of.
 template <int NG, bool kF16, int kPages>
 __global__ void __launch_bounds__(kThreads, NG == 8 ? 4 : 3)
 paged_attention_mma_kernel(const AttnParams p) {
@@ -414,9 +458,9 @@ paged_attention_mma_kernel(const AttnParams p) {
   const bool early = p.early_meta;
   if (!early) pdl_prologue();
 
-  int L = __ldg(p.lens + b);
-  const bool bad_len = L < 0 || L > p.len_cap;
-  if (bad_len) L = L < 0 ? 0 : p.len_cap;
+  const Row me = row_of(p, b);
+  const int L = me.L;
+  const bool bad_len = me.bad;
   // flags a clamped length (once per sequence); a write, so after the wait
   auto flag_len = [&]() {
     if (bad_len && p.dev_error != nullptr && part == 0 && kh == 0 &&
@@ -426,12 +470,12 @@ paged_attention_mma_kernel(const AttnParams p) {
   // stretch length: fixed on contiguous pages (the host sets p.part to it)
   const int S = kB8 ? kPartB8 : kContig ? KVQ_ATTN_MMA_PART : p.part;
   const int nparts = (L + S - 1) / S;
-  if (part >= nparts) {
+  if (part >= nparts || !me.live) {
     if (early) pdl_prologue();
     flag_len();
-    if (part == 0) {  // empty context: the output is zero
+    if (part == 0 && me.live) {  // empty context: the output is zero
       for (int i = tid; i < p.G * kD; i += kThreads)
-        p.out[b * p.out_stride0 + (kh * p.G) * kD + i] = 0;
+        p.out[me.q * p.out_stride0 + (kh * p.G) * kD + i] = 0;
     }
     return;
   }
@@ -472,7 +516,7 @@ paged_attention_mma_kernel(const AttnParams p) {
   bool lane_in = false, hi_in = false;  // the block holds tokens of the range
   if (nsteps > 0) {
     const int e1 = p.b_shift >= 0 ? ((w1 - 1) >> p.b_shift) : (w1 - 1) / p.B;
-    const int32_t* row = p.block_table + b * p.bt_stride;
+    const int32_t* row = p.block_table + me.seq * p.bt_stride;
     lane_in = e0 + lane <= e1;
     if (lane_in) bt_lane = __ldg(row + e0 + lane);
     if constexpr (kContig) {
@@ -502,7 +546,7 @@ paged_attention_mma_kernel(const AttnParams p) {
     qv[n] = make_uint4(0u, 0u, 0u, 0u);
     if (8 * n + g < p.G)
       qv[n] = __ldg(reinterpret_cast<const uint4*>(
-          p.q + b * p.q_stride0 + (kh * p.G + 8 * n + g) * kD + 32 * t +
+          p.q + me.q * p.q_stride0 + (kh * p.G + 8 * n + g) * kD + 32 * t +
           8 * warp));
   }
   const float v_scale_in = tid == 0 ? __ldg(p.v_scale) : 0.f;
@@ -1110,7 +1154,8 @@ paged_attention_mma_kernel(const AttnParams p) {
       fw[w] = ex2(mw[w] - M);
       den += wbuf[w][16 * kMergeRow + 16 + hh] * fw[w];
     }
-    const float inv = den > 0.f ? 1.0f / den : 0.f;
+    const bool live = has_weights(p, den);
+    const float inv = live ? 1.0f / den : 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
@@ -1129,12 +1174,12 @@ paged_attention_mma_kernel(const AttnParams p) {
     const int da = 4 * k, dc = 64 + 4 * (k ^ 1);
     if (nparts == 1) {
       auto pack = [&](float lo, float hi) -> uint32_t {
-        const float ylo = den > 0.f ? lo * inv * v_scale : 0.f;
-        const float yhi = den > 0.f ? hi * inv * v_scale : 0.f;
+        const float ylo = live ? lo * inv * v_scale : 0.f;
+        const float yhi = live ? hi * inv * v_scale : 0.f;
         return static_cast<uint32_t>(float_to_out<kF16>(ylo)) |
                (static_cast<uint32_t>(float_to_out<kF16>(yhi)) << 16);
       };
-      uint16_t* orow = p.out + b * p.out_stride0 + (kh * p.G + hh) * kD;
+      uint16_t* orow = p.out + me.q * p.out_stride0 + (kh * p.G + hh) * kD;
       *reinterpret_cast<uint2*>(orow + da) =
           make_uint2(pack(a.x, a.y), pack(a.z, a.w));
       *reinterpret_cast<uint2*>(orow + dc) =
@@ -1143,8 +1188,7 @@ paged_attention_mma_kernel(const AttnParams p) {
       const int64_t rr =
           (static_cast<int64_t>(b) * p.Hq + kh * p.G + hh) * p.max_parts +
           part;
-      const float s = den > 0.f ? inv : 0.f;
-      const bool live = den > 0.f;
+      const float s = inv;
       float* trow = p.tmp_out + rr * kD;
       *reinterpret_cast<float4*>(trow + da) =
           live ? make_float4(a.x * s, a.y * s, a.z * s, a.w * s)
@@ -1183,9 +1227,9 @@ attention_merge_kernel(const AttnParams p) {
   const int b = live ? static_cast<int>(row / p.Hq) : 0;
   const int h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.Hq)
                      : 0;
-  int L = live ? __ldg(p.lens + b) : 0;
+  const Row me = live ? row_of(p, b) : Row{0, 0, 0, false, false};
   pdl_prologue();
-  L = L < 0 ? 0 : (L > p.len_cap ? p.len_cap : L);
+  const int L = me.live ? me.L : 0;
   const int nparts = (L + p.part - 1) / p.part;
   if (!live || nparts <= 1) return;
   const int64_t row0 = row * p.max_parts;
@@ -1228,17 +1272,18 @@ attention_merge_kernel(const AttnParams p) {
           src[1]);
     }
   }
-  const float f = den > 0.f ? 1.0f / den : 0.f;
+  const bool some = has_weights(p, den);
+  const float f = some ? 1.0f / den : 0.f;
   const float vs = __ldg(p.v_scale);
   uint32_t packed[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const float y0 = den > 0.f ? acc[2 * k] * f * vs : 0.f;
-    const float y1 = den > 0.f ? acc[2 * k + 1] * f * vs : 0.f;
+    const float y0 = some ? acc[2 * k] * f * vs : 0.f;
+    const float y1 = some ? acc[2 * k + 1] * f * vs : 0.f;
     packed[k] = static_cast<uint32_t>(float_to_out<kF16>(y0)) |
                 (static_cast<uint32_t>(float_to_out<kF16>(y1)) << 16);
   }
-  *reinterpret_cast<uint4*>(p.out + b * p.out_stride0 + h * kD + 8 * sub) =
+  *reinterpret_cast<uint4*>(p.out + me.q * p.out_stride0 + h * kD + 8 * sub) =
       make_uint4(packed[0], packed[1], packed[2], packed[3]);
 }
 

@@ -126,8 +126,8 @@ def lib() -> ctypes.CDLL:
         L.kvq_chunk_attention_nvfp4.argtypes = [
             P, c.c_int64, c.c_int32, c.c_int64, c.c_int32, P, c.c_int32,
             c.c_int32, c.c_int32, c.c_int32, P, P, c.c_int64, c.c_int32,
-            c.c_int64, c.c_int32, P, c.c_int64, c.c_int32, P, P, P,
-            c.c_float, P, c.c_int64, P, c.c_int64, c.c_uint32, P, P]
+            c.c_int64, c.c_int32, P, c.c_int64, c.c_int32, P, c.c_int32, P,
+            P, c.c_float, P, c.c_int64, P, c.c_int64, c.c_uint32, P, P]
         L.kvq_chunk_attention_nvfp4.restype = c.c_int
         L.kvq_chunk_attention_workspace_bytes.argtypes = []
         L.kvq_chunk_attention_workspace_bytes.restype = c.c_int64
@@ -485,7 +485,7 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
                               scale: float, out: torch.Tensor,
                               max_q_len: int,
                               workspace: torch.Tensor | None = None,
-                              flags: int = 0,
+                              max_context_len: int = 0, flags: int = 0,
                               dev_error: torch.Tensor | None = None,
                               stream: int | None = None) -> None:
     """Causal attention of chunks of new tokens over the NVFP4 cache (see
@@ -496,9 +496,9 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     the last of its context_lens[b] cached tokens.  key_cache / value_cache:
     the store's 4-D page views; block_table int32 [num_seqs, max_blocks];
     cu_q_lens int32 [num_seqs + 1]; context_lens int32 [num_seqs];
-    max_q_len: the longest chunk.  The workspace
-    (``chunk_attention_workspace``) is allocated here when it is not
-    given."""
+    max_q_len: the longest chunk; max_context_len: the longest context (0:
+    the block table's width).  The workspace (``chunk_attention_workspace``)
+    is allocated here when it is not given."""
     fn = "kvq_chunk_attention_nvfp4"
     dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
     if query.dtype not in dtypes or out.dtype != query.dtype:
@@ -537,8 +537,9 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
         value_cache.data_ptr(), key_cache.stride(0), key_cache.size(1),
         key_cache.size(0), layout, block_table.data_ptr(),
         block_table.stride(0) if n > 1 else block_table.size(1),
-        block_table.size(1), context_lens.data_ptr(), k_scale.data_ptr(),
-        v_scale.data_ptr(), float(scale), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        block_table.size(1), context_lens.data_ptr(), int(max_context_len),
+        k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         out.data_ptr(), out.stride(0) if total > 1 else Hq * D, int(flags),
         _ptr(dev_error), _stream_of(query) if stream is None else stream)
     _check(fn, st)

@@ -312,10 +312,40 @@ def test_ragged_batch():
     c.check(c.run())
 
 
-@pytest.mark.parametrize("max_q", [0, 1, 20, 100000])
-def test_max_q_len_is_a_hint(max_q):
+@pytest.mark.parametrize("max_q", [70, 71, 100000])
+def test_max_q_len_is_a_bound(max_q):
     c = Case([70, 1, 9], [200, 300, 40], hq=8, hkv=1, seed=17)
     c.check(c.run(max_q=max_q))
+
+
+@pytest.mark.parametrize("max_q", [0, 1, 3])
+def test_chunks_beyond_max_q_len(max_q):
+    """Flagged, their rows left as they were."""
+    c = Case([70, 1, 9], [200, 300, 40], hq=8, hkv=1, seed=17)
+    got, ref = c.run(bits=kvq.KVQ_DEVERR_SEQ, max_q=max_q), c.ref()
+    assert (got[:70] == 77.0).all() and (got[71:] == 77.0).all()
+    got[:70], got[71:] = ref[0][:70], ref[0][71:]
+    c.check(got, ref)
+
+
+@pytest.mark.parametrize("n", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (16, 1), (6, 2)])
+def test_short_chunks(n, hq, hkv):
+    """Every size around the change between the two kernels, in batches of
+    one size, and beside longer and empty ones; contexts of one stretch and
+    of several."""
+    for q, lens in (([n] * 3, [n, 700, 4000]),
+                    ([n, 0, 150, 1, n], [1900, 30, 333, 2600, max(n - 1, 0)])):
+        c = Case(q, lens, hq=hq, hkv=hkv, seed=n)
+        c.check(c.run(), what=(q, lens))
+        c.check(c.run(max_context_len=max(lens)), what=(q, lens))
+
+
+def test_context_beyond_max_context_len():
+    for n in (1, 30):
+        c = Case([n, 1], [200, 90], hq=4, hkv=1, seed=n)
+        c.check(c.run(bits=kvq.KVQ_DEVERR_SEQ, max_context_len=120),
+                c.ref(lens=[120, 90]))
 
 
 def test_same_bits_every_time():
