@@ -471,7 +471,7 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  *                for the block table's width.  Sizes the launch for chunks
  *                of a few tokens (as for kvq_paged_attention_nvfp4: a loose
  *                bound costs time).
- * workspace      workspace_bytes of device memory, 16-byte aligned; at
+ * workspace      workspace_bytes of device memory, 32-byte aligned; at
  *                least kvq_chunk_attention_workspace_bytes() (the same for
  *                every call on a device), else KVQ_ERR_SCRATCH.  Nothing in
  *                it has to be initialised; its contents afterwards are

@@ -216,6 +216,13 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
+  asm volatile(
+      "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+      "r"(v[6]), "r"(v[7])
+      : "memory");
+}
 __device__ __forceinline__ uint4 ldg128(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -372,15 +379,25 @@ __device__ __forceinline__ void rescale(uint32_t col, float f) {
 // An item is a block of up to kRows = 256 rows (token, head of the KV head)
 // of one sequence and KV head; it spans the KV tiles up to its last row's
 // position (one at least, so that rows that see nothing are written too).  It
-// counts as kItemUnits units and, for each tile, two units if it has more
-// than 128 rows, else one.  The units of all items, in the order sequence,
-// block, KV head, tile, are cut into equal shares, one per CTA; an item that
-// is cut leaves partial results, which the merge kernel joins.  A cut inside
-// a tile's two units falls behind the tile, one inside an item's own units
-// before its first tile; every share has at least kItemUnits + 2 units, so
-// that no share in the middle of an item is without a tile.
+// counts as kItemUnits units for its own (query, output: measured at some 6
+// us against 2 us for a tile, whether half of its rows are used or all) and
+// one for each tile.  The units of all items, in the order sequence, block,
+// KV head, tile, are cut into equal shares, one per CTA; an item that is cut
+// leaves partial results, which the merge kernel joins.  Every share has more
+// than kItemUnits units, so that none in the middle of an item is without a
+// tile.
+// A cut costs two partial results (a full one: 133 KB written and read
+// again).  So the end of a share within kSnap units of an item's end moves
+// there.
 constexpr int kRows = 256;
-constexpr int kItemUnits = 2;
+constexpr int kItemUnits = 3;
+constexpr int kSnap = 2;
+
+// Where a share's end at unit r of an item of `size` units falls.
+__device__ __forceinline__ int snap(int r, int size) {
+  if (min(r, size - r) > kSnap) return r;
+  return r <= size - r ? 0 : size;
+}
 
 struct Seq {
   int q0, n, L;
@@ -428,9 +445,8 @@ struct Blocks {
     const int short_by = max(kRows - left, 0) - rest;
     return max(tiles - (short_by > 0) - (short_by > step), 1);
   }
-  __device__ __forceinline__ int weight() const { return left > 128 ? 2 : 1; }
   __device__ __forceinline__ int units() const {
-    return kItemUnits + width() * weight();
+    return kItemUnits + width();
   }
 };
 
@@ -451,22 +467,20 @@ struct Walk {
   int rem, end;   // the segment's units, from the item's first one
   int64_t left;   // units of the share from here on
   Seq s;
-  int W, weight;  // tiles of the item
+  int W;          // tiles of the item
   int kv0, kv1;
+  int two;        // it has two query tiles (more than 128 rows)
   int seg, tiles;  // segments and tiles of the share before this one
   int there;       // (in the ring) this segment exists
 
-  __device__ __forceinline__ static int tile(int unit, int weight) {
-    return max(unit - kItemUnits + weight - 1, 0) / weight;
-  }
   __device__ __forceinline__ void enter(const ChunkParams& p) {
     Blocks k;
     k.begin(p, s, block);
     W = k.width();
-    weight = k.weight();
+    two = k.left > 128;
     end = static_cast<int>(min(static_cast<int64_t>(k.units()), rem + left));
-    kv0 = tile(rem, weight);
-    kv1 = tile(end, weight);
+    kv0 = max(rem - kItemUnits, 0);
+    kv1 = max(end - kItemUnits, 0);
   }
   // To the next segment that has a tile (the first one: from a position with
   // rem set and kv0 == kv1); false: there is none.
@@ -532,16 +546,18 @@ __device__ __forceinline__ float* slot_of(const ChunkParams& p, int cta,
 }
 
 // A segment that begins an item and does not end it: which CTAs go on with
-// it, up to the one whose share has the unit that its last tile begins with.
+// it.
 __device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
                                       int64_t U, int64_t share_end) {
-  const int64_t last = share_end - w.left - w.rem + kItemUnits +
-                       static_cast<int64_t>(w.W) * w.weight - w.weight;
+  const int64_t begin = share_end - w.left - w.rem;
+  const int size = kItemUnits + w.W;
   const int cta = blockIdx.x;
   int more = 0, ctas;
+  int64_t end;
   do {
     ++more;
-  } while (share_begin(U, cta + more + 1, &ctas) <= last);
+    end = share_begin(U, cta + more + 1, &ctas) - begin;
+  } while (end < size && snap(static_cast<int>(end), size) < size);
   *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
       w.b, w.block, w.h, w.seg > 0, more, {0, 0, 0}};
 }
@@ -592,7 +608,7 @@ constexpr int kValidAt = kBarAt + 8 * 22;
 constexpr int kNanAt = kValidAt + 128;
 constexpr int kMiscAt = kNanAt + 1024;   // 16 ints
 constexpr int kScanAt = kMiscAt + 64;    // 32 int64
-constexpr int kUnitsAt = kScanAt + 256;  // 3 int64: all units, share's ends
+constexpr int kUnitsAt = kScanAt + 256;  // 3 int64: all, share's end, begin
 constexpr int kSumAt = kUnitsAt + 32;    // [slot][row] floats
 constexpr int kRefAt = kSumAt + 1024;    // [slot][row] floats
 // The segments for the softmax warps ([segment % 4]; when segment s begins,
@@ -708,32 +724,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         u1 = share_begin(U, blockIdx.x + 1, &ctas);
         if (tid == 0) {
           units_kept[0] = U;
-          units_kept[1] = u1;
+          units_kept[1] = units_kept[2] = U;  // (what no sequence holds)
         }
+        __syncthreads();
       }
       // (r >= rounds - 1: u0 and u1 are known)
-      if (r >= rounds - 1 && (rounds == 1 || r >= rounds) && units > 0 &&
-          u0 < u1 && incl - units <= u0 && u0 < incl) {
-        int64_t rem = u0 - (incl - units);
+      if (r < rounds - 1 || (rounds > 1 && r < rounds) || units == 0)
+        continue;
+#pragma unroll 1
+      for (int end = 0; end < 2; ++end) {
+        const int64_t u = end ? u1 : u0;
+        if (u < incl - units || u >= incl) continue;
+        int64_t rem = u - (incl - units);
+        Walk w = {};
         Blocks k;
         k.begin(p, s, 0);
-        int i = 0;
 #pragma unroll 1
         for (; rem >= static_cast<int64_t>(k.units()) * p.Hkv; k.next()) {
           rem -= static_cast<int64_t>(k.units()) * p.Hkv;
-          ++i;
+          ++w.block;
         }
-        Walk w = {};
+        const int size = k.units();
         w.b = b;
-        w.block = i;
-        w.h = static_cast<int>(rem) / k.units();
-        w.rem = static_cast<int>(rem) - w.h * k.units();
-        w.left = u1 - u0;
+        w.h = static_cast<int>(rem) / size;
+        const int at = static_cast<int>(rem) - w.h * size;
+        w.rem = snap(at, size);
         w.s = s;
-        w.there = w.next(p, true);
-        ring[0] = w;
-        misc[2] = w.there;
+        units_kept[2 - end] = u + w.rem - at;
+        if (end == 0) ring[0] = w;
       }
+    }
+    __syncthreads();
+    if (tid == 0 && units_kept[2] < units_kept[1]) {
+      Walk w = ring[0];
+      w.left = units_kept[1] - units_kept[2];
+      w.there = w.next(p, true);
+      ring[0] = w;
+      misc[2] = w.there;
     }
   }
   fence_before();
@@ -776,16 +803,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (a row that is none sees all, so that it does not slow the others)
         pos = at < rows ? w.s.L - w.s.n + tok : INT32_MAX;
         if (m == 0 || rows > 128) {
-          // the query row, rounded to fp16, its sign folded with the scale's
-          const uint16_t* src = p.q + (w.s.q0 + tok) * p.q_stride0 +
-                                (w.h * p.G + (r - tok * p.G)) * kD;
-          const uint32_t dst = base + kQAt + m * kTile + row * 128;
+          // the query rows, rounded to fp16, their sign folded with the
+          // scale's: two rows of the warp at a time, 16 bytes per lane (a
+          // row per lane would touch 32 rows with every load)
+          const int64_t from = at < rows ? (w.s.q0 + tok) * p.q_stride0 +
+                                               (w.h * p.G + (r - tok * p.G)) *
+                                                   kD
+                                         : int64_t{-1};
           const uint32_t flip = c0 < 0.0f ? 0x80008000u : 0u;
+          const int ch = lane & 15;
           uint4 v[16];
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
+            const int64_t row_at =
+                __shfl_sync(0xFFFFFFFFu, from, 2 * g + (lane >> 4));
             v[g] = make_uint4(0, 0, 0, 0);
-            if (at < rows && c0 != 0.0f) v[g] = ldg128(src + 8 * g);
+            if (row_at >= 0 && c0 != 0.0f)
+              v[g] = ldg128(p.q + row_at + 8 * ch);
           }
 #pragma unroll
           for (int g = 0; g < 16; ++g) {
@@ -793,7 +827,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               x[k] = (kF16 ? x[k] : bf16x2_to_f16x2(x[k])) ^ flip;
-            sts128(dst + (g >> 3) * kHalf + (((g & 7) ^ (row & 7)) << 4), x);
+            const int to = (warp & 3) * 32 + 2 * g + (lane >> 4);
+            sts128(base + kQAt + m * kTile + (ch >> 3) * kHalf + to * 128 +
+                       (((ch & 7) ^ (to & 7)) << 4),
+                   x);
           }
           fence_async_smem();
           __syncwarp();
@@ -911,6 +948,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
                       (w.h * p.G + (r - tok * p.G)) * kD;
       float* part = slot + at * kD;
+      // whole 32-byte sectors (of half sectors the SM stores no more a cycle)
+      const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 &&
+                        p.out_stride0 % 16 == 0;
       // columns: the row of the slot's own output, or half a row of the two
       // slots' joined ones
 #pragma unroll 1
@@ -939,24 +979,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (at < rows && whole) {
+          uint32_t x[16];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            uint32_t x[4];
+          for (int g = 0; g < 16; ++g) {
+            const float a = __uint_as_float(o[2 * g]) * inv;
+            const float b = __uint_as_float(o[2 * g + 1]) * inv;
+            x[g] = kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+          }
+          if (wide) {
+            stg256(dst + col, x);
+            stg256(dst + col + 16, x + 8);
+          } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float a = __uint_as_float(o[8 * g + 2 * j]) * inv;
-              const float b = __uint_as_float(o[8 * g + 2 * j + 1]) * inv;
-              x[j] = kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
-            }
-            *reinterpret_cast<uint4*>(dst + col + 8 * g) =
-                make_uint4(x[0], x[1], x[2], x[3]);
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<uint4*>(dst + col + 8 * g) = make_uint4(
+                  x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]);
           }
         } else if (at < rows) {
 #pragma unroll
-          for (int g = 0; g < 8; ++g)
-            *reinterpret_cast<uint4*>(part + col + 4 * g) =
-                make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2],
-                           o[4 * g + 3]);
+          for (int g = 0; g < 4; ++g) stg256(part + col + 8 * g, o + 8 * g);
         }
       }
       if (!whole && at < rows && (two || m == 0)) {
@@ -1147,7 +1188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t segs = 0, turns = 0;
     bool go = true;
     while (go) {
-      const bool two = uniform(walk->weight) == 2;
+      const bool two = uniform(walk->two) != 0;
       const int n = uniform(walk->kv1 - walk->kv0);
       const int step = two ? 1 : 2, first = two ? 0 : m;
       const int q = two ? m : 0;

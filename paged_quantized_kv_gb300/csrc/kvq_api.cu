@@ -541,7 +541,7 @@ kvq_status kvq_chunk_attention_nvfp4(
       !aligned(value_cache, 16) || page_stride % 16 != 0 ||
       !aligned(block_table, 4) || !aligned(cu_q_lens, 4) ||
       !aligned(context_lens, 4) || !aligned(k_scale, 4) ||
-      !aligned(v_scale, 4) || !aligned(workspace, 16))
+      !aligned(v_scale, 4) || !aligned(workspace, 32))
     return KVQ_ERR_ALIGN;
   if (workspace_bytes < chunk_workspace_bytes(sm_count()))
     return KVQ_ERR_SCRATCH;
