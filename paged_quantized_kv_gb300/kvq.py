@@ -37,6 +37,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -83,6 +84,8 @@ class KvqError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libkvq.so (raises if it was not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -425,22 +428,22 @@ def kvq_paged_attention_nvfp4_noalloc(query: torch.Tensor,
     _check("kvq_paged_attention_nvfp4_noalloc", st)
 
 
-def _same_device(fn: str, *tensors) -> None:
-    """Every tensor given is on the current CUDA device (whose stream the
-    call runs on), else KVQ_ERR_ARG: a host or foreign pointer must not
-    reach a kernel."""
-    if any(t is not None and not t.is_cuda for t in tensors):
-        raise KvqError(fn, KVQ_ERR_ARG)
-    here = torch.cuda.current_device()
-    if any(t is not None and t.device.index != here for t in tensors):
-        raise KvqError(fn, KVQ_ERR_ARG)
-
-
-def _int32_vector(fn: str, *tensors) -> None:
+def _here(fn: str, *tensors) -> int:
+    """The current device's stream, once every tensor given is on that
+    device, else KVQ_ERR_ARG: a host or foreign pointer must not reach a
+    kernel.  (Raw calls: these checks are most of a small call's time.)"""
+    here = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
     for t in tensors:
-        if t.dtype != torch.int32:
+        if t is not None and (here < 0 or t.get_device() != here):
+            raise KvqError(fn, KVQ_ERR_ARG)
+    return torch._C._cuda_getCurrentRawStream(here)
+
+
+def _vector(fn: str, dtype: torch.dtype, *tensors) -> None:
+    for t in tensors:
+        if t.dtype is not dtype:
             raise KvqError(fn, KVQ_ERR_DTYPE)
-        if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
+        if t.dim() != 1 or (t.stride(0) != 1 and t.numel() > 1):
             raise KvqError(fn, KVQ_ERR_SHAPE)
 
 
@@ -510,7 +513,7 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
             or out.stride(1) != D):
         raise KvqError(fn, KVQ_ERR_SHAPE)
     layout = _page_views(fn, key_cache, value_cache)
-    _int32_vector(fn, cu_q_lens, context_lens)
+    _vector(fn, torch.int32, cu_q_lens, context_lens)
     n = context_lens.numel()
     if block_table.dtype != torch.int32:
         raise KvqError(fn, KVQ_ERR_DTYPE)
@@ -523,7 +526,7 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
         raise KvqError(fn, KVQ_ERR_DTYPE)
     _dev_error_ok(fn, dev_error)
-    _same_device(fn, query, out, key_cache, value_cache, block_table,
+    here = _here(fn, query, out, key_cache, value_cache, block_table,
                  cu_q_lens, context_lens, k_scale, v_scale, workspace,
                  dev_error)
     if workspace is None:
@@ -541,7 +544,7 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
         k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         out.data_ptr(), out.stride(0) if total > 1 else Hq * D, int(flags),
-        _ptr(dev_error), _stream_of(query) if stream is None else stream)
+        _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
@@ -556,32 +559,24 @@ def alloc_page_pool(num_blocks: int, num_rows: int, max_blocks_per_seq: int,
 
 def _pool_args(fn: str, ref_count, block_table, seq_lens, dev_error,
                *others):
-    """The state's checks, and its leading C arguments."""
-    _int32_vector(fn, ref_count, seq_lens)
-    if block_table.dtype != torch.int32:
+    """The state's checks; its leading C arguments, and the stream."""
+    _vector(fn, torch.int32, ref_count, seq_lens)
+    if block_table.dtype is not torch.int32:
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if (block_table.dim() != 2 or block_table.size(0) != seq_lens.numel()
-            or (block_table.numel() > 1 and block_table.size(1) > 1
-                and block_table.stride(1) != 1)):
+    if block_table.dim() != 2:
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    # rows that overlap (an expanded table) would be written by several
-    if (block_table.size(0) > 1 and block_table.size(1) > 0
-            and block_table.stride(0) < block_table.size(1)):
+    rows, width = block_table.shape
+    stride, step = block_table.stride()
+    # (rows that overlap, as of an expanded table, would be written by
+    # several)
+    if rows != seq_lens.numel() or (rows and width and (
+            (width > 1 and step != 1) or (rows > 1 and stride < width))):
         raise KvqError(fn, KVQ_ERR_SHAPE)
     _dev_error_ok(fn, dev_error)
-    _same_device(fn, ref_count, block_table, seq_lens, dev_error, *others)
-    rows, width = block_table.shape
+    here = _here(fn, ref_count, block_table, seq_lens, dev_error, *others)
     return (ref_count.data_ptr(), ref_count.numel(), block_table.data_ptr(),
-            block_table.stride(0) if rows > 1 else width, rows, width,
-            seq_lens.data_ptr())
-
-
-def _int64_vector(fn: str, *tensors) -> None:
-    for t in tensors:
-        if t.dtype != torch.int64:
-            raise KvqError(fn, KVQ_ERR_DTYPE)
-        if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1):
-            raise KvqError(fn, KVQ_ERR_SHAPE)
+            stride if rows > 1 and width else width, rows, width,
+            seq_lens.data_ptr()), here
 
 
 def kvq_extend_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
@@ -595,17 +590,17 @@ def kvq_extend_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
     ``alloc_page_pool``; seq_ids int32 [n]; cu_new int32 [n + 1];
     slot_mapping int64 [total], written whole."""
     fn = "kvq_extend_sequences"
-    _int32_vector(fn, seq_ids, cu_new)
-    _int64_vector(fn, slot_mapping)
+    _vector(fn, torch.int32, seq_ids, cu_new)
+    _vector(fn, torch.int64, slot_mapping)
     n = seq_ids.numel()
     if cu_new.numel() != n + 1:
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
-                       seq_ids, cu_new, slot_mapping)
+    state, here = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                             seq_ids, cu_new, slot_mapping)
     st = lib().kvq_extend_sequences(
         *state, int(block_size), seq_ids.data_ptr(), cu_new.data_ptr(), n,
         slot_mapping.data_ptr(), slot_mapping.numel(), int(flags),
-        _ptr(dev_error), _stream_of(ref_count) if stream is None else stream)
+        _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
@@ -619,17 +614,16 @@ def kvq_fork_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
     ``include/kvq.h``); ``kvq_copy_pages(caches, copy_src, copy_dst)`` then
     copies the partly filled last pages.  All four lists int32 [n]."""
     fn = "kvq_fork_sequences"
-    _int32_vector(fn, parent_ids, child_ids, copy_src, copy_dst)
+    _vector(fn, torch.int32, parent_ids, child_ids, copy_src, copy_dst)
     n = parent_ids.numel()
     if any(t.numel() != n for t in (child_ids, copy_src, copy_dst)):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
-                       parent_ids, child_ids, copy_src, copy_dst)
+    state, here = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                             parent_ids, child_ids, copy_src, copy_dst)
     st = lib().kvq_fork_sequences(
         *state, int(block_size), parent_ids.data_ptr(),
         child_ids.data_ptr(), n, copy_src.data_ptr(), copy_dst.data_ptr(),
-        int(flags), _ptr(dev_error),
-        _stream_of(ref_count) if stream is None else stream)
+        int(flags), _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
@@ -646,19 +640,19 @@ def kvq_compact_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
     moves their bytes.  keep int32 [total]; src_slots, dst_slots int64
     [total], written whole."""
     fn = "kvq_compact_sequences"
-    _int32_vector(fn, seq_ids, keep, cu_keep)
-    _int64_vector(fn, src_slots, dst_slots)
+    _vector(fn, torch.int32, seq_ids, keep, cu_keep)
+    _vector(fn, torch.int64, src_slots, dst_slots)
     n = seq_ids.numel()
     if (cu_keep.numel() != n + 1 or src_slots.numel() != keep.numel()
             or dst_slots.numel() != keep.numel()):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
-                       seq_ids, keep, cu_keep, src_slots, dst_slots)
+    state, here = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                             seq_ids, keep, cu_keep, src_slots, dst_slots)
     st = lib().kvq_compact_sequences(
         *state, int(block_size), seq_ids.data_ptr(), keep.data_ptr(),
         cu_keep.data_ptr(), n, src_slots.data_ptr(), dst_slots.data_ptr(),
         keep.numel(), int(flags), _ptr(dev_error),
-        _stream_of(ref_count) if stream is None else stream)
+        here if stream is None else stream)
     _check(fn, st)
 
 
@@ -669,47 +663,53 @@ def kvq_free_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
     """Rows seq_ids[i] become empty, their pages are dropped (see
     ``include/kvq.h``)."""
     fn = "kvq_free_sequences"
-    _int32_vector(fn, seq_ids)
-    state = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
-                       seq_ids)
+    _vector(fn, torch.int32, seq_ids)
+    state, here = _pool_args(fn, ref_count, block_table, seq_lens, dev_error,
+                             seq_ids)
     st = lib().kvq_free_sequences(
         *state, seq_ids.data_ptr(), seq_ids.numel(), int(flags),
-        _ptr(dev_error), _stream_of(ref_count) if stream is None else stream)
+        _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
 def _cache_list(fn: str, caches, dims: int):
-    """(tensors' common shape and strides of one cache, a C array of their
-    addresses, how many, a tensor): caches is a list of uint8 tensors
-    [num_blocks, ...] of one shape, or one tensor with the caches stacked in
-    front."""
+    """(one cache's shape and strides, the addresses as a C array, how many,
+    the tensors): caches is a list of uint8 tensors [num_blocks, ...] of one
+    shape, or one tensor with the caches stacked in front."""
     if isinstance(caches, torch.Tensor):
-        if caches.dtype != torch.uint8:
+        if caches.dtype is not torch.uint8:
             raise KvqError(fn, KVQ_ERR_DTYPE)
-        if caches.dim() < dims + 1 or caches.size(0) == 0:
+        shape, strides = caches.shape, caches.stride()
+        if len(shape) < dims + 1 or shape[0] == 0:
             raise KvqError(fn, KVQ_ERR_SHAPE)
-        n, first = caches.size(0), caches[0]
-        if n > 1 and caches.stride(0) < first.size(0) * first.stride(0):
+        n, step = shape[0], strides[0]
+        shape, strides = shape[1:], strides[1:]
+        if n > 1 and step < shape[0] * strides[0]:
             raise KvqError(fn, KVQ_ERR_SHAPE)  # caches would overlap
-        base, step = caches.data_ptr(), caches.stride(0)
-        ptrs = [base + k * step for k in range(n)]
-        tensors = [caches]
+        base = caches.data_ptr()
+        ptrs = range(base, base + n * step, step) if n > 1 else (base,)
+        tensors = (caches,)
     else:
-        tensors = list(caches)
+        tensors = tuple(caches)
         if not tensors:
             raise KvqError(fn, KVQ_ERR_SHAPE)
-        first = tensors[0]
+        n, shape, strides = len(tensors), tensors[0].shape, \
+            tensors[0].stride()
         for t in tensors:
-            if t.dtype != torch.uint8:
+            if t.dtype is not torch.uint8:
                 raise KvqError(fn, KVQ_ERR_DTYPE)
-            if t.shape != first.shape or t.stride() != first.stride():
+            if t.shape != shape or t.stride() != strides:
                 raise KvqError(fn, KVQ_ERR_SHAPE)
-        if first.dim() < dims:
+        if len(shape) < dims:
             raise KvqError(fn, KVQ_ERR_SHAPE)
         ptrs = [t.data_ptr() for t in tensors]
-    if first.size(0) > 0 and not first[0].is_contiguous():
-        raise KvqError(fn, KVQ_ERR_SHAPE)
-    return first, (ctypes.c_void_p * len(ptrs))(*ptrs), len(ptrs), tensors
+    # a page's bytes lie together
+    page = 1
+    for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
+        if size != 1 and stride != page:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+        page *= size
+    return shape, strides, page, struct.pack(f"{n}P", *ptrs), n, tensors
 
 
 def kvq_copy_pages(caches, src_pages: torch.Tensor, dst_pages: torch.Tensor,
@@ -720,19 +720,18 @@ def kvq_copy_pages(caches, src_pages: torch.Tensor, dst_pages: torch.Tensor,
     one shape, each page contiguous, or one tensor [n, num_blocks, ...];
     src_pages, dst_pages int32 [pairs], negative = skip."""
     fn = "kvq_copy_pages"
-    first, ptrs, n, tensors = _cache_list(fn, caches, 2)
-    _int32_vector(fn, src_pages, dst_pages)
+    shape, strides, page, ptrs, n, tensors = _cache_list(fn, caches, 2)
+    _vector(fn, torch.int32, src_pages, dst_pages)
     if src_pages.numel() != dst_pages.numel():
         raise KvqError(fn, KVQ_ERR_SHAPE)
     _dev_error_ok(fn, dev_error)
-    _same_device(fn, *tensors, src_pages, dst_pages, dev_error)
-    if first.size(0) == 0:
+    here = _here(fn, *tensors, src_pages, dst_pages, dev_error)
+    if shape[0] == 0:
         return
     st = lib().kvq_copy_pages(
-        ptrs, n, first.stride(0), first[0].numel(), first.size(0),
+        ptrs, n, strides[0] if shape[0] > 1 else page, page, shape[0],
         src_pages.data_ptr(), dst_pages.data_ptr(), src_pages.numel(),
-        int(flags), _ptr(dev_error),
-        _stream_of(src_pages) if stream is None else stream)
+        int(flags), _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
@@ -747,26 +746,26 @@ def kvq_move_tokens_nvfp4(kv_caches, src_slots: torch.Tensor,
     one such tensor with the caches stacked in front; src_slots, dst_slots
     int64 [moves], negative = skip; cu_moves int32 [lists + 1]."""
     fn = "kvq_move_tokens_nvfp4"
-    first, ptrs, n, tensors = _cache_list(fn, kv_caches, 5)
-    if first.dim() != 5 or first.size(1) != 2 or first.size(4) % 9 != 0:
+    shape, strides, page, ptrs, n, tensors = _cache_list(fn, kv_caches, 5)
+    if len(shape) != 5 or shape[1] != 2 or shape[4] % 9 != 0:
         raise KvqError(fn, KVQ_ERR_SHAPE)
     if layout not in (KVQ_LAYOUT_HND, KVQ_LAYOUT_NHD):
         raise KvqError(fn, KVQ_ERR_LAYOUT)
-    H, B = first.size(2), first.size(3)
+    H, B = shape[2], shape[3]
     if layout == KVQ_LAYOUT_NHD:
         H, B = B, H
-    _int64_vector(fn, src_slots, dst_slots)
-    _int32_vector(fn, cu_moves)
+    _vector(fn, torch.int64, src_slots, dst_slots)
+    _vector(fn, torch.int32, cu_moves)
     if src_slots.numel() != dst_slots.numel() or cu_moves.numel() < 1:
         raise KvqError(fn, KVQ_ERR_SHAPE)
     _dev_error_ok(fn, dev_error)
-    _same_device(fn, *tensors, src_slots, dst_slots, cu_moves, dev_error)
+    here = _here(fn, *tensors, src_slots, dst_slots, cu_moves, dev_error)
     st = lib().kvq_move_tokens_nvfp4(
-        ptrs, n, first.stride(1), first.stride(0), first.size(0), B,
-        int(layout), H, first.size(4) // 9 * 16, src_slots.data_ptr(),
+        ptrs, n, page // 2, strides[0] if shape[0] > 1 else page, shape[0],
+        B, int(layout), H, shape[4] // 9 * 16, src_slots.data_ptr(),
         dst_slots.data_ptr(), src_slots.numel(), cu_moves.data_ptr(),
         cu_moves.numel() - 1, int(flags), _ptr(dev_error),
-        _stream_of(src_slots) if stream is None else stream)
+        here if stream is None else stream)
     _check(fn, st)
 
 
