@@ -659,7 +659,7 @@ kvq_status kvq_move_tokens_nvfp4(
     return KVQ_ERR_ARG;
   if (num_caches < 0 || num_lists < 0 || total_moves < 0 || num_blocks < 0 ||
       num_heads <= 0 || head_size <= 0 || block_size <= 0 ||
-      num_blocks > INT32_MAX || num_heads > 32767 || total_moves > INT32_MAX)
+      num_blocks > INT32_MAX || num_heads > 65535 || total_moves > INT32_MAX)
     return KVQ_ERR_SHAPE;
   if (head_size % 64 != 0 || head_size > 8192 || block_size % 4 != 0)
     return KVQ_ERR_SHAPE;
@@ -705,6 +705,7 @@ kvq_status kvq_move_tokens_nvfp4(
   p.D = head_size;
   p.S = static_cast<int32_t>(S);
   p.B = block_size;
+  p.b_shift = ilog2_exact(B);
   p.swizzle_k = (flags & KVQ_F_SWIZZLE_K_SCALE) != 0u;
   p.pdl = (flags & KVQ_F_PDL) != 0u;
   for (int32_t first = 0; first < num_caches; first += kMaxCaches) {

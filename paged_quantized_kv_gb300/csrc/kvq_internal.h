@@ -268,6 +268,7 @@ struct MoveParams {
   int64_t total;
   int32_t* err;
   int32_t num_caches, num_lists, H, D, S, B;
+  int32_t b_shift;         // log2(B) when B is a power of two, else -1
   bool swizzle_k, pdl;
 };
 cudaError_t launch_move_tokens(const MoveParams& p, cudaStream_t stream);

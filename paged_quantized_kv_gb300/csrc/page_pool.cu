@@ -30,6 +30,9 @@ namespace cg = cooperative_groups;
 constexpr int kCluster = 8;     // CTAs of a pool kernel (portable size)
 constexpr int kThreads = 1024;
 constexpr int kChunk = 4 * kThreads;  // counts of one scan round of a CTA
+// Up to this many slots an extend writes itself (8192 threads, two each: a
+// second launch takes longer); more are left to a second kernel.
+constexpr int kClusterSlots = 16384;
 
 __device__ __forceinline__ void flag(int32_t* err, int32_t bits) {
   if (err != nullptr) atomicOr(err, bits);
@@ -284,7 +287,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   cluster.sync();
   const int tid = rank * kThreads + static_cast<int>(threadIdx.x);
   const int64_t covered = cus[n];
-  for (int64_t t = tid; t < p.total; t += kCluster * kThreads) {
+  if (p.total > kClusterSlots) {
+    // the rest is slots_kernel's: each entry's first slot for it, or -1
+    for (int i = tid; i < n; i += kCluster * kThreads) {
+      if (cus[i + 1] == cus[i]) continue;
+      int64_t slot = -1;
+      if (old[i] >= 0 && off[i + 1] <= max(all, off[i]))
+        slot = static_cast<int64_t>(
+                   p.table[p.ids[i] * p.stride + old[i] / B]) * B +
+               old[i] % B;
+      p.slots[cus[i]] = slot;
+    }
+    if (!ok && tid == 0) p.slots[0] = -1;
+  }
+  for (int64_t t = tid; p.total <= kClusterSlots && t < p.total;
+       t += kCluster * kThreads) {
     int64_t slot = -1;
     if (t < covered) {
       const int i = last_at_most(cus, n, static_cast<int>(t));
@@ -303,6 +320,41 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
       p.lens[p.ids[i]] = old[i] + (cus[i + 1] - cus[i]);
     else
       flag(p.err, KVQ_DEVERR_FULL);
+  }
+}
+
+// The slots of many new tokens, by the whole GPU (262144 tokens: 47 us by the
+// cluster's eight SMs, measured with a free before it).  Reads the new state;
+// an entry's first slot says whether it was served.
+constexpr int kSlotThreads = 256;
+__global__ void __launch_bounds__(kSlotThreads)
+    slots_kernel(const __grid_constant__ PoolParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  int* cus = reinterpret_cast<int*>(smem);
+  pdl_prologue();
+  const int n = p.n, B = p.B;
+  const bool ok = offsets_ok(p.cu, n, p.total);
+  for (int i = threadIdx.x; i <= n; i += kSlotThreads)
+    cus[i] = ok ? p.cu[i] : 0;
+  __syncthreads();
+  const int64_t covered = cus[n];
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kSlotThreads +
+                   threadIdx.x;
+       t < p.total; t += static_cast<int64_t>(gridDim.x) * kSlotThreads) {
+    if (t >= covered) {
+      p.slots[t] = -1;
+      continue;
+    }
+    const int i = last_at_most(cus, n, static_cast<int>(t));
+    if (t == cus[i]) continue;  // written
+    int64_t slot = -1;
+    if (p.slots[cus[i]] >= 0) {
+      const int id = p.ids[i];
+      const int pos = p.lens[id] - (cus[i + 1] - static_cast<int>(t));
+      const int32_t page = p.table[id * p.stride + pos / B];
+      slot = static_cast<int64_t>(page) * B + pos % B;
+    }
+    p.slots[t] = slot;
   }
 }
 
@@ -531,7 +583,14 @@ cudaError_t launch_cluster(K kernel, const PoolParams& p,
 }  // namespace
 
 cudaError_t launch_extend(const PoolParams& p, cudaStream_t stream) {
-  return launch_cluster(extend_kernel, p, stream);
+  const cudaError_t err = launch_cluster(extend_kernel, p, stream);
+  if (err != cudaSuccess || p.total <= kClusterSlots) return err;
+  const int64_t ctas = (p.total + kSlotThreads - 1) / kSlotThreads;
+  return launch_kernel(slots_kernel,
+                       dim3(static_cast<unsigned>(
+                           ctas < 8 * sm_count() ? ctas : 8 * sm_count())),
+                       kSlotThreads, 4 * static_cast<size_t>(p.n + 1), stream,
+                       true, p);
 }
 
 cudaError_t launch_fork(const PoolParams& p, cudaStream_t stream) {

@@ -112,6 +112,26 @@ def test_extend_one_by_one_and_long():
     g.extend([1], [200])                          # past the row: refused
 
 
+def test_extend_many_tokens():
+    """Slots enough for the second kernel: refused entries, empty ones,
+    tokens behind the last, an order of offsets that is refused whole."""
+    m = Pool(6000, 40, 700, 16)
+    g = Gpu(m)
+    rng = np.random.default_rng(3)
+    g.extend(rng.permutation(40)[:30].tolist(),
+             rng.integers(0, 50, 30).tolist())
+    new = rng.integers(0, 2000, 20).tolist()
+    new[3], new[7], new[19] = 0, 11500, 0
+    g.extend(rng.permutation(40)[:20].tolist(), new, total=sum(new) + 77)
+    g.extend([1, 2, 1, 3], [9000, 5000, 3000, 7000])
+    g.extend([4, 5], None, total=20000, cu=[0, 15000, 14000])
+    g.extend([4, 5], None, total=20000, cu=[5, 15000, 20000])
+    g.extend([0, 4, 5], [0, 0, 0], total=17000)
+    g.free(list(range(40)))
+    g.extend([6, 7, 8], [11200, 11200, 11200])
+    g.extend(list(range(30)), [3000] * 30)         # the pool runs out
+
+
 def test_extend_refusals():
     m = Pool(20, 6, 4, 8)
     g = Gpu(m)
