@@ -216,6 +216,20 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
   asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+               : "=r"(v.x), "=r"(v.y)
+               : "r"(a));
+  return v;
+}
 __device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
   asm volatile(
       "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
@@ -596,7 +610,12 @@ enum Bar {
 constexpr int kQAt = 0;                       // 2 tiles
 constexpr int kKAt = kQAt + 2 * kTile;        // kStages tiles
 constexpr int kVAt = kKAt + kStages * kTile;  // kStages tiles
-constexpr int kBarAt = kVAt + kStages * kTile;
+// The fillers' raw bytes: two slots each of 32 rows of 64 data bytes (by
+// 16-byte piece, then lane) and 8 scale bytes.
+constexpr int kRawSlot = 32 * 72;
+constexpr int kRawBytes = 2 * kRawSlot;
+constexpr int kRawAt = kVAt + kStages * kTile;
+constexpr int kBarAt = kRawAt + kFillers * kRawBytes;
 // Per tile and quarter: the tokens that are not left out ([8][4] words).  K
 // of tile k waits for the logits of tile k - 2, whose product is issued after
 // the weights of tile k - 4 at the latest: eight entries are enough.
@@ -618,7 +637,8 @@ constexpr int kRingAt = kRefAt + 1024;
 constexpr int kWalkAt = kRingAt + 4 * static_cast<int>(sizeof(Walk));
 constexpr int kSmemBytes =
     kWalkAt + (kFillers + 2) * static_cast<int>(sizeof(Walk)) + 1024;
-static_assert(kBars <= 22 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
+static_assert(kSmemBytes <= 227 * 1024 && kRawBytes % 16 == 0 &&
+                  kBars <= 22 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
                   sizeof(Walk) % 8 == 0,
               "");
 // Tensor memory: logits (and, over them, weights) of the two slots, outputs
@@ -1014,10 +1034,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftWarps + 2) {
     // --- dequantise: a quarter (32 tokens) of a tile's K or V at a time ------
     // The quarters K 0..3, V 0..3 of the share's tiles, in order, are dealt
-    // round-robin to the warps.  A warp has three in hand: the one whose raw
-    // bytes are in registers, the next one, whose page is known, and the one
-    // behind it, whose block id is on its way (`job`, `kt` and `walk` are at
-    // that one).
+    // round-robin to the warps.  A warp has four in hand: the one that it
+    // dequantises, whose raw bytes are in shared memory, two whose bytes are
+    // on their way there (a slot each; every lane copies and reads its own
+    // token's), and the one behind them, whose block id is on its way (`job`,
+    // `kt` and `walk` are at that one).
     int job = warp - kSoftWarps - 2;  // 0..3: K quarters, 4..7: V quarters
     // (this segment: its sequence's length and table row, its head, its end)
     int kt = walk->kv0, kv1 = walk->kv1, len = walk->s.L, seg = 0;
@@ -1039,39 +1060,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         blk = __ldg(table + j);
       }
     };
-    // The next job.  Tokens that are not to be read load the query's first
-    // bytes instead, and scale them by 0: loads without a branch need no
-    // moves at the end of the loop, where they would wait for the data.
-    const uint8_t *data = nullptr, *scales = nullptr;
-    bool next_some = false, next_first = false, next_in = false;
-    int next_pos = 0, next_job = 0;
-    uint32_t next_mask = 0, next_cnt = 0, next_seg = 0;
-    auto step = [&]() {
+    // The last job whose copies were issued, and the one before it.
+    struct Job {
+      bool some, first, in;
+      int pos, job;
+      uint32_t mask, cnt, seg;
+    };
+    Job next, after;
+    const uint32_t raw = base + kRawAt + (warp - kSoftWarps - 2) * kRawBytes +
+                         16 * lane;
+    // copies of the job at (kt, job) into slot `slot`, and on to the next
+    auto issue = [&](uint32_t slot) {
+      Job n = {more, first, false, pos, job, 0, cnt,
+               static_cast<uint32_t>(seg)};
       bool bad = false;
-      data = scales = reinterpret_cast<const uint8_t*>(p.q);
-      next_in = false;
-      next_some = more;
-      next_pos = pos;
-      next_job = job;
-      next_cnt = cnt;
-      next_seg = seg;
-      next_first = first;
-      const bool v = job >= 4;
+      const uint8_t *data = reinterpret_cast<const uint8_t*>(p.q),
+                    *scales = data;
       if (quad) {
         bad = blk < 0 || blk >= p.num_blocks;
-        const bool in = pos < len;
+        const bool in = pos < len, v = job >= 4;
         if (!bad) {
           const uint8_t* page =
               (v ? p.side[1] : p.side[0]) + blk * p.page_stride;
           data = page + data_h + off * p.dts;
           // swizzled: row off % 4 of the band, other lanes' scales too
           scales = page + scale_h + off * p.sts;
-          next_in = in;
+          n.in = in;
         } else if (in && !v) {
           flag(p.dev_error, KVQ_DEVERR_BLOCK);
         }
       }
-      next_mask = __ballot_sync(0xFFFFFFFFu, !bad);
+      n.mask = __ballot_sync(0xFFFFFFFFu, !bad);
+      if (more) {
+        // (a token that is not to be read: the query's first bytes, which
+        // are scaled by 0)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                           raw + slot * kRawSlot + 512 * i),
+                       "l"(data + 16 * i)
+                       : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(
+                         raw + slot * kRawSlot + 2048 - 8 * lane),
+                     "l"(scales)
+                     : "memory");
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
       if (more) {
         job += kFillers;
         if (job >= 8) {
@@ -1092,18 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         look_up();
       }
-    };
-    uint4 d[4];
-    uint2 sc;
-    auto load = [&](int i) {
-      asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(d[i].x), "=r"(d[i].y), "=r"(d[i].z), "=r"(d[i].w)
-                   : "l"(data + 16 * i));
-    };
-    auto load_scales = [&]() {
-      asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];"
-                   : "=r"(sc.x), "=r"(sc.y)
-                   : "l"(scales));
+      return n;
     };
     // swizzled scales: 4 x 4 byte transposition over the band's lanes, to
     // words of the even and the odd groups of this thread's token
@@ -1115,22 +1138,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     look_up();
-    step();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) load(i);
-    load_scales();
-    while (next_some) {
-      const int stage = next_cnt & 1;
-      const uint32_t phase = (next_cnt >> 1) & 1;
-      const bool is_v = next_job >= 4, in = next_in;
-      const int quarter = next_job & 3, cur_pos = next_pos;
+    next = issue(0);
+    after = issue(1);
+    for (uint32_t slot = 0; next.some; slot ^= 1) {
+      const int stage = next.cnt & 1;
+      const uint32_t phase = (next.cnt >> 1) & 1;
+      const bool is_v = next.job >= 4, in = next.in, first = next.first;
+      const int quarter = next.job & 3, cur_pos = next.pos;
       const bool swz = is_v || p.swizzle_k;
-      const uint32_t mask = next_mask, cur = next_cnt, cur_seg = next_seg;
-      const bool first = next_first;
-      step();
+      const uint32_t mask = next.mask, cur = next.cnt, cur_seg = next.seg;
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
       if (!warp_wait(bar((is_v ? kVEmpty : kKEmpty) + stage), phase ^ 1,
                      abort))
         goto done;
+      const uint32_t from = raw + slot * kRawSlot;
+      const uint2 sc = lds64(from + 2048 - 8 * lane);
       if (!is_v && lane == 0)
         reinterpret_cast<volatile uint32_t*>(
             smem + kValidAt)[(cur & 7) * 4 + quarter] = mask;
@@ -1154,14 +1176,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst =
           (base + (is_v ? kVAt : kKAt) + stage * kTile +
            (32 * quarter + lane) * 128) | ((lane & 7) << 4);
-      load_scales();
 #pragma unroll
       for (int g = 0; g < 4; ++g) {  // groups 2g, 2g + 1
+        const uint4 d = lds128(from + 512 * g);
         const uint32_t pair = swz ? prmt(lo, hi, g | ((g + 4) << 4))
                                   : (g < 2 ? lo : hi) >> (16 * (g & 1));
         const uint32_t sf = e4m3x2_to_f16x2(pair & 0xFFFFu);
         const uint32_t se = prmt(sf, sf, 0x1010u), so = prmt(sf, sf, 0x3232u);
-        const uint32_t w[4] = {d[g].x, d[g].y, d[g].z, d[g].w};
+        const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t o[4];
@@ -1169,11 +1191,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ch = 4 * g + i;  // 16-byte chunk of the row
           sts128((dst ^ ((ch & 7) << 4)) + (ch >> 3) * kHalf, o);
         }
-        load(g);  // the next job's bytes into the registers just used
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar((is_v ? kVFull : kKFull) + stage));
+      next = after;
+      after = issue(slot);  // (this lane has read its bytes)
     }
   } else if (warp >= kSoftWarps && any) {
     // --- products of slot m: the warp waits, one lane issues -----------------
@@ -1286,6 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 done:
   __syncwarp();
   if (*abort != 0) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
     // whoever waits for this warp's rows goes on, to its own wait that gives
     // up
     if (warp < kSoftWarps) bar_arrive(1 + (warp & 3), 64);

@@ -117,6 +117,11 @@ constexpr int kDepth = KVQ_ATTN_MMA_DEPTH;  // steps in flight per warp
 #define KVQ_ATTN_MMA_LAST_SHARE 4
 #endif
 constexpr int kLastShare = KVQ_ATTN_MMA_LAST_SHARE;
+// Rows of chunks take shorter stretches (1024, 512 tokens) where these would
+// leave the SMs fewer CTAs than this each.  Measured: 16 single tokens over
+// 300 to 2300 tokens beside longer chunks 90 us at 1792, 84 at 1024; one
+// token over 131000 (592 CTAs) 46 us at 1792, 61 at 1024, 101 at 512.
+constexpr int kChunkCtas = 3;
 // the longest stretch (the first of two, 2 kLastShare S / (kLastShare + 1)
 // tokens) leaves each warp at most 1024 tokens: 64 blocks of 16
 static_assert(2 * kLastShare * KVQ_ATTN_MMA_PART / (kLastShare + 1) <=
@@ -467,8 +472,11 @@ paged_attention_mma_kernel(const AttnParams p) {
         tid == 0)
       atomicOr(p.dev_error, KVQ_DEVERR_SEQ);
   };
-  // stretch length: fixed on contiguous pages (the host sets p.part to it)
-  const int S = kB8 ? kPartB8 : kContig ? KVQ_ATTN_MMA_PART : p.part;
+  // stretch length: fixed on contiguous pages (the host sets p.part to it),
+  // but for chunks' rows
+  const int S = kContig && p.cu == nullptr
+                    ? (kB8 ? kPartB8 : KVQ_ATTN_MMA_PART)
+                    : p.part;
   const int nparts = (L + S - 1) / S;
   if (part >= nparts || !me.live) {
     if (early) pdl_prologue();
@@ -1297,7 +1305,17 @@ cudaError_t launch_mma(const AttnParams& caller, cudaStream_t stream) {
   // contiguous pages, 32 elsewhere.
   AttnParams p = caller;
   // (the caller's partitions are at most 512 tokens)
-  if (kContig) p.part = kPages >= 9 ? kPartB8 : KVQ_ATTN_MMA_PART;
+  if (kContig) {
+    const int most = kPages >= 9 ? kPartB8 : KVQ_ATTN_MMA_PART;
+    p.part = most;
+    if (p.cu != nullptr) {
+      const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.Hkv;
+      const int64_t want = static_cast<int64_t>(kChunkCtas) * sm_count();
+      while (p.part > 512 &&
+             rows * ((p.len_cap + p.part - 1) / p.part) < want)
+        p.part = p.part > 1024 ? 1024 : 512;
+    }
+  }
   const int parts =
       static_cast<int>((static_cast<int64_t>(p.len_cap) + p.part - 1) / p.part);
   static bool configured[64] = {false};  // per instantiation and device
