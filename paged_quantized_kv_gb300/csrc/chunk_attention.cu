@@ -598,8 +598,9 @@ enum Bar {
   kVEmpty = kVFull + kStages,
   kQFull = kVEmpty + kStages,  // [slot] the query rows are in shared memory
   kSFull = kQFull + 2,         // [slot] logits are in tensor memory
-  kPFull = kSFull + 2,         // [slot] weights are in tensor memory
-  kODone = kPFull + 2,         // [slot] they are multiplied with V
+  kPFull = kSFull + 2,         // [slot][half] weights are in tensor memory
+  kPDone = kPFull + 4,         // [slot] the first half is multiplied with V
+  kODone = kPDone + 2,         // [slot] all of them are
   kTurn = kODone + 2,          // [slot] the tensor cores are this slot's
   kOFree = kTurn + 2,          // the segment's output has been read
   kSegment = kOFree + 1,       // the next segment is in the ring
@@ -619,7 +620,7 @@ constexpr int kBarAt = kRawAt + kFillers * kRawBytes;
 // Per tile and quarter: the tokens that are not left out ([8][4] words).  K
 // of tile k waits for the logits of tile k - 2, whose product is issued after
 // the weights of tile k - 4 at the latest: eight entries are enough.
-constexpr int kValidAt = kBarAt + 8 * 22;
+constexpr int kValidAt = kBarAt + 8 * 28;
 // Per segment, group and quarter: the first token whose V scale is NaN
 // ([8][8][4] ints).  V of tile k waits for tile k - 2's product with V, and
 // that one for the epilogues of all segments before its own: when segment s
@@ -638,7 +639,7 @@ constexpr int kWalkAt = kRingAt + 4 * static_cast<int>(sizeof(Walk));
 constexpr int kSmemBytes =
     kWalkAt + (kFillers + 2) * static_cast<int>(sizeof(Walk)) + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && kRawBytes % 16 == 0 &&
-                  kBars <= 22 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
+                  kBars <= 28 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
                   sizeof(Walk) % 8 == 0,
               "");
 // Tensor memory: logits (and, over them, weights) of the two slots, outputs
@@ -676,7 +677,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int m = 0; m < 2; ++m) {
       mbar_init(bar(kQFull + m), 4);
       mbar_init(bar(kSFull + m), 1);
-      mbar_init(bar(kPFull + m), 4);
+      mbar_init(bar(kPFull + 2 * m), 4);
+      mbar_init(bar(kPFull + 2 * m + 1), 4);
+      mbar_init(bar(kPDone + m), 1);
       mbar_init(bar(kTurn + m), 1);
       mbar_init(bar(kODone + m), 1);
     }
@@ -866,70 +869,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!warp_wait(bar(kSFull + m), cnt & 1, abort)) goto done;
         fence_after();
         // Weights are exp2 of the scaled logits minus a reference: the
-        // maximum of the first tile.  Later tiles do without their maximum:
-        // as long as a row's weights sum up to less than kMost, none is out
-        // of fp16's range.  Where that fails the tile is done over, with the
-        // maximum for the new reference.
-        bool look = kt == kt0;
-        uint32_t s[128];
-        float ts;
-        for (;;) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(s_col + 32 * k, s + 32 * k);
-          tmem_wait_ld();
-          // (looked at only now: the products keep shared memory busy, and
-          // what is read from it comes late)
-          const uint4 valid = *reinterpret_cast<const uint4*>(
-              smem + kValidAt + ((tiles + kt) & 7) * 16);
-          const int lim = pos - kt * kKeys;  // the row sees columns 0 .. lim
-          const bool all = lim >= kKeys - 1 &&
-                           (valid.x & valid.y & valid.z & valid.w) == ~0u;
-          if (!__all_sync(0xFFFFFFFFu, all)) {
-            mask32(s, valid.x & first_bits(lim));
-            mask32(s + 32, valid.y & first_bits(lim - 32));
-            mask32(s + 64, valid.z & first_bits(lim - 64));
-            mask32(s + 96, valid.w & first_bits(lim - 96));
-          }
-          if (look) {
-            const float top = fmaxf(max64(s), max64(s + 64)) * c;
-            const float f = top > ref ? ex2(ref - top) : 1.0f;
-            ref = fmaxf(ref, top);
-            sum *= f;
-            if (kt > kt0) {
-              if (!warp_spin(bar(kODone + m), (cnt - 1) & 1, abort))
-                goto done;
-              fence_after();
-              rescale(o_col, f);
+        // maximum of the first half of the first tile.  Later ones do
+        // without their maximum: as long as a row's weights of half a tile
+        // sum up to less than kMost, none is out of fp16's range.  Where
+        // that fails the half is done over, with its maximum for the new
+        // reference.  The product of the first half with V begins while the
+        // second is made.
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          bool look = kt == kt0 && half == 0;
+          uint32_t s[64];
+          float ts;
+          for (;;) {
+            tmem_ld32(s_col + 64 * half, s);
+            tmem_ld32(s_col + 64 * half + 32, s + 32);
+            const uint2 valid = *reinterpret_cast<const uint2*>(
+                smem + kValidAt + ((tiles + kt) & 7) * 16 + 8 * half);
+            // (the row sees columns 0 .. lim)
+            const int lim = pos - kt * kKeys - 64 * half;
+            tmem_wait_ld();
+            if (!__all_sync(0xFFFFFFFFu,
+                            lim >= 63 && (valid.x & valid.y) == ~0u)) {
+              mask32(s, valid.x & first_bits(lim));
+              mask32(s + 32, valid.y & first_bits(lim - 32));
             }
-          }
-          const float low = ref == -INFINITY ? 0.0f : ref;
-          const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
-          uint64_t add[2] = {0, 0};
+            if (look) {
+              const float top = max64(s) * c;
+              const float f = top > ref ? ex2(ref - top) : 1.0f;
+              ref = fmaxf(ref, top);
+              sum *= f;
+              if (kt > kt0 || half > 0) {
+                // (every product of this slot so far)
+                if (!warp_spin(bar((half ? kPDone : kODone) + m),
+                               (half ? cnt : cnt - 1) & 1, abort))
+                  goto done;
+                fence_after();
+                rescale(o_col, f);
+              }
+            }
+            const float low = ref == -INFINITY ? 0.0f : ref;
+            const uint64_t cc = pack2(c, c), ll = pack2(-low, -low);
+            uint64_t add[2] = {0, 0};
 #pragma unroll
-          for (int k = 0; k < 128; k += 2) {
-            float a, b;
-            unpack2(fma2(pack2(__uint_as_float(s[k]),
-                               __uint_as_float(s[k + 1])), cc, ll), a, b);
-            a = ex2(a);
-            b = ex2(b);
-            add[(k >> 1) & 1] = add2(add[(k >> 1) & 1], pack2(a, b));
-            s[k >> 1] = pack_f16x2(a, b);
+            for (int k = 0; k < 64; k += 2) {
+              float a, b;
+              unpack2(fma2(pack2(__uint_as_float(s[k]),
+                                 __uint_as_float(s[k + 1])), cc, ll), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              add[(k >> 1) & 1] = add2(add[(k >> 1) & 1], pack2(a, b));
+              s[k >> 1] = pack_f16x2(a, b);
+            }
+            float e, o;
+            unpack2(add2(add[0], add[1]), e, o);
+            ts = e + o;
+            // (a row that has seen nothing has no reference yet)
+            const bool again = !(ts < kMost) || ref == -INFINITY;
+            if (look || !__any_sync(0xFFFFFFFFu, again)) break;
+            look = true;
           }
-          float e, o;
-          unpack2(add2(add[0], add[1]), e, o);
-          ts = e + o;
-          // (a row that has seen nothing has no reference yet)
-          const bool again = !(ts < kMost) || ref == -INFINITY;
-          if (look || !__any_sync(0xFFFFFFFFu, again)) break;
-          look = true;
+          tmem_st32(s_col + 32 * half, s);
+          sum += ts;
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kPFull + 2 * m + half));
         }
-        tmem_st32(s_col, s);
-        tmem_st32(s_col + 32, s + 32);
-        sum += ts;
-        tmem_wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull + m));
       }
       // --- epilogue ---------------------------------------------------------------
       const int n = kv1 - kv0;
@@ -1228,40 +1233,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = first; i < n + step; i += step) {
         const bool pv = i >= first + step, qk = i < n;
         const uint32_t tv = cnt + i - step, tk = cnt + i;  // their tiles
-        // (the weights last: they come last, and every test on the way from
-        // them to the products would add to the slot's round)
-        if (pv && !warp_wait(bar(kVFull + (tv & 1)), (tv >> 1) & 1, abort))
-          goto done;
+        // (the weights after V: they come last, and every test on the way
+        // from them to the products would add to the slot's round)
+        const uint32_t a = desc_lo<16>(base + kQAt + q * kTile);
+        const uint32_t k = desc_lo<16>(base + kKAt + (tk & 1) * kTile);
+        const uint32_t v = desc_lo<kHalf>(base + kVAt + (tv & 1) * kTile);
+        const uint32_t s_at = tmem + 128 * m, o_at = s_at + kOCol;
+        if (pv) {
+          if (!warp_wait(bar(kVFull + (tv & 1)), (tv >> 1) & 1, abort))
+            goto done;
+          // the output's columns are free once the last segment's are read
+          // (after the weights: see the phases above)
+          if (!warp_wait(bar(kPFull + 2 * m), p_cnt & 1, abort)) goto done;
+          if (i == first + step && segs > 0 &&
+              !warp_wait(bar(kOFree), (segs - 1) & 1, abort))
+            goto done;
+          fence_after();
+          if (elect()) {
+            mma_ts(o_at, s_at, v, kIdescBmn, i > first + step);
+#pragma unroll
+            for (int x = 1; x < 4; ++x)
+              mma_ts(o_at, s_at + 8 * x, v + x * (2048 >> 4), kIdescBmn, 1);
+            mma_commit(bar(kPDone + m));
+          }
+          __syncwarp();
+        }
         if (qk && !warp_wait(bar(kKFull + (tk & 1)), (tk >> 1) & 1, abort))
           goto done;
-        // Two query tiles take turns: batches that ran side by side would
-        // end side by side, and leave the tensor cores idle while both
-        // slots make their weights.
+        // Two query tiles take turns with the rest: batches that ran side by
+        // side would end side by side, and leave the tensor cores idle while
+        // both slots make their weights.
         if (two && pv) {
           if (turns + m > 0 &&
               !warp_wait(bar(kTurn + m), (turns + m - 1) & 1, abort))
             goto done;
           ++turns;
         }
-        const uint32_t a = desc_lo<16>(base + kQAt + q * kTile);
-        const uint32_t k = desc_lo<16>(base + kKAt + (tk & 1) * kTile);
-        const uint32_t v = desc_lo<kHalf>(base + kVAt + (tv & 1) * kTile);
-        const uint32_t s_at = tmem + 128 * m, o_at = s_at + kOCol;
-        if (pv) {
-          // the output's columns are free once the last segment's are read
-          if (i == first + step && segs > 0) {
-            if (!warp_wait(bar(kPFull + m), p_cnt & 1, abort)) goto done;
-            if (!warp_wait(bar(kOFree), (segs - 1) & 1, abort)) goto done;
-          }
-          if (!warp_wait(bar(kPFull + m), p_cnt & 1, abort)) goto done;
-          ++p_cnt;
-        }
+        if (pv && !warp_wait(bar(kPFull + 2 * m + 1), p_cnt++ & 1, abort))
+          goto done;
         fence_after();
         if (elect()) {
           if (pv) {
-            mma_ts(o_at, s_at, v, kIdescBmn, i > first + step);
 #pragma unroll
-            for (int x = 1; x < 8; ++x)
+            for (int x = 4; x < 8; ++x)
               mma_ts(o_at, s_at + 8 * x, v + x * (2048 >> 4), kIdescBmn, 1);
             mma_commit(bar(kODone + m));
             mma_commit(bar(kVEmpty + (tv & 1)));
