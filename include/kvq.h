@@ -478,10 +478,12 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  *                unspecified.  Calls that can overlap on the GPU (other
  *                streams, graphs replayed side by side) each need their own.
  * out            dtype [total_q, num_q_heads, 128], rows out_stride0
- *                elements apart (multiple of 8), 16-byte aligned.
+ *                elements apart (multiple of 8), 16-byte aligned; must not
+ *                overlap query.
  * flags          KVQ_F_SWIZZLE_K_SCALE, KVQ_F_PDL, or 0.
  * dev_error      nullable (KVQ_DEVERR_BLOCK: the token is left out;
- *                KVQ_DEVERR_SEQ; KVQ_DEVERR_TIMEOUT).
+ *                KVQ_DEVERR_SEQ; KVQ_DEVERR_TIMEOUT: a bounded wait gave up,
+ *                rows may be missing).
  * total_q == 0 or num_seqs == 0 returns KVQ_OK without launching.
  */
 kvq_status kvq_chunk_attention_nvfp4(

@@ -1,5 +1,41 @@
 // chunk_attention.cu -- attention of a chunk of new tokens over the NVFP4
 // pages, sm_103a: tcgen05 products with everything between them on chip.
+//
+// For the rows (new token, head of a KV head) of a sequence, with positions
+// P: S = Q K^T, W = exp2(c S - reference) for the tokens t <= P, O = W V,
+// out = O v_scale / sum W, where K = e2m1 * e4m3 in fp16 (exact: 6 bits) and
+// c = scale * k_scale * log2 e.
+//
+// One CTA per SM.  Its unit of work is a KV tile of 128 tokens for up to two
+// query tiles of 128 rows ("slots"):
+//   * Fillers copy the tile's raw NVFP4 rows to shared memory two jobs ahead
+//     and dequantise them into the operands' swizzled layouts, K (rows x
+//     dims) and V (the same bytes, read MN-major): the cache is read as
+//     NVFP4, once per 256 rows, and nothing dequantised leaves the SM.
+//   * Product warps issue S (both operands in shared memory) and O += W V (W
+//     in tensor memory): 16 tcgen05.mma of 128 x 128 x 16 per slot and tile,
+//     512 cycles for each product (measured, the unit's full rate).
+//   * Softmax warps hold a row per thread: logits from tensor memory, weights
+//     back over them, no exchange between threads.  The reference is the
+//     first tile's maximum; later tiles go without theirs (see kMost).
+// Chunks of up to 128 rows have one query tile; its KV tiles alternate
+// between the slots, whose two results the epilogue joins.
+// Work is cut over the context into equal shares (the schedule below), so
+// few rows over a long context use every SM; a second kernel joins the parts.
+//
+// Measured: 2048 tokens over 8192 with 64 query and 8 KV heads (481 GFLOP)
+// 0.41 ms, 1176 TFLOP/s, 59 % of the measured bf16 rate; 500 over 131000 1.60
+// ms, 1336 TFLOP/s, 68 %.  The tensor cores are active half of the time on
+// the first (by their counter), and two slots are all that tensor memory
+// holds.  What bounds it is the softmax: with half of its exponentials left
+// out (wrong results, a copy of an earlier step) the second case took 1.34 ms
+// in place of 1.60, without the dequantisation's conversions 1.60 as before.
+// Alone, a softmax step of 128 x 128 takes 1200 cycles with one slot's warps
+// running and 1650 with both (the exponentials' unit takes one warp's in 4
+// cycles), and each hand-over between the units some 340 for both ways.
+// Sixteen softmax warps of half a row each were slower, 2.02 ms against 1.65.
+// 16 tokens of 32 sequences over 2000 to 4000: 0.115 ms for 0.13 GB.  Chunks
+// of a few tokens go through the decode kernel instead (short_chunk).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -584,8 +620,9 @@ __device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
 // queue hardly more than one instruction, so what a warp spends between two
 // batches of them (waits, commits) is hidden only by the other warp's.  Warps
 // 10 .. 15 (fillers) dequantise.
-// (An SM quarter holds the registers of four warps of 128: a 17th warp would
-// cost every warp a quarter of its registers.)
+// (16 warps of 128 registers fill the register file; a split of the registers
+// by role, softmax 176 and the others 80, was 2 % slower: 420 us against 411
+// at 2048 tokens over 8192.)
 constexpr int kSoftWarps = 8;
 constexpr int kFillers = 6;
 constexpr int kThreads = 32 * (kSoftWarps + 2 + kFillers);
@@ -604,7 +641,7 @@ enum Bar {
   kTurn = kODone + 2,          // [slot] the tensor cores are this slot's
   kOFree = kTurn + 2,          // the segment's output has been read
   kSegment = kOFree + 1,       // the next segment is in the ring
-  kLast = kSegment + 1,          // (a wait that gave up: products in flight)
+  kLast = kSegment + 1,        // (a wait that gave up: products in flight)
   kBars = kLast + 1
 };
 
@@ -798,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp < kSoftWarps) {
     // --- softmax ----------------------------------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    
     const int m = warp >> 2, row = tid & 127;
     const uint32_t lanes =
         tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -1033,8 +1070,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kOFree));
     }
-  } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
   }
   if (warp >= kSoftWarps + 2) {
     // --- dequantise: a quarter (32 tokens) of a tile's K or V at a time ------
@@ -1262,7 +1297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           goto done;
         // Two query tiles take turns with the rest: batches that ran side by
         // side would end side by side, and leave the tensor cores idle while
-        // both slots make their weights.
+        // both slots make their weights (1 % on long contexts).
         if (two && pv) {
           if (turns + m > 0 &&
               !warp_wait(bar(kTurn + m), (turns + m - 1) & 1, abort))
@@ -1332,7 +1367,9 @@ done:
     if (warp == kSoftWarps || warp == kSoftWarps + 1) {
       if (elect()) {
         mma_commit(bar(kLast));
-        for (int i = 0; i < 1 << 20 && !mbar_try(bar(kLast), 0); ++i) {
+        const uint64_t start = dev::global_ns();
+        while (!mbar_try(bar(kLast), 0) &&
+               dev::global_ns() - start < KVQ_WAIT_LIMIT_NS) {
         }
         flag(p.dev_error, KVQ_DEVERR_TIMEOUT);
       }
@@ -1425,7 +1462,11 @@ int64_t chunk_workspace_bytes(int sms) {
 
 // Short chunks go token by token through the decode kernel, which walks the
 // context once for every token, but at three times the speed of a tile of
-// 128 rows that is mostly padding, and with nothing to set up.
+// 128 rows that is mostly padding, and with nothing to set up: 200 single
+// tokens over 512 to 2560 tokens of context 73 us against 391 us by tiles,
+// five tokens of 8 sequences 25 us against 34 us.  Up to four tokens always,
+// up to eight where there are no more than one (sequence, KV head) per SM;
+// single tokens beside longer chunks too.
 static int short_chunk(const ChunkParams& p) {
   if (p.max_q_len <= 4) return p.max_q_len > 1 ? p.max_q_len : 1;
   const bool few = static_cast<int64_t>(p.num_seqs) * p.Hkv <= sm_count();
@@ -1445,7 +1486,7 @@ cudaError_t launch_chunk_attention(const ChunkParams& caller,
       (parts > 1 && cells * (kD + 2) * 4 > chunk_workspace_bytes(sm_count())))
     p.skip = 0;
   cudaError_t err = cudaSuccess;
-  const bool tiles = p.max_q_len > p.skip;
+  const bool tiles = p.skip == 0 || p.max_q_len > p.skip;
   if (tiles)
     err = p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
   if (err != cudaSuccess || p.skip == 0) return err;
