@@ -531,6 +531,11 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
                  dev_error)
     if workspace is None:
         workspace = chunk_attention_workspace(query.device)
+        if stream is not None and stream != here:
+            # (not to be handed out again before that stream is past it)
+            workspace.record_stream(torch.cuda.ExternalStream(
+                stream, device=query.device) if stream else
+                torch.cuda.default_stream(query.device))
     if not workspace.is_contiguous():
         raise KvqError(fn, KVQ_ERR_SHAPE)
     st = lib().kvq_chunk_attention_nvfp4(

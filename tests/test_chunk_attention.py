@@ -398,6 +398,23 @@ def test_graph_streams_and_workspaces():
         assert torch.equal(c.out, w)
 
 
+def test_own_workspace_on_another_stream():
+    """A workspace that the call allocates is not handed out again while a
+    stream given by its handle still uses it."""
+    c = Case([300], [5000], hq=8, hkv=1, seed=77).upload()
+    size = kvq.chunk_attention_workspace().numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    c.call(stream=side.cuda_stream)
+    other = [torch.full((size,), 0, dtype=torch.uint8, device="cuda")
+             for _ in range(2)]
+    torch.cuda.synchronize()
+    c.check(c.out.double().cpu().numpy())
+    assert all(int(x.max()) == 0 for x in other)
+
+
 def test_pdl_chain():
     """Store, then chunk attention, launched with dependent launch, many
     times over."""
