@@ -630,8 +630,8 @@ kvq_status kvq_copy_pages(uint8_t* const* caches, int32_t num_caches,
   const int piece = copy_piece_bytes(vec32);
   const int64_t pieces = (page_bytes + piece - 1) / piece;
   // one launch's warps stay below 2^31 (and its CTAs far below the limit)
-  if (pieces * num_pairs >=
-      (int64_t{1} << 31) / std::min(num_caches, kMaxCaches))
+  if (pieces >= (int64_t{1} << 31) / std::min(num_caches, kMaxCaches) /
+                    num_pairs)
     return KVQ_ERR_SHAPE;
   p.pieces = static_cast<int32_t>(pieces);
   for (int32_t first = 0; first < num_caches; first += kMaxCaches) {

@@ -152,6 +152,7 @@ def ptrs(*addresses):
     (dict(dst=A + 2), ALIGN), (dict(page_stride=584), ALIGN),
     (dict(page_bytes=568), ALIGN),
     (dict(pairs=1 << 30, page_bytes=1 << 20, page_stride=1 << 20), SHAPE),
+    (dict(pairs=1 << 17, page_bytes=1 << 58, page_stride=1 << 58), SHAPE),
     (dict(n=0, caches=None), kvq.KVQ_OK),
     (dict(pairs=0, src=None), kvq.KVQ_OK)])
 def test_copy_pages(lib, kw, code):
