@@ -631,7 +631,7 @@ kvq_status kvq_free_sequences(int32_t* ref_count, int64_t num_blocks,
  * caches (any layout: the bytes are copied).
  *
  * caches         HOST array of num_caches device pointers, page 0 of each,
- *                16-byte aligned; read during the call.
+ *                16-byte aligned, all different; read during the call.
  * page_bytes     bytes of a page, page_stride bytes from page to page;
  *                multiples of 16, 0 < page_bytes <= page_stride.
  * src_pages, dst_pages  int32 [num_pairs], device.  A pair with a negative
@@ -654,7 +654,8 @@ kvq_status kvq_copy_pages(uint8_t* const* caches, int32_t num_caches,
  * caches.  Bytes of other tokens are left as they are.
  *
  * caches         HOST array of num_caches device pointers, page 0 of the K
- *                side of each, 16-byte aligned; read during the call.
+ *                side of each, 16-byte aligned, all different; read during
+ *                the call.
  * value_offset   bytes from a cache's K side to its V side (multiple of 16,
  *                >= H*B*(D/2 + S)); page_stride, num_blocks, block_size,
  *                layout, num_heads, head_size (<= 8192) as for
@@ -673,8 +674,8 @@ kvq_status kvq_copy_pages(uint8_t* const* caches, int32_t num_caches,
  *                kvq_compact_sequences satisfy it.
  * flags          KVQ_F_SWIZZLE_K_SCALE, KVQ_F_PDL, or 0.
  * num_caches, num_lists or total_moves == 0 returns KVQ_OK without
- * launching.  One list is walked in order by one thread block per cache,
- * head and side: long work comes as several lists or caches.
+ * launching.  One list is walked in order by one thread block per cache and
+ * (up to) four heads: long work comes as several lists or caches.
  */
 kvq_status kvq_move_tokens_nvfp4(
     uint8_t* const* caches, int32_t num_caches, int64_t value_offset,

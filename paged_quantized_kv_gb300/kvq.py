@@ -708,6 +708,9 @@ def _cache_list(fn: str, caches, dims: int):
         if len(shape) < dims:
             raise KvqError(fn, KVQ_ERR_SHAPE)
         ptrs = [t.data_ptr() for t in tensors]
+        # (one cache twice: its tokens would be moved twice, at once)
+        if n > 1 and shape[0] != 0 and len(set(ptrs)) < n:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
     # a page's bytes lie together
     page = 1
     for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):

@@ -286,6 +286,7 @@ def test_binding_moves(lib):
         (([kv], i32(3), i64(3), i32(2)), {}, kvq.KVQ_ERR_DTYPE),
         (([kv], i64(3), i64(3), i64(2)), {}, kvq.KVQ_ERR_DTYPE),
         (([kv], i64(3), i64(3), i32(2)), dict(layout=3), kvq.KVQ_ERR_LAYOUT),
+        (([kv, kv], i64(3), i64(3), i32(2)), {}, SHAPE),
         (([kv[:, 0]], i64(3), i64(3), i32(2)), {}, SHAPE),
         (([kv[..., :32]], i64(3), i64(3), i32(2)), {}, SHAPE),
     ]:
