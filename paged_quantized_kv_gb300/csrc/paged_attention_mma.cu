@@ -190,8 +190,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Rows
 // ---------------------------------------------------------------------------
 // Row b of a launch: its query and output row, its sequence (block-table
-// row) and its context length.  A decode step's row b is sequence b.  With
-// p.cu it is new token b % per_seq of sequence b / per_seq, which sees the
+// row) and its context length.  A decode step's row b is sequence b.  In a
+// launch for chunks (kChunk) it is new token b % per_seq of sequence b / per_seq, which sees the
 // context up to itself; a token that the sequence does not have, or whose
 // sequence has more than per_seq of them, is none (live false).
 struct Row {
@@ -200,9 +200,10 @@ struct Row {
   bool live, bad;  // bad: lengths or offsets out of range
 };
 
+template <bool kChunk>
 __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
   Row r = {b, b, 0, true, false};
-  if (p.cu == nullptr) {
+  if constexpr (!kChunk) {
     r.L = __ldg(p.lens + b);
     r.bad = r.L < 0 || r.L > p.len_cap;
     r.L = max(0, min(r.L, p.len_cap));
@@ -224,8 +225,9 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
 }
 
 // Whether a row has weights: a row of a chunk whose weights are NaN has.
-__device__ __forceinline__ bool has_weights(const AttnParams& p, float den) {
-  return den > 0.f || (p.cu != nullptr && den != den);
+template <bool kChunk>
+__device__ __forceinline__ bool has_weights(float den) {
+  return den > 0.f || (kChunk && den != den);
 }
 
 // ---------------------------------------------------------------------------
@@ -432,9 +434,9 @@ constexpr float kLazy = 8.0f;
 // bands); 9, 10 = 1, 3 with block_size 8 (linear K scales): 8-token piece
 // j of step i is block 4i + j, and a stretch is kPartB8 tokens long, so
 // that a warp's range spans at most 64 blocks.
-// Chunks of a few new tokens run here too (p.cu set), each token as a row of
+// Chunks of a few new tokens run here too (kChunk), each token as a row of
 // its own: see row_of.
-template <int NG, bool kF16, int kPages>
+template <int NG, bool kF16, int kPages, bool kChunk>
 __global__ void __launch_bounds__(kThreads, NG == 8 ? 4 : 3)
 paged_attention_mma_kernel(const AttnParams p) {
   constexpr bool kB8 = kPages >= 9;
@@ -463,7 +465,7 @@ paged_attention_mma_kernel(const AttnParams p) {
   const bool early = p.early_meta;
   if (!early) pdl_prologue();
 
-  const Row me = row_of(p, b);
+  const Row me = row_of<kChunk>(p, b);
   const int L = me.L;
   const bool bad_len = me.bad;
   // flags a clamped length (once per sequence); a write, so after the wait
@@ -474,7 +476,7 @@ paged_attention_mma_kernel(const AttnParams p) {
   };
   // stretch length: fixed on contiguous pages (the host sets p.part to it),
   // but for chunks' rows
-  const int S = kContig && p.cu == nullptr
+  const int S = kContig && !kChunk
                     ? (kB8 ? kPartB8 : KVQ_ATTN_MMA_PART)
                     : p.part;
   const int nparts = (L + S - 1) / S;
@@ -1162,7 +1164,7 @@ paged_attention_mma_kernel(const AttnParams p) {
       fw[w] = ex2(mw[w] - M);
       den += wbuf[w][16 * kMergeRow + 16 + hh] * fw[w];
     }
-    const bool live = has_weights(p, den);
+    const bool live = has_weights<kChunk>(den);
     const float inv = live ? 1.0f / den : 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), c = a;
 #pragma unroll
@@ -1225,7 +1227,7 @@ constexpr int kMergeRows = kMergeThreads / 16;
 // Rows of at most this many partitions issue all their loads at once.
 constexpr int kMergeFew = 4;
 
-template <bool kF16>
+template <bool kF16, bool kChunk>
 __global__ void __launch_bounds__(kMergeThreads)
 attention_merge_kernel(const AttnParams p) {
   const int sub = threadIdx.x & 15;  // dims 8 sub .. 8 sub + 7
@@ -1235,7 +1237,7 @@ attention_merge_kernel(const AttnParams p) {
   const int b = live ? static_cast<int>(row / p.Hq) : 0;
   const int h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.Hq)
                      : 0;
-  const Row me = live ? row_of(p, b) : Row{0, 0, 0, false, false};
+  const Row me = live ? row_of<kChunk>(p, b) : Row{0, 0, 0, false, false};
   pdl_prologue();
   const int L = me.live ? me.L : 0;
   const int nparts = (L + p.part - 1) / p.part;
@@ -1280,7 +1282,7 @@ attention_merge_kernel(const AttnParams p) {
           src[1]);
     }
   }
-  const bool some = has_weights(p, den);
+  const bool some = has_weights<kChunk>(den);
   const float f = some ? 1.0f / den : 0.f;
   const float vs = __ldg(p.v_scale);
   uint32_t packed[4];
@@ -1295,10 +1297,10 @@ attention_merge_kernel(const AttnParams p) {
       make_uint4(packed[0], packed[1], packed[2], packed[3]);
 }
 
-template <int NG, bool kF16, int kPages>
-cudaError_t launch_mma(const AttnParams& caller, cudaStream_t stream) {
+template <int NG, bool kF16, int kPages, bool kChunk>
+cudaError_t launch_form_of(const AttnParams& caller, cudaStream_t stream) {
   constexpr bool kContig = kPages != 0;
-  auto kernel = paged_attention_mma_kernel<NG, kF16, kPages>;
+  auto kernel = paged_attention_mma_kernel<NG, kF16, kPages, kChunk>;
   // A CTA may cover a longer partition than the caller's (fewer, longer
   // warp ranges; the scratch rows keep the caller's max_parts stride and
   // need fewer entries).  A warp range spans at most 64 blocks on
@@ -1308,7 +1310,7 @@ cudaError_t launch_mma(const AttnParams& caller, cudaStream_t stream) {
   if (kContig) {
     const int most = kPages >= 9 ? kPartB8 : KVQ_ATTN_MMA_PART;
     p.part = most;
-    if (p.cu != nullptr) {
+    if constexpr (kChunk) {
       const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.Hkv;
       const int64_t want = static_cast<int64_t>(kChunkCtas) * sm_count();
       while (p.part > 512 &&
@@ -1339,6 +1341,13 @@ cudaError_t launch_mma(const AttnParams& caller, cudaStream_t stream) {
                       p);
   if (err != cudaSuccess || parts <= 1) return err;
   return launch_attention_merge(p, stream);
+}
+
+template <int NG, bool kF16, int kPages>
+cudaError_t launch_mma(const AttnParams& p, cudaStream_t stream) {
+  return p.cu != nullptr
+             ? launch_form_of<NG, kF16, kPages, true>(p, stream)
+             : launch_form_of<NG, kF16, kPages, false>(p, stream);
 }
 
 template <int NG, bool kF16, int kSwz>
@@ -1378,10 +1387,13 @@ cudaError_t launch_layout(const AttnParams& p, cudaStream_t stream) {
 cudaError_t launch_attention_merge(const AttnParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.Hq;
   const dim3 grid(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
-  return p.f16 ? launch_kernel(attention_merge_kernel<true>, grid,
-                               kMergeThreads, 0, stream, true, p)
-               : launch_kernel(attention_merge_kernel<false>, grid,
-                               kMergeThreads, 0, stream, true, p);
+  auto kernel =
+      p.cu != nullptr
+          ? (p.f16 ? attention_merge_kernel<true, true>
+                   : attention_merge_kernel<false, true>)
+          : (p.f16 ? attention_merge_kernel<true, false>
+                   : attention_merge_kernel<false, false>);
+  return launch_kernel(kernel, grid, kMergeThreads, 0, stream, true, p);
 }
 
 cudaError_t launch_paged_attention_mma(const AttnParams& p,
