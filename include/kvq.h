@@ -675,7 +675,7 @@ kvq_status kvq_copy_pages(uint8_t* const* caches, int32_t num_caches,
  * flags          KVQ_F_SWIZZLE_K_SCALE, KVQ_F_PDL, or 0.
  * num_caches, num_lists or total_moves == 0 returns KVQ_OK without
  * launching.  One list is walked in order by one thread block per cache and
- * (up to) four heads: long work comes as several lists or caches.
+ * (up to) two heads: long work comes as several lists or caches.
  */
 kvq_status kvq_move_tokens_nvfp4(
     uint8_t* const* caches, int32_t num_caches, int64_t value_offset,

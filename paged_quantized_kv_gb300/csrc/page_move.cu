@@ -2,8 +2,13 @@
 // whole pages (kvq_copy_pages) and single NVFP4 tokens
 // (kvq_move_tokens_nvfp4), in many caches (a model's layers) at once.
 //
-// Both read and write every byte once and compute nothing: they are bound
-// by HBM bandwidth, and for a few pages by the launch.
+// Both read and write every byte once and compute nothing.  Measured: copies
+// of 1.47 GB (read and written) 216 us, 6.8 TB/s, the HBM's rate; 2.2 us for
+// a few pages, the launch's time.  Moves of 2.26 GB in an eviction round 433
+// us with the state's two calls, 5.2 TB/s: bound by the memory's latency (a
+// step's reads, barrier, writes), which more warps per SM cover best (see
+// there), and by scales, whose 8 bytes per token and side are a quarter of
+// the sector that they move (1.5 times the bytes written, by L2's counter).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -104,16 +109,19 @@ __global__ void __launch_bounds__(kCopyThreads)
 // is written.  A thread moves the 16-byte piece c of its token's rows (32
 // elements) with its two group scales, K and V, of kHeads heads: what the
 // slots cost (two divisions, the page's address) is spent once for 2 kHeads
-// pieces, and with one head per CTA is what bounds the kernel (668 us
-// against 338 us of HBM time for 2.26 GB).  A step has kTokens tokens per
-// thread, so that kHeads * kTokens = 4 loads of each side are in flight.
+// pieces.  A step has kTokens tokens per thread.  What bounds it is the wait
+// for memory between a step's barriers (with four heads at three CTAs per SM
+// the schedulers issued in 30 % of the cycles), so that warps matter most: a
+// round of 2.26 GB by 4 heads at 3 CTAs per SM 511 us, at 4 457; by 2 heads
+// at 5 433 (at 6, with spills, 445); by 1 head at 6 446.  Reading a step
+// ahead takes more registers than it gives: 2 heads at 4 466, 4 heads 586.
 // A V scale (and a swizzled K scale) of group j of a token at offset r of
 // its 4-token band is byte 4j + r of the band's head tile, whose 4 rows are
 // scale-row strides apart.
 constexpr int kMoveThreads = 256;
 
-template <int kHeads, int kTokens>
-__global__ void __launch_bounds__(kMoveThreads)
+template <int kHeads, int kTokens, int kCtas>
+__global__ void __launch_bounds__(kMoveThreads, kCtas)
     move_tokens_kernel(const __grid_constant__ MoveParams p) {
   pdl_prologue();
   const int i = blockIdx.x;  // list
@@ -208,10 +216,10 @@ __global__ void __launch_bounds__(kMoveThreads)
   }
 }
 
-template <int kHeads, int kTokens>
+template <int kHeads, int kTokens, int kCtas>
 cudaError_t launch_move(const MoveParams& p, cudaStream_t stream) {
   return launch_kernel(
-      move_tokens_kernel<kHeads, kTokens>,
+      move_tokens_kernel<kHeads, kTokens, kCtas>,
       dim3(p.num_lists, (p.H + kHeads - 1) / kHeads, p.num_caches),
       kMoveThreads, 0, stream, p.pdl, p);
 }
@@ -232,15 +240,16 @@ cudaError_t launch_copy_pages(const CopyParams& p, bool vec32,
 
 int copy_piece_bytes(bool vec32) { return kUnroll * 32 * (vec32 ? 32 : 16); }
 
-// Four heads to a CTA, fewer where the SMs would not all have two CTAs.
+// One head to a CTA (four tokens deep, three CTAs per SM) while all of those
+// run at once, else two heads (one token, five per SM).  Measured with 16
+// lists of 8 heads, with the state's calls before: 384 CTAs of one head 93 us
+// against 121 by two heads, 512 130 against 125, 2048 300 against 264.
 cudaError_t launch_move_tokens(const MoveParams& p, cudaStream_t stream) {
-  const int64_t lists = static_cast<int64_t>(p.num_lists) * p.num_caches;
-  const int64_t want = 2 * sm_count();
-  if (p.H >= 4 && lists * ((p.H + 3) / 4) >= want)
-    return launch_move<4, 1>(p, stream);
-  if (p.H >= 2 && lists * ((p.H + 1) / 2) >= want)
-    return launch_move<2, 2>(p, stream);
-  return launch_move<1, 4>(p, stream);
+  const int64_t ctas =
+      static_cast<int64_t>(p.num_lists) * p.num_caches * p.H;
+  return p.H == 1 || ctas <= 3 * sm_count()
+             ? launch_move<1, 4, 3>(p, stream)
+             : launch_move<2, 1, 5>(p, stream);
 }
 
 }  // namespace kvq

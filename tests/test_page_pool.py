@@ -396,6 +396,42 @@ def test_move_tokens(nhd, swz, block, heads, D):
     assert int(err.item()) == bits == 1
 
 
+@pytest.mark.parametrize("nhd", [False, True], ids=["HND", "NHD"])
+@pytest.mark.parametrize("swz", [False, True])
+@pytest.mark.parametrize("heads,D", [(2, 128), (3, 64), (5, 128), (1, 64)])
+def test_move_tokens_many_lists(nhd, swz, heads, D):
+    """More thread blocks than run at once: heads go in pairs, the last one
+    alone where their number is odd.  Every list compacts four pages of its
+    own in place, of none to all of their tokens."""
+    rng = np.random.default_rng(heads)
+    block, lists, layers = 8, 300, 2
+    nb = 4 * lists
+    models = [Pages(nb, block, heads, D, nhd, swz) for _ in range(layers)]
+    for m in models:
+        m.data[:] = rng.integers(0, 256, m.data.shape)
+    shape = (block, heads) if nhd else (heads, block)
+    t = [dev(m.data, torch.uint8).view(nb, 2, *shape, D // 2 + D // 16)
+         for m in models]
+    perm = rng.permutation(nb)
+    src, dst, cu = [], [], [0]
+    for i in range(lists):
+        table = perm[4 * i:4 * i + 4]
+        keep = np.nonzero(rng.random(4 * block) < (i % 5) / 4)[0]
+        j = np.arange(len(keep))
+        src += (table[keep // block] * block + keep % block).tolist()
+        dst += (table[j // block] * block + j % block).tolist()
+        cu.append(len(src))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kvq.kvq_move_tokens_nvfp4(
+        t, dev(src, torch.int64), dev(dst, torch.int64), dev(cu),
+        layout=kvq.KVQ_LAYOUT_NHD if nhd else kvq.KVQ_LAYOUT_HND,
+        flags=kvq.KVQ_F_SWIZZLE_K_SCALE if swz else 0, dev_error=err)
+    for m, x in zip(models, t):
+        want, bits = move_tokens(m, src, dst)
+        assert np.array_equal(x.cpu().numpy().reshape(want.shape), want)
+    assert int(err.item()) == 0
+
+
 def test_move_tokens_bad_lists():
     m = Pages(6, 4, 1).fill(np.random.default_rng(0))
     t = dev(m.data, torch.uint8).view(6, 2, 1, 4, 72)
