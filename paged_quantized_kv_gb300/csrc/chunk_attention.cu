@@ -24,12 +24,12 @@
 // few rows over a long context use every SM; a second kernel joins the parts.
 //
 // Measured: 2048 tokens over 8192 with 64 query and 8 KV heads (481 GFLOP)
-// 0.41 ms, 1176 TFLOP/s, 59 % of the measured bf16 rate; 500 over 131000 1.60
-// ms, 1336 TFLOP/s, 68 %.  The tensor cores are active half of the time on
+// 0.40 ms, 1196 TFLOP/s, 61 % of the measured bf16 rate; 500 over 131000 1.53
+// ms, 1396 TFLOP/s, 71 %.  The tensor cores are active half of the time on
 // the first (by their counter), and two slots are all that tensor memory
 // holds.  What bounds it is the softmax: with half of its exponentials left
 // out (wrong results, a copy of an earlier step) the second case took 1.34 ms
-// in place of 1.60, without the dequantisation's conversions 1.60 as before.
+// where that step took 1.60, without the dequantisation's conversions 1.60.
 // Alone, a softmax step of 128 x 128 takes 1200 cycles with one slot's warps
 // running and 1650 with both (the exponentials' unit takes one warp's in 4
 // cycles), and each hand-over between the units some 340 for both ways.
@@ -621,8 +621,8 @@ __device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
 // batches of them (waits, commits) is hidden only by the other warp's.  Warps
 // 10 .. 15 (fillers) dequantise.
 // (16 warps of 128 registers fill the register file; a split of the registers
-// by role, softmax 176 and the others 80, was 2 % slower: 420 us against 411
-// at 2048 tokens over 8192.)
+// by role, softmax 176 and the others 80, was 2 % slower, 420 us against 411
+// at 2048 tokens over 8192, halves of the softmax not unrolled.)
 constexpr int kSoftWarps = 8;
 constexpr int kFillers = 6;
 constexpr int kThreads = 32 * (kSoftWarps + 2 + kFillers);
@@ -834,8 +834,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncwarp();
 
   if (warp < kSoftWarps) {
-    // --- softmax ----------------------------------------------------------------
-    
+    // --- softmax ------------------------------------------------------------
     const int m = warp >> 2, row = tid & 127;
     const uint32_t lanes =
         tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -912,7 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // that fails the half is done over, with its maximum for the new
         // reference.  The product of the first half with V begins while the
         // second is made.
-#pragma unroll 1
+        // (Unrolled: 500 tokens over 131000 1.53 ms against 1.61.)
+#pragma unroll
         for (int half = 0; half < 2; ++half) {
           bool look = kt == kt0 && half == 0;
           uint32_t s[64];
@@ -973,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(bar(kPFull + 2 * m + half));
         }
       }
-      // --- epilogue ---------------------------------------------------------------
+      // --- epilogue ---------------------------------------------------------
       const int n = kv1 - kv0;
       cnt0 += two ? n : (n + 1) >> 1;
       cnt1 += two ? n : n >> 1;
