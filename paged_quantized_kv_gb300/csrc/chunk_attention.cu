@@ -627,6 +627,14 @@ constexpr int kSoftWarps = 8;
 constexpr int kFillers = 6;
 constexpr int kThreads = 32 * (kSoftWarps + 2 + kFillers);
 constexpr int kStages = 2;
+// Barriers that announce segments, taken in turn.  With one, slot 1's softmax
+// warps could miss a phase: a product warp announces segment s + 2 once slot
+// 0's query of s + 1 is there, while slot 1's warps may still be in the
+// epilogue of s, and then wait for s + 1 by the parity that s + 2 has turned
+// back (many short items, or a short one behind one of two query tiles: the
+// waits gave up).  Segment s + 3 is announced only behind slot 1's warps'
+// part in s + 1: two are enough.
+constexpr int kAnnounced = 2;
 
 enum Bar {
   kKFull = 0,                  // [stage] a tile of K is in shared memory
@@ -640,8 +648,8 @@ enum Bar {
   kODone = kPDone + 2,         // [slot] all of them are
   kTurn = kODone + 2,          // [slot] the tensor cores are this slot's
   kOFree = kTurn + 2,          // the segment's output has been read
-  kSegment = kOFree + 1,       // the next segment is in the ring
-  kLast = kSegment + 1,        // (a wait that gave up: products in flight)
+  kSegment = kOFree + 1,       // [segment % kAnnounced] it is in the ring
+  kLast = kSegment + kAnnounced,  // (a wait that gave up: products in flight)
   kBars = kLast + 1
 };
 
@@ -721,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kODone + m), 1);
     }
     mbar_init(bar(kOFree), kSoftWarps);
-    mbar_init(bar(kSegment), 2);
+    for (int i = 0; i < kAnnounced; ++i) mbar_init(bar(kSegment + i), 2);
     mbar_init(bar(kLast), 2);
     misc[0] = 0;
     misc[2] = 0;
@@ -844,7 +852,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = c0 != 0.0f ? fabsf(c0) * kLog2e : 1.0f;
     uint32_t cnt0 = 0, cnt1 = 0;  // tiles of the slots so far
     for (uint32_t seg = 0; any; ++seg) {
-      if (seg > 0 && !warp_wait(bar(kSegment), (seg - 1) & 1, abort))
+      if (seg > 0 && !warp_wait(bar(kSegment + seg % kAnnounced),
+                                (seg - 1) / kAnnounced & 1, abort))
         goto done;
       if (seg > 0 && !ring[seg & 3].there) break;
       int kv0, kv1, pos, tiles, rows;
@@ -1345,7 +1354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // (from both warps: no query of the next segment is announced
             // before both have seen this one's)
-            mbar_arrive(bar(kSegment));
+            mbar_arrive(bar(kSegment + (segs + 1) % kAnnounced));
           }
           __syncwarp();
         }

@@ -1,0 +1,42 @@
+"""The barriers of the chunk attention's tile kernel in a model (no GPU),
+with the ring sizes that the kernel's source has."""
+import os
+import re
+
+import pytest
+
+from paged_quantized_kv_gb300 import build as kbuild
+from tests.chunk_protocol import random_run
+
+with open(os.path.join(kbuild.CSRC, "chunk_attention.cu")) as f:
+    SOURCE = f.read()
+
+
+def ring(name, default):
+    """A ring's size in the kernel; a kernel without the constant has
+    `default`."""
+    found = re.search(rf"constexpr int {name} = (\d+);", SOURCE)
+    return int(found.group(1)) if found else default
+
+
+def faults(kinds, empties, announcements, runs):
+    out = {}
+    for seed in range(runs):
+        for x in random_run(seed, empties, announcements):
+            if x[0] in kinds or x[1] in kinds:
+                out.setdefault(x[:2], (seed, x))
+    return out
+
+
+def test_announced_segments_are_not_missed():
+    """Slot 1's softmax warps may still be in the last segment's epilogue
+    when the one behind the next is announced."""
+    found = faults(("missed", "stuck"), ring("kEmpties", 2),
+                   ring("kAnnounced", 1), 1500)
+    assert not {k: v for k, v in found.items()
+                if k[0] == "missed" and "segment" in k[1]}
+
+
+def test_the_model_finds_a_single_announcement_barrier():
+    found = faults(("missed",), 4, 1, 60)
+    assert ("missed", "segment[0]") in found
