@@ -627,6 +627,14 @@ constexpr int kSoftWarps = 8;
 constexpr int kFillers = 6;
 constexpr int kThreads = 32 * (kSoftWarps + 2 + kFillers);
 constexpr int kStages = 2;
+// Barriers that say that a tile's products are done, taken in turn by the
+// tiles.  A filler has no quarter of K and V both in every tile and so does
+// not look at every phase.  By a barrier for each stage it could take tile
+// t - 4's product with V, still running for one slot while the other was
+// ahead, for that of t - 2, and fill the tile under it.  With four barriers
+// the one that it waits on last stood for tile t - 6, which was done before
+// whatever the filler waited for at t - 2, where it had work.
+constexpr int kEmpties = 4;
 // Barriers that announce segments, taken in turn.  With one, slot 1's softmax
 // warps could miss a phase: a product warp announces segment s + 2 once slot
 // 0's query of s + 1 is there, while slot 1's warps may still be in the
@@ -638,10 +646,10 @@ constexpr int kAnnounced = 2;
 
 enum Bar {
   kKFull = 0,                  // [stage] a tile of K is in shared memory
-  kKEmpty = kKFull + kStages,  // [stage] its products are done
-  kVFull = kKEmpty + kStages,
+  kKEmpty = kKFull + kStages,  // [tile % kEmpties] its products are done
+  kVFull = kKEmpty + kEmpties,
   kVEmpty = kVFull + kStages,
-  kQFull = kVEmpty + kStages,  // [slot] the query rows are in shared memory
+  kQFull = kVEmpty + kEmpties,  // [slot] the query rows are in shared memory
   kSFull = kQFull + 2,         // [slot] logits are in tensor memory
   kPFull = kSFull + 2,         // [slot][half] weights are in tensor memory
   kPDone = kPFull + 4,         // [slot] the first half is multiplied with V
@@ -665,7 +673,7 @@ constexpr int kBarAt = kRawAt + kFillers * kRawBytes;
 // Per tile and quarter: the tokens that are not left out ([8][4] words).  K
 // of tile k waits for the logits of tile k - 2, whose product is issued after
 // the weights of tile k - 4 at the latest: eight entries are enough.
-constexpr int kValidAt = kBarAt + 8 * 28;
+constexpr int kValidAt = kBarAt + 8 * 32;
 // Per segment, group and quarter: the first token whose V scale is NaN
 // ([8][8][4] ints).  V of tile k waits for tile k - 2's product with V, and
 // that one for the epilogues of all segments before its own: when segment s
@@ -684,7 +692,7 @@ constexpr int kWalkAt = kRingAt + 4 * static_cast<int>(sizeof(Walk));
 constexpr int kSmemBytes =
     kWalkAt + (kFillers + 2) * static_cast<int>(sizeof(Walk)) + 1024;
 static_assert(kSmemBytes <= 227 * 1024 && kRawBytes % 16 == 0 &&
-                  kBars <= 28 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
+                  kBars <= 32 && kValidAt % 16 == 0 && kUnitsAt % 8 == 0 &&
                   sizeof(Walk) % 8 == 0,
               "");
 // Tensor memory: logits (and, over them, weights) of the two slots, outputs
@@ -715,9 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(kKFull + s), 4);
-      mbar_init(bar(kKEmpty + s), 2);
       mbar_init(bar(kVFull + s), 4);
-      mbar_init(bar(kVEmpty + s), 2);
+    }
+    for (int t = 0; t < kEmpties; ++t) {
+      mbar_init(bar(kKEmpty + t), 2);
+      mbar_init(bar(kVEmpty + t), 2);
     }
     for (int m = 0; m < 2; ++m) {
       mbar_init(bar(kQFull + m), 4);
@@ -1191,14 +1201,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     after = issue(1);
     for (uint32_t slot = 0; next.some; slot ^= 1) {
       const int stage = next.cnt & 1;
-      const uint32_t phase = (next.cnt >> 1) & 1;
       const bool is_v = next.job >= 4, in = next.in, first = next.first;
       const int quarter = next.job & 3, cur_pos = next.pos;
       const bool swz = is_v || p.swizzle_k;
       const uint32_t mask = next.mask, cur = next.cnt, cur_seg = next.seg;
       asm volatile("cp.async.wait_group 1;" ::: "memory");
-      if (!warp_wait(bar((is_v ? kVEmpty : kKEmpty) + stage), phase ^ 1,
-                     abort))
+      // (of the tile before in this stage; a barrier as it was made counts as
+      // one whose phase 1 is over: the first two tiles wait for nothing)
+      const uint32_t old = cur - kStages;
+      if (!warp_wait(bar((is_v ? kVEmpty : kKEmpty) + old % kEmpties),
+                     old / kEmpties & 1, abort))
         goto done;
       const uint32_t from = raw + slot * kRawSlot;
       const uint2 sc = lds64(from + 2048 - 8 * lane);
@@ -1322,8 +1334,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int x = 4; x < 8; ++x)
               mma_ts(o_at, s_at + 8 * x, v + x * (2048 >> 4), kIdescBmn, 1);
             mma_commit(bar(kODone + m));
-            mma_commit(bar(kVEmpty + (tv & 1)));
-            if (!two) mma_commit(bar(kVEmpty + (tv & 1)));
+            mma_commit(bar(kVEmpty + tv % kEmpties));
+            if (!two) mma_commit(bar(kVEmpty + tv % kEmpties));
             if (two && !qk) mbar_arrive(bar(kTurn + 1 - m));
           }
           if (qk) {
@@ -1335,8 +1347,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (x == 4 && two && pv) mbar_arrive(bar(kTurn + 1 - m));
             }
             mma_commit(bar(kSFull + m));
-            mma_commit(bar(kKEmpty + (tk & 1)));
-            if (!two) mma_commit(bar(kKEmpty + (tk & 1)));
+            mma_commit(bar(kKEmpty + tk % kEmpties));
+            if (!two) mma_commit(bar(kKEmpty + tk % kEmpties));
           }
         }
         __syncwarp();

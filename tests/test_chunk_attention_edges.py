@@ -58,3 +58,29 @@ def test_shares_of_many_short_segments(seed):
                               [0, int(q[b])], c.lens[b:b + 1], KS, VS,
                               c.scale)
         c.check(got[at], ref, what=b)
+
+
+@pytest.mark.parametrize("slot", [0, 1])
+@pytest.mark.parametrize("G", [8, 16])
+def test_one_slot_far_behind_the_other(slot, G):
+    """Short chunks over long contexts, whose KV tiles alternate between the
+    slots: the logits grow from tile to tile of one slot only, so that its
+    weights are done over each time, and the other gets ahead."""
+    c = Case([12] * 5, [9000] * 5, hq=G, hkv=1, seed=G + slot)
+    cut = 16 * 64
+    c.pages.data[:, 0, :cut] = 0x22                      # every code 1.0
+    c.pages.data[:, 0, cut:] = 0x20                      # 2^-3
+    for row in c.table:
+        for j, page in enumerate(row[:9000 // 16]):
+            tile = j * 16 // 128
+            if tile % 2 == slot:
+                c.pages.data[page, 0, cut:] = 0x20 + min(tile, 0x28)
+    c.q = c.q.abs() * 0.5
+    c.check(c.run())
+    ws = kvq.chunk_attention_workspace()
+    c.call(workspace=ws)
+    want = c.out.clone()
+    for _ in range(50):
+        c.call(workspace=ws)
+        assert torch.equal(c.out, want)
+    assert int(c.err.item()) == 0

@@ -23,7 +23,7 @@ def faults(kinds, empties, announcements, runs):
     out = {}
     for seed in range(runs):
         for x in random_run(seed, empties, announcements):
-            if x[0] in kinds or x[1] in kinds:
+            if x[0] in kinds:
                 out.setdefault(x[:2], (seed, x))
     return out
 
@@ -40,3 +40,18 @@ def test_announced_segments_are_not_missed():
 def test_the_model_finds_a_single_announcement_barrier():
     found = faults(("missed",), 4, 1, 60)
     assert ("missed", "segment[0]") in found
+
+
+def test_tiles_are_not_filled_under_their_products():
+    """A filler that skips a phase of a tile ring's barrier must not take an
+    older one for its own."""
+    found = faults(("early", "K under its product", "V under its product",
+                    "V at its product"), ring("kEmpties", 2),
+                   ring("kAnnounced", 1), 1500)
+    assert not {k: v for k, v in found.items() if "o_done" not in str(k[1])}
+
+
+def test_the_model_finds_a_tile_filled_too_early():
+    found = faults(("early", "V under its product"), 2, 2, 60)
+    assert any(k[1].startswith("v_empty") for k in found)
+    assert any(k[0] == "V under its product" for k in found)
