@@ -1000,16 +1000,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (two) {
         if (!warp_wait(bar(kODone + m), (cnt - 1) & 1, abort)) goto done;
       } else {
-        // the slots' sums and references (a product of this segment with V
-        // is done, so every warp has read those of the last segment)
+        // The slots' sums and references (a product of this segment with V
+        // is done, so every warp has read those of the last segment).  Each
+        // slot's warps wait for its own last product: of the other slot's
+        // phases they have not looked at each, and could take an older one
+        // for this.  Behind the joint barrier that one is over, and the wait
+        // for it passes at once.
+        const bool both = n > 1;
+        const uint32_t last0 = cnt0 - 1, last1 = cnt1 - 1;
         float* x_sum = reinterpret_cast<float*>(smem + kSumAt) + row;
         float* x_ref = reinterpret_cast<float*>(smem + kRefAt) + row;
-        if (!warp_wait(bar(kODone), (cnt0 - 1) & 1, abort)) goto done;
-        if (n > 1 && !warp_wait(bar(kODone + 1), (cnt1 - 1) & 1, abort))
+        const int own = m == 1 && both;
+        if (!warp_wait(bar(kODone + own), (own ? last1 : last0) & 1, abort))
           goto done;
         x_sum[128 * m] = sum;
         x_ref[128 * m] = ref;
         bar_sync(1 + (warp & 3), 64);
+        if (both && !warp_wait(bar(kODone + 1 - own),
+                               (own ? last0 : last1) & 1, abort))
+          goto done;
         const float r0 = x_ref[0], r1 = x_ref[128];
         ref = fmaxf(r0, r1);
         w0 = r0 == ref ? 1.0f : ex2(r0 - ref);

@@ -34,10 +34,11 @@ class Model:
     segments."""
 
     def __init__(self, segments, seed, empties, announcements, slow=None,
-                 tail=30):
+                 tail=30, own_first=True):
         self.rng = random.Random(seed)
         self.segs, self.slow, self.tail = segments, slow or {}, tail
         self.depth, self.ann = empties, announcements
+        self.own_first = own_first
         self.now, self.queue, self.pushed, self.faults = 0, [], 0, []
         self.bars = {}
         for name, n, count in (
@@ -168,11 +169,18 @@ class Model:
 
     def join(self, m, w, n, tiles, s):
         who = f"softmax {m}.{w}"
-        yield self.wait("o_done", 0, tiles[0] - 1)
-        if n > 1:
+        # its own slot's last product, the joint barrier, the other slot's
+        # (or, as the model's alternative, both before it)
+        own = 1 if m == 1 and n > 1 else 0
+        if not self.own_first:
+            own = 0
+        yield self.wait("o_done", own, tiles[own] - 1)
+        if n > 1 and not self.own_first:
             yield self.wait("o_done", 1, tiles[1] - 1)
         self.check(not self.joining.get((w, 1 - m)), "sums written", who, s)
         yield ("pair", w, 2)
+        if n > 1 and self.own_first:
+            yield self.wait("o_done", 1 - own, tiles[1 - own] - 1)
         self.joining[w, m] = True
         yield self.takes(who, .3)
         self.joining[w, m] = False
@@ -258,7 +266,7 @@ class Model:
             self.arrive("v_full" if v else "k_full", t & 1)
 
 
-def random_run(seed, empties, announcements):
+def random_run(seed, empties, announcements, own_first=True):
     """A random share under random delays, some roles much slower."""
     rng = random.Random(seed)
     if rng.random() < .3:
@@ -270,4 +278,4 @@ def random_run(seed, empties, announcements):
     names += ["product 0", "product 1"] + [f"filler {f}" for f in range(6)]
     slow = {x: rng.choice([3, 10, 30]) for x in names if rng.random() < .15}
     return Model(segs, seed, empties, announcements, slow,
-                 rng.choice([0, 5, 30, 100])).run()
+                 rng.choice([0, 5, 30, 100]), own_first).run()

@@ -19,11 +19,12 @@ def ring(name, default):
     return int(found.group(1)) if found else default
 
 
-def faults(kinds, empties, announcements, runs):
+def faults(kinds, empties, announcements, runs, own_first=True):
+    """The kinds of fault (all for None) that random runs find."""
     out = {}
     for seed in range(runs):
-        for x in random_run(seed, empties, announcements):
-            if x[0] in kinds:
+        for x in random_run(seed, empties, announcements, own_first):
+            if kinds is None or x[0] in kinds:
                 out.setdefault(x[:2], (seed, x))
     return out
 
@@ -55,3 +56,16 @@ def test_the_model_finds_a_tile_filled_too_early():
     found = faults(("early", "V under its product"), 2, 2, 60)
     assert any(k[1].startswith("v_empty") for k in found)
     assert any(k[0] == "V under its product" for k in found)
+
+
+def test_no_fault_of_any_kind():
+    """Both slots' results are joined once each slot has waited for its own
+    last product; nothing is early, missed, stuck or overwritten."""
+    own_first = "kODone + own" in SOURCE
+    assert faults(None, ring("kEmpties", 2), ring("kAnnounced", 1), 3000,
+                  own_first) == {}
+
+
+def test_the_model_finds_a_wait_for_the_other_slot():
+    found = faults(("early",), 4, 2, 60, own_first=False)
+    assert found and all("o_done" in k[1] for k in found)
