@@ -57,6 +57,18 @@ constexpr int kTile = 2 * kHalf;           // a [128 x 128] fp16 tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 32768.0f;          // see the softmax
 
+// Test builds only: in three of four thread blocks one softmax warp, another
+// from block to block, gives up at the end of the first or second segment as
+// if its wait there had run out (0 in the library).
+#ifndef KVQ_TEST_GIVE_UP
+#define KVQ_TEST_GIVE_UP 0
+#endif
+__device__ __forceinline__ bool test_gives_up(int warp, uint32_t seg) {
+  return KVQ_TEST_GIVE_UP != 0 && blockIdx.x % 4 != 3 &&
+         warp == static_cast<int>(blockIdx.x * 3 % 8) &&
+         seg == blockIdx.x / 8 % 2;
+}
+
 // ---------------------------------------------------------------------------
 // tcgen05 helpers
 // ---------------------------------------------------------------------------
@@ -581,9 +593,10 @@ __device__ __noinline__ bool advance(const ChunkParams& p, Walk* walk) {
 
 // What the merge kernel needs of an item that begins in a CTA's share and
 // goes on in the next ones': partial results in this CTA's slot `slot` and
-// in slot 0 of the `more` CTAs behind it.
+// in slot 0 of the `more` CTAs behind it.  And whether a wait of this CTA
+// gave up: an item with a part of such a CTA is left out.
 struct Cut {
-  int32_t b, block, h, slot, more, pad[3];
+  int32_t b, block, h, slot, more, gave_up, pad[2];
 };
 constexpr int kMaxCtas = 512;
 constexpr int64_t kCutBytes = kMaxCtas * sizeof(Cut);
@@ -609,7 +622,7 @@ __device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
     end = share_begin(U, cta + more + 1, &ctas) - begin;
   } while (end < size && snap(static_cast<int>(end), size) < size);
   *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
-      w.b, w.block, w.h, w.seg > 0, more, {0, 0, 0}};
+      w.b, w.block, w.h, w.seg > 0, more, 0, {0, 0}};
 }
 
 // ---------------------------------------------------------------------------
@@ -679,7 +692,11 @@ constexpr int kValidAt = kBarAt + 8 * 32;
 // that one for the epilogues of all segments before its own: when segment s
 // is filled, those up to s - 3 are over.
 constexpr int kNanAt = kValidAt + 128;
-constexpr int kMiscAt = kNanAt + 1024;   // 16 ints
+// 16 ints: whether a wait gave up, the tensor memory's address, whether there
+// is a segment; from kJoined on, one per softmax warp: the segments whose
+// sums it has left for the other slot's warp.
+constexpr int kMiscAt = kNanAt + 1024;
+constexpr int kJoined = 4;
 constexpr int kScanAt = kMiscAt + 64;    // 32 int64
 constexpr int kUnitsAt = kScanAt + 256;  // 3 int64: all, share's end, begin
 constexpr int kSumAt = kUnitsAt + 32;    // [slot][row] floats
@@ -743,13 +760,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kLast), 2);
     misc[0] = 0;
     misc[2] = 0;
+    for (int w = 0; w < kSoftWarps; ++w) misc[kJoined + w] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid < 256) nan_at[tid] = INT32_MAX;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (tid == 0)  // nothing to join, unless the end of this CTA says so
-    (reinterpret_cast<Cut*>(p.workspace) + blockIdx.x)->more = 0;
+  Cut* const own_cut = reinterpret_cast<Cut*>(p.workspace) + blockIdx.x;
+  if (tid == 0)  // nothing to join, unless note_cut says so
+    own_cut->more = own_cut->gave_up = 0;
 
   // --- this CTA's share -----------------------------------------------------
   // inclusive scan of the sequences' units, kThreads of them at a time; with
@@ -997,6 +1016,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       cnt0 += two ? n : (n + 1) >> 1;
       cnt1 += two ? n : n >> 1;
       float w0 = 1.0f, w1 = 0.0f;
+      if (test_gives_up(warp, seg)) {
+        *abort = 1;
+        goto done;
+      }
       if (two) {
         if (!warp_wait(bar(kODone + m), (cnt - 1) & 1, abort)) goto done;
       } else {
@@ -1015,7 +1038,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           goto done;
         x_sum[128 * m] = sum;
         x_ref[128 * m] = ref;
+        // (a warp that has given up arrives at the end of the kernel, where
+        // it does not count: without its sums this one has no rows either)
+        if (lane == 0) misc[kJoined + warp] = static_cast<int>(seg) + 1;
         bar_sync(1 + (warp & 3), 64);
+        if (uniform(misc[kJoined + (warp ^ 4)]) <= static_cast<int>(seg))
+          goto gone;
         if (both && !warp_wait(bar(kODone + 1 - own),
                                (own ? last0 : last1) & 1, abort))
           goto done;
@@ -1389,9 +1417,15 @@ done:
   __syncwarp();
   if (*abort != 0) {
     asm volatile("cp.async.wait_all;" ::: "memory");
-    // whoever waits for this warp's rows goes on, to its own wait that gives
-    // up
+    // whoever waits for this warp's sums goes on, finds that they are not
+    // there and comes to no further barrier of this kind
     if (warp < kSoftWarps) bar_arrive(1 + (warp & 3), 64);
+  }
+gone:
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (*abort != 0) {  // (the same in every thread: all waits are over)
     // products in flight end by themselves; wait for them before the tensor
     // memory goes
     if (warp == kSoftWarps || warp == kSoftWarps + 1) {
@@ -1401,14 +1435,18 @@ done:
         while (!mbar_try(bar(kLast), 0) &&
                dev::global_ns() - start < KVQ_WAIT_LIMIT_NS) {
         }
-        flag(p.dev_error, KVQ_DEVERR_TIMEOUT);
       }
       __syncwarp();
     }
+    // the rows that this CTA has written are right, its parts may be missing
+    if (tid == 0) {
+      own_cut->gave_up = 1;
+      flag(p.dev_error, KVQ_DEVERR_TIMEOUT);
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
   }
-  fence_before();
-  __syncthreads();
-  fence_after();
   if (warp == 0)
     asm volatile(
         "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
@@ -1427,6 +1465,10 @@ __global__ void __launch_bounds__(256)
   const int cta = blockIdx.x;
   const Cut cut = *(reinterpret_cast<const Cut*>(p.workspace) + cta);
   if (cut.more == 0) return;
+  int lost = 0;  // a part may be missing: the rows are left as they were
+  for (int k = threadIdx.x; k <= cut.more; k += blockDim.x)
+    lost |= (reinterpret_cast<const Cut*>(p.workspace) + cta + k)->gave_up;
+  if (__syncthreads_or(lost)) return;
   const Seq s = seq_of(p, cut.b);
   const int row0 = cut.block * kRows;
   const int rows = min(kRows, s.n * p.G - row0);
