@@ -16,8 +16,9 @@
 //     in tensor memory): 16 tcgen05.mma of 128 x 128 x 16 per slot and tile,
 //     512 cycles for each product (measured, the unit's full rate).
 //   * Softmax warps hold a row per thread: logits from tensor memory, weights
-//     back over them, no exchange between threads.  The reference is the
-//     first tile's maximum; later tiles go without theirs (see kMost).
+//     back over them, no exchange between threads.  The reference comes from
+//     the maximum of the first half tile; later ones go without theirs (see
+//     kMost).
 // Chunks of up to 128 rows have one query tile; its KV tiles alternate
 // between the slots, whose two results the epilogue joins.
 // Work is cut over the context into equal shares (the schedule below), so
@@ -55,7 +56,8 @@ constexpr int kKeys = 128;                 // tokens of a KV tile
 constexpr int kHalf = 128 * 128;           // bytes of half a tile (64 dims)
 constexpr int kTile = 2 * kHalf;           // a [128 x 128] fp16 tile
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMost = 32768.0f;          // see the softmax
+constexpr float kMost = 65504.0f;          // see the softmax
+constexpr float kBelow = 8.0f;
 
 // Test builds only: in three of four thread blocks one softmax warp, another
 // from block to block, gives up at the end of the first or second segment as
@@ -942,13 +944,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kt = kt0; kt < kv1; kt += step, ++cnt) {
         if (!warp_wait(bar(kSFull + m), cnt & 1, abort)) goto done;
         fence_after();
-        // Weights are exp2 of the scaled logits minus a reference: the
-        // maximum of the first half of the first tile.  Later ones do
-        // without their maximum: as long as a row's weights of half a tile
-        // sum up to less than kMost, none is out of fp16's range.  Where
-        // that fails the half is done over, with its maximum for the new
-        // reference.  The product of the first half with V begins while the
-        // second is made.
+        // Weights are exp2 of the scaled logits minus a reference: kBelow
+        // less than the maximum of the first half of the first tile, so that
+        // the weight there is 2^8.  They are rounded to fp16, which keeps 11
+        // bits of those down to 2^-14, 2^-22 of that weight: behind one token
+        // that takes nearly all of the weight (the first of a long context,
+        // often) thousands of others may share the rest.  (With a weight of 1
+        // there, 2^-14 of it, 30000 tokens with 0.1 to 1 % of the weight together
+        // came out up to 22 % off.)
+        // Later halves do without their maximum: as long as a row's weights
+        // of half a tile sum up to less than kMost, fp16's largest number,
+        // none is out of range; 64 of 2^8 are 2^14.  Where that fails the
+        // half is done over, with its maximum for the new reference.  The
+        // product of the first half with V begins while the second is made.
         // (Unrolled: 500 tokens over 131000 1.53 ms against 1.61.)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -969,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mask32(s + 32, valid.y & first_bits(lim - 32));
             }
             if (look) {
-              const float top = max64(s) * c;
+              const float top = max64(s) * c - kBelow;
               const float f = top > ref ? ex2(ref - top) : 1.0f;
               ref = fmaxf(ref, top);
               sum *= f;

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from paged_quantized_kv_gb300 import kvq
-from tests.page_models import chunk_attention
+from tests.page_models import E4M3, chunk_attention
 from tests.test_chunk_attention import KS, VS, Case
 
 pytestmark = pytest.mark.gpu
@@ -77,3 +77,74 @@ def test_one_slot_far_behind_the_other(slot, G):
         c.call(workspace=ws)
         assert torch.equal(c.out, want)
     assert int(c.err.item()) == bits
+
+
+def sink_case(n, seqs, L, share, seed):
+    """`seqs` sequences over the same pages: keys of zeros behind a first key
+    of ones, so that a row's query (a multiple of ones) sets the weight of
+    the first token, whose V is zero: between `share` and 1 - (1 - share) / 8.
+    The other V are not negative, so that the output is of the size of
+    mag."""
+    rng = np.random.default_rng(seed)
+    c = Case([n], [L], hq=2, hkv=1, seed=seed)
+    cut = 16 * 64
+    c.pages.data[:, 0, :cut] = 0
+    c.pages.data[:, 0, cut:] = 0x38                      # scales 1.0
+    c.pages.data[:, 1, :cut] &= 0x77                     # codes >= 0
+    page = c.table[0, 0]
+    for side, code in ((0, 0x22), (1, 0)):               # 1.0; 0.0
+        d, _ = c.pages.places(side, 0)
+        c.pages.data[page, side, d[0]] = code
+    rest = (1 - share) * np.exp2(-3 * rng.random((n, 2)))
+    x0 = np.log(L * (1 - rest) / rest)                   # the first logit
+    q = np.repeat((x0 / (c.scale * KS * 128))[..., None], 128, -1)
+    c.q = torch.from_numpy(q).to(c.dt)
+    ref = c.ref()
+    c.q = c.q.repeat(seqs, 1, 1)
+    c.table = np.repeat(c.table, seqs, 0)
+    c.lens = np.full(seqs, L, dtype=np.int32)
+    c.cu = (n * np.arange(seqs + 1)).astype(np.int32)
+    return c, ref
+
+
+@pytest.mark.parametrize("n,seqs,L,share", [
+    (9, 160, 30000, 0.99),      # a share of the work is a sequence
+    (66, 80, 30000, 0.99),      # two query tiles
+    (9, 160, 60000, 0.9), (9, 160, 2000, 0.999)])
+def test_one_token_takes_nearly_all(n, seqs, L, share):
+    """The general bound's u |out| + 2^-10 mag, here (u + 2^-10) mag; the
+    weight of the reference is 2^7 at least beside those formed with it, so
+    that one below fp16's normal range is off by 2^-25 of 2^7 times the sum,
+    together seen 2^-32 vmax; and the fp32 sums, whose terms all have one
+    sign: L / 16 steps of the product with V, L / 64 + 32 of the weights',
+    each off by 2^-23 of the sum at most: below L / 8 2^-23 mag for the
+    lengths here."""
+    c, (out, mag, seen, vmax) = sink_case(n, seqs, L, share, seed=n)
+    got = c.run(max_context_len=L).reshape(seqs, n, 2, 128)
+    tol = (2.0 ** -8 + 2.0 ** -10 + L / 8 * 2.0 ** -23) * mag + (
+        seen * 2.0 ** -32 * vmax)[:, None, None]
+    worst = (np.abs(got - out) / mag).max()
+    assert (np.abs(got - out) <= tol).all(), worst
+
+
+@pytest.mark.parametrize("n", [12, 100])
+@pytest.mark.parametrize("rise", [3, 7, 8, 9, 12, 20, -20])
+def test_logits_that_rise_from_tile_to_tile(n, rise):
+    """By `rise` in log2 from each 64 tokens to the next, over seven tiles:
+    within what the running reference takes without being set anew, and past
+    it.  Logits are up to 194 here: eight steps of an fp32 sum, each off by
+    2^-23 of that at most, are 2^-12.3 on a weight, above the fraction bar
+    and below it: beside the general bound, 2^-11 mag."""
+    L = 14 * 64
+    c = Case([n], [L], hq=2, hkv=1, seed=n)
+    cut = 16 * 64
+    c.pages.data[:, 0, :cut] = 0x22                      # every code 1.0
+    for j, page in enumerate(c.table[0, :L // 16]):
+        times = j // 4 + 1 if rise > 0 else 14 - j // 4  # exact in e4m3
+        c.pages.data[page, 0, cut:] = int(np.nonzero(E4M3 == times)[0][0])
+    c.q = torch.full_like(c.q, abs(rise) * np.log(2) / (c.scale * KS * 128))
+    out, mag, seen, vmax = c.ref()
+    got = c.run()
+    tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -10 + 2.0 ** -11) * mag + (
+        (seen * 2.0 ** -25 + 2.0 ** -24) * vmax)[:, None, None]
+    assert (np.abs(got - out) <= tol).all()
