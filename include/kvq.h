@@ -446,8 +446,9 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  * cores, weights rounded to fp16 against a running reference, fp32 sums and
  * merges, out rounded once), except that for longer chunks the denominator
  * sums the weights before they are rounded, and the reference is set 8 (in
- * log2) below the maximum and may lag 16 behind it: weights down to 2^-22 of
- * the one that set it keep fp16's 11 bits.
+ * log2) below the maximum (7 for chunks of a few tokens) and may lag 16 (15)
+ * behind it: weights down to 2^-22 (2^-21) of the one that set it keep fp16's
+ * 11 bits.
  *
  * query          bf16 / fp16 (dtype) [total_q, num_q_heads, 128], rows
  *                query_stride0 elements apart (multiple of 8), 16-byte

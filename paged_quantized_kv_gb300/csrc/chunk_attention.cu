@@ -950,8 +950,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // bits of those down to 2^-14, 2^-22 of that weight: behind one token
         // that takes nearly all of the weight (the first of a long context,
         // often) thousands of others may share the rest.  (With a weight of 1
-        // there, 2^-14 of it, 30000 tokens with 0.1 to 1 % of the weight together
-        // came out up to 22 % off.)
+        // there 30000 tokens with 0.1 to 1 % of the weight together came out
+        // up to 22 % off.)
         // Later halves do without their maximum: as long as a row's weights
         // of half a tile sum up to less than kMost, fp16's largest number,
         // none is out of range; 64 of 2^8 are 2^14.  Where that fails the

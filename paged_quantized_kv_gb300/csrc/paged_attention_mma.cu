@@ -420,6 +420,12 @@ constexpr uint32_t kOnes2 = 0x3C003C00u;  // f16x2 {1, 1}
 // units) before the accumulators are rescaled: weights stay below 2^8, far
 // inside fp16, and their rounding is still relative (2^-11).
 constexpr float kLazy = 8.0f;
+// Rows of chunks set the reference this much below the maximum: weights of up
+// to 2^7 then, below 2^15 before the next move.  Behind one token that takes
+// nearly all of the weight, those of a warp's others keep fp16's 11 bits down
+// to 2^-21 of it (450 tokens that shared 2^-13 came out up to 4 % off without
+// this).
+constexpr float kChunkBelow = 7.0f;
 
 // kContig (kPages != 0): pages whose rows a warp copies as whole 8- or
 // 16-token pieces in the pages' own order, one block id and lane-constant
@@ -815,8 +821,8 @@ paged_attention_mma_kernel(const AttnParams p) {
   // over the warp's tokens by the tensor cores (c2, c3 repeat it and are
   // not read)
   // m_neg: -m_run, or 0 while m_run is -inf (no usable token yet)
-  // m_thr: (m_run + kLazy) / c2, the unscaled logit above which a step
-  // moves the reference
+  // m_thr: (m_run + kLazy) / c2 (rows of chunks: + kChunkBelow), the
+  // unscaled logit above which a step moves the reference
   float m_run[NB][2], m_neg[NB][2], m_thr[NB][2], lacc[NB][4];
   float o[4][2][NB][4];
 #pragma unroll
@@ -980,12 +986,13 @@ paged_attention_mma_kernel(const AttnParams p) {
           bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, 4));
           bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, 8));
           bm = fmaxf(bm, __shfl_xor_sync(0xFFFFFFFFu, bm, 16));
+          if constexpr (kChunk) bm -= kChunkBelow;
           const float mnew = fmaxf(m_run[n][c], bm);
           if (mnew > m_run[n][c]) {
             const float alpha = ex2(m_run[n][c] - mnew);  // 0 from -inf
             m_run[n][c] = mnew;
             m_neg[n][c] = -mnew;
-            m_thr[n][c] = (mnew + kLazy) / c2;
+            m_thr[n][c] = (mnew + (kChunk ? kChunkBelow + kLazy : kLazy)) / c2;
             lacc[n][c] *= alpha;
 #pragma unroll
             for (int mb = 0; mb < 4; ++mb)

@@ -110,7 +110,9 @@ def sink_case(n, seqs, L, share, seed):
 @pytest.mark.parametrize("n,seqs,L,share", [
     (9, 160, 30000, 0.99),      # a share of the work is a sequence
     (66, 80, 30000, 0.99),      # two query tiles
-    (9, 160, 60000, 0.9), (9, 160, 2000, 0.999)])
+    (9, 160, 60000, 0.9), (9, 160, 2000, 0.999),
+    (4, 8, 30000, 0.9995),      # the decode kernel's rows
+    (1, 8, 450, 0.9995), (8, 8, 100, 0.9999)])
 def test_one_token_takes_nearly_all(n, seqs, L, share):
     """The general bound's u |out| + 2^-10 mag, here (u + 2^-10) mag; the
     weight of the reference is 2^7 at least beside those formed with it, so
@@ -127,7 +129,7 @@ def test_one_token_takes_nearly_all(n, seqs, L, share):
     assert (np.abs(got - out) <= tol).all(), worst
 
 
-@pytest.mark.parametrize("n", [12, 100])
+@pytest.mark.parametrize("n", [3, 12, 100])
 @pytest.mark.parametrize("rise", [3, 7, 8, 9, 12, 20, -20])
 def test_logits_that_rise_from_tile_to_tile(n, rise):
     """By `rise` in log2 from each 64 tokens to the next, over seven tiles:
