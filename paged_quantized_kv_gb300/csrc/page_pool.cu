@@ -575,9 +575,12 @@ cudaError_t launch_cluster(K kernel, const PoolParams& p,
                            cudaStream_t stream) {
   const size_t smem = pool_smem(p.rows, p.n);
   if (smem > 40 * 1024) {
+    // the most that any call can need: the attribute is the kernel's, and a
+    // size of this call's own could be put back by another host thread
+    // before the launch
     const cudaError_t err = cudaFuncSetAttribute(
         kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        static_cast<int>(smem));
+        static_cast<int>(pool_smem(kPoolMaxRows, kPoolMaxList)));
     if (err != cudaSuccess) return err;
   }
   return launch_kernel(kernel, dim3(kCluster), kThreads, smem, stream, p.pdl,
