@@ -573,7 +573,8 @@ kvq_status kvq_extend_sequences(
  * Refused: rows outside [0, num_rows), a child named twice or not empty
  * (length 0 and no first page), a parent's length out of range
  * (KVQ_DEVERR_SEQ); a parent's partly filled last page that is not a page
- * (KVQ_DEVERR_BLOCK); KVQ_DEVERR_FULL as for kvq_extend_sequences.  A full
+ * (KVQ_DEVERR_BLOCK); a parent with a page that nobody holds (count 0 or
+ * less, KVQ_DEVERR_REF); KVQ_DEVERR_FULL as for kvq_extend_sequences.  A full
  * page of the parent that is not a page becomes -1 in the child, flagged
  * (KVQ_DEVERR_BLOCK).
  */

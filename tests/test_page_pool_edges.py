@@ -3,11 +3,13 @@ that nobody holds, lists without entries, entries that need no page, table
 entries that are no pages."""
 import threading
 
+import numpy as np
 import pytest
 import torch
 
 from paged_quantized_kv_gb300 import kvq
-from tests.test_page_pool import dev
+from tests.page_models import DEV_BLOCK, DEV_REF, Pool
+from tests.test_page_pool import Gpu, dev
 
 pytestmark = pytest.mark.gpu
 
@@ -54,3 +56,78 @@ def test_two_threads_with_pools_of_different_sizes():
     assert refused == []
     for state in states.values():
         assert state == (0, 0, [0, 1, 2, 4, 5])
+
+
+class HeldPool(Pool):
+    """The rule of forks that the base model does not have: a parent with a
+    page that nobody holds (count 0 or less) is refused."""
+
+    def fork(self, parents, children):
+        R, W = self.table.shape
+        left, bits = [], 0
+        for i, (p, c) in enumerate(zip(parents, children)):
+            bad = False
+            if (0 <= p < R and 0 <= c < R and list(children).count(c) == 1
+                    and self.lens[c] == 0 and not (W and self.table[c, 0] >= 0)
+                    and 0 <= self.lens[p] <= W * self.B):
+                L = int(self.lens[p])
+                used = self.table[p, :self._pages_for(L)]
+                if L % self.B == 0 or self._page(used[-1]):
+                    bad = any(self._page(x) and self.ref[x] <= 0
+                              for x in used)
+            if bad:
+                bits |= DEV_REF
+            else:
+                left.append(i)
+        src = np.full(len(parents), -1, dtype=np.int32)
+        dst = np.full(len(parents), -1, dtype=np.int32)
+        src[left], dst[left], more = super().fork(
+            [parents[i] for i in left], [children[i] for i in left])
+        return src, dst, bits | more
+
+
+def test_fork_of_pages_that_nobody_holds():
+    m = HeldPool(12, 9, 4, 4)
+    g = Gpu(m)
+    g.extend([0, 1, 2], [10, 8, 6])           # pages 0..2, 3..4, 5..6
+    m.ref[1] = 0                              # a full page of row 0
+    g.load()
+    a, b, bits = g.fork([0, 1, 2], [3, 4, 5])
+    assert bits == DEV_REF and a.tolist() == [-1, -1, 6]
+    assert b.tolist() == [-1, -1, 1]          # the free page, not shared
+    assert m.lens[3] == 0 and m.lens[4] == 8
+    m.ref[6] = 0                              # the partly filled one of row 2
+    g.load()
+    assert g.fork([2], [6])[2] == DEV_REF
+    m.ref[6] = -3
+    g.load()
+    assert g.fork([2, 1], [6, 7])[2] == DEV_REF
+    m.ref[6], m.table[2, 0] = 1, 77           # beside a page that is none
+    g.load()
+    assert g.fork([2], [6])[2] == DEV_BLOCK
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_fork_with_counts_at_random(seed):
+    """Long rows (the checks of a call are spread over the cluster), counts
+    taken away at random, entries that need pages and that do not, pools
+    that run out: equal calls give equal states."""
+    rng = np.random.default_rng(seed)
+    rows, width = 120, 400
+    m = HeldPool(20000, rows, width, 4)
+    g = Gpu(m)
+    g.extend(list(range(40)), rng.integers(0, 4 * width, 40).tolist())
+    held = np.nonzero(m.ref)[0]
+    m.ref[rng.choice(held, int(rng.integers(1, 30)))] = rng.integers(-1, 1)
+    named = np.isin(np.arange(m.nb), m.table)
+    free = np.nonzero((m.ref == 0) & ~named)[0]
+    left = int(rng.integers(0, 40))
+    m.ref[free[left:]] = 7                    # others hold the rest
+    before = (m.ref.copy(), m.table.copy(), m.lens.copy())
+    parents = rng.integers(0, 40, 60).tolist()
+    kids = (40 + rng.permutation(80)[:60]).tolist()
+    for _ in range(5):
+        m.ref, m.table, m.lens = (x.copy() for x in before)
+        g.load()
+        bits = g.fork(parents, kids)[2]
+        assert bits & DEV_REF
