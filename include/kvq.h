@@ -532,7 +532,8 @@ int64_t kvq_chunk_attention_workspace_bytes(void);
  * Limits: num_rows <= 2^18, lists of at most 4096 entries, block_size > 0,
  * max_blocks_per_seq * block_size < 2^31 - block_size.
  * flags: KVQ_F_PDL or 0.  A list of 0 entries returns KVQ_OK without
- * launching.
+ * launching: slots and other outputs are left as they were then, whatever
+ * their number.  (The Python binding fills the slots with -1.)
  */
 
 /*

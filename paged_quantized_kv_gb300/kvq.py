@@ -584,6 +584,19 @@ def _pool_args(fn: str, ref_count, block_table, seq_lens, dev_error,
             seq_lens.data_ptr()), here
 
 
+def _fill_none(stream: int | None, *slots) -> None:
+    """-1 in the slots of a list without entries (the C entry launches
+    nothing for one), on the call's stream."""
+    for t in slots:
+        if stream is None:
+            t.fill_(-1)
+            continue
+        with torch.cuda.stream(
+                torch.cuda.ExternalStream(stream, device=t.device) if stream
+                else torch.cuda.default_stream(t.device)):
+            t.fill_(-1)
+
+
 def kvq_extend_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
                          seq_lens: torch.Tensor, seq_ids: torch.Tensor,
                          cu_new: torch.Tensor, slot_mapping: torch.Tensor,
@@ -607,6 +620,8 @@ def kvq_extend_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
         slot_mapping.data_ptr(), slot_mapping.numel(), int(flags),
         _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
+    if n == 0:
+        _fill_none(stream, slot_mapping)
 
 
 def kvq_fork_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
@@ -659,6 +674,8 @@ def kvq_compact_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,
         keep.numel(), int(flags), _ptr(dev_error),
         here if stream is None else stream)
     _check(fn, st)
+    if n == 0:
+        _fill_none(stream, src_slots, dst_slots)
 
 
 def kvq_free_sequences(ref_count: torch.Tensor, block_table: torch.Tensor,

@@ -131,3 +131,35 @@ def test_fork_with_counts_at_random(seed):
         g.load()
         bits = g.fork(parents, kids)[2]
         assert bits & DEV_REF
+
+
+def test_lists_without_entries_write_their_outputs():
+    """No entry, but room for slots: all of them -1, on the stream given."""
+    ref, table, lens = kvq.alloc_page_pool(8, 3, 4)
+    none, cu = dev([]), dev([0])
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        out = [torch.full((9,), 5, dtype=torch.int64, device="cuda")
+               for _ in range(3)]
+        torch.cuda.synchronize()
+        handle = None if stream is None else stream.cuda_stream
+        kvq.kvq_extend_sequences(ref, table, lens, none, cu, out[0], 4,
+                                 stream=handle)
+        kvq.kvq_compact_sequences(ref, table, lens, none, dev([0] * 9), cu,
+                                  out[1], out[2], 4, stream=handle)
+        torch.cuda.synchronize()
+        for x in out:
+            assert x.tolist() == [-1] * 9
+    assert not bool(ref.any()) and bool((table == -1).all())
+
+
+def test_lists_without_entries_in_a_graph():
+    ref, table, lens = kvq.alloc_page_pool(8, 3, 4)
+    none, cu = dev([]), dev([0])
+    slots = torch.zeros(6, dtype=torch.int64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_extend_sequences(ref, table, lens, none, cu, slots, 4)
+    assert slots.tolist() == [0] * 6
+    graph.replay()
+    assert slots.tolist() == [-1] * 6
