@@ -130,7 +130,8 @@ enum {
                                   written */
   KVQ_DEVERR_REF = 1 << 4,   /* a page that other sequences share (or that
                                 nobody holds) would have been written, or a
-                                page that nobody holds was dropped */
+                                page that nobody holds was dropped or would
+                                have been shared */
   KVQ_DEVERR_FULL = 1 << 5   /* not enough free pages */
 };
 
@@ -514,8 +515,9 @@ int64_t kvq_chunk_attention_workspace_bytes(void);
  *                page; 0 = free.  All zero to begin with.
  *   block_table  int32 [num_rows, >= max_blocks_per_seq], rows
  *                block_table_stride apart; entry j of a row is the page of
- *                its tokens j * block_size ..; -1 = no page.  All -1 to
- *                begin with.
+ *                its tokens j * block_size ..; a negative entry = no page
+ *                (the calls write -1 and leave others as they are).  All -1
+ *                to begin with.
  *   seq_lens     int32 [num_rows], tokens of each row's sequence; 0 for an
  *                empty row.
  *
@@ -551,9 +553,10 @@ int64_t kvq_chunk_attention_workspace_bytes(void);
  * Refused: a row outside [0, num_rows) or named twice, a length outside
  * [0, max_blocks_per_seq * block_size] before or after (KVQ_DEVERR_SEQ); a
  * partly filled last page that is not a page (KVQ_DEVERR_BLOCK) or not this
- * row's alone (KVQ_DEVERR_REF); KVQ_DEVERR_FULL: entry i is served if the
- * free pages cover what it and all entries before it need (entries that
- * KVQ_DEVERR_FULL refuses still count, the others do not).
+ * row's alone (KVQ_DEVERR_REF); KVQ_DEVERR_FULL: an entry that needs pages
+ * is served if the free pages cover what it and all entries before it need
+ * (entries that KVQ_DEVERR_FULL refuses still count, the others do not); one
+ * that needs none is always served.
  */
 kvq_status kvq_extend_sequences(
     int32_t* ref_count, int64_t num_blocks, int32_t* block_table,
@@ -618,9 +621,10 @@ kvq_status kvq_compact_sequences(
  * kvq_free_sequences -- rows seq_ids[i] become empty: every page that they
  * hold is dropped once per entry (free when nobody else holds it), the
  * entries become -1 and the lengths 0.  A row outside [0, num_rows) is
- * skipped (KVQ_DEVERR_SEQ); so is an entry that is not a page
- * (KVQ_DEVERR_BLOCK, it becomes -1) and a count that is already 0
- * (KVQ_DEVERR_REF, it stays 0).
+ * skipped (KVQ_DEVERR_SEQ); so is an entry of num_blocks or more
+ * (KVQ_DEVERR_BLOCK, it becomes -1), a page whose count is 0 or less
+ * (KVQ_DEVERR_REF, the count stays), and a negative entry (no page: it stays,
+ * nothing is flagged).
  */
 kvq_status kvq_free_sequences(int32_t* ref_count, int64_t num_blocks,
                               int32_t* block_table,

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from paged_quantized_kv_gb300 import kvq
-from tests.page_models import DEV_BLOCK, DEV_REF, Pool
+from tests.page_models import DEV_BLOCK, DEV_FULL, DEV_REF, Pool
 from tests.test_page_pool import Gpu, dev
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +163,31 @@ def test_lists_without_entries_in_a_graph():
     assert slots.tolist() == [0] * 6
     graph.replay()
     assert slots.tolist() == [-1] * 6
+
+
+def test_entries_that_need_no_page_are_served_by_a_full_pool():
+    g = Gpu(Pool(4, 6, 4, 4))
+    g.extend([0, 1], [6, 5])
+    # the pool is empty: two entries need a page, the others have room
+    _, bits = g.extend([2, 0, 3, 1], [1, 2, 9, 3])
+    assert bits == DEV_FULL
+    assert g.m.lens[:4].tolist() == [8, 8, 0, 0]
+    _, _, bits = g.fork([0, 1], [4, 5])       # full pages only: shared
+    assert bits == 0 and g.m.lens[4:].tolist() == [8, 8]
+
+
+def test_negative_entries_are_no_pages():
+    """Whatever the negative value: not dropped, not flagged, left."""
+    m = Pool(8, 4, 5, 4)
+    m.table[0] = [3, -5, 1, -1, -7]
+    m.ref[[1, 3]] = 1
+    m.lens[0] = 10
+    g = Gpu(m)
+    assert g.compact([0], [[]])[2] == 0
+    assert m.table[0].tolist() == [-1, -5, -1, -1, -7]
+    m.table[1] = [-9, 2, -1, -1, -1]
+    m.ref[2] = 1
+    g.load()
+    assert g.free([0, 1]) == 0
+    assert m.table[1, 0] == -9 and (m.ref == 0).all()
+    assert g.extend([1], [5])[1] == 0         # the row is an empty one
