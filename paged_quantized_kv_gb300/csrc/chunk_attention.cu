@@ -1110,7 +1110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int g = 0; g < 16; ++g) {
             const float a = __uint_as_float(o[2 * g]) * inv;
             const float b = __uint_as_float(o[2 * g + 1]) * inv;
-            x[g] = kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+            // (a row that sees nothing gets zeros whatever the scales are)
+            x[g] = pos < 0 ? 0u
+                           : kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
           }
           if (wide) {
             stg256(dst + col, x);
@@ -1482,6 +1484,7 @@ __global__ void __launch_bounds__(256)
   const int rows = min(kRows, s.n * p.G - row0);
   const int lane = threadIdx.x & 31;
   const float vs = __ldg(p.v_scale);
+  const int blind = s.n - s.L;  // tokens that see nothing, whose rows are 0
   for (int i = 0; i < kMergeRows / 8; ++i) {
     const int row = blockIdx.y * kMergeRows + 8 * i + (threadIdx.x >> 5);
     if (row >= rows) return;
@@ -1508,7 +1511,11 @@ __global__ void __launch_bounds__(256)
     const int head = cut.h * p.G + (row0 + row - tok * p.G);
     uint16_t* dst = p.out + (s.q0 + tok) * p.out_stride0 + head * kD +
                     4 * lane;
-    uint2 w;
+    uint2 w = make_uint2(0, 0);
+    if (tok < blind) {
+      *reinterpret_cast<uint2*>(dst) = w;
+      continue;
+    }
     w.x = kF16 ? pack_f16x2(o.x * inv, o.y * inv)
                : pack_bf16x2(o.x * inv, o.y * inv);
     w.y = kF16 ? pack_f16x2(o.z * inv, o.w * inv)

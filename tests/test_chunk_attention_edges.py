@@ -150,3 +150,20 @@ def test_logits_that_rise_from_tile_to_tile(n, rise):
     tol = 2.0 ** -8 * np.abs(out) + (2.0 ** -10 + 2.0 ** -11) * mag + (
         (seen * 2.0 ** -25 + 2.0 ** -24) * vmax)[:, None, None]
     assert (np.abs(got - out) <= tol).all()
+
+
+@pytest.mark.parametrize("n,L", [(30, 10), (200, 60), (4, 2)])
+def test_rows_that_see_nothing_under_any_scale(n, L):
+    """Zeros, even where the tensor scales are not numbers; the rows that see
+    a token are NaN then."""
+    c = Case([n], [L], hq=4, hkv=1, seed=40).upload()
+    for k_scale, v_scale in ((float("nan"), VS), (KS, float("nan")),
+                             (float("inf"), VS)):
+        c.ks.fill_(k_scale)
+        c.vs.fill_(v_scale)
+        c.out.fill_(77.0)
+        c.call()
+        got = c.out.double().cpu().numpy()
+        assert (got[:n - L] == 0).all(), (k_scale, v_scale)
+        if np.isnan(k_scale) or np.isnan(v_scale):
+            assert np.isnan(got[n - L:]).all()
