@@ -167,3 +167,107 @@ def test_rows_that_see_nothing_under_any_scale(n, L):
         assert (got[:n - L] == 0).all(), (k_scale, v_scale)
         if np.isnan(k_scale) or np.isnan(v_scale):
             assert np.isnan(got[n - L:]).all()
+
+
+@pytest.mark.parametrize("n", [1, 3, 4])
+@pytest.mark.parametrize("fits", [True, False])
+def test_short_chunks_on_both_sides_of_the_workspace(n, fits):
+    """Single tokens and drafts whose partial results, counted over the width
+    of the block table, fit the workspace, and such that do not and go
+    through the tile kernel."""
+    rng = np.random.default_rng(n)
+    seqs = 130
+    lens = (n + rng.integers(0, 60, seqs)).tolist()
+    lens[5], lens[100] = 700, 1300
+    c = Case([n] * seqs, lens, hq=16, hkv=1, seed=n)
+    room = kvq.chunk_attention_workspace().numel()
+    parts = room // (seqs * n * 16 * 130 * 4)      # stretches of 512 tokens
+    width = (parts if fits else parts + 1) * 512 // 16
+    table = np.full((seqs, width), -1, dtype=np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    c.table = table
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("max_q", [8, 40])
+def test_rows_of_offsets_out_of_order(max_q):
+    """Clamped and flagged: the rows that a clamped sequence has are its
+    attention (with max_q_len 8 only those of chunks up to it), all others
+    and the memory around the output are left as they were."""
+    for cu in ([0, 9, 40], [-3, 8, 16], [0, 12, 8], [50, 60, 70],
+               [0, 5, 1 << 30]):
+        c = Case([8, 8], [40, 43], hq=4, hkv=1, seed=13)
+        c.cu = np.asarray(cu, dtype=np.int32)
+        c.upload()
+        guard = torch.full((16 + 64, 4, 128), 77.0, dtype=c.dt,
+                           device="cuda")
+        c.call(out=guard[32:48], max_q=max_q)
+        torch.cuda.synchronize()
+        assert int(c.err.item()) == kvq.KVQ_DEVERR_SEQ, cu
+        whole = guard.double().cpu().numpy()
+        assert (whole[:32] == 77.0).all() and (whole[48:] == 77.0).all(), cu
+        got = whole[32:48]
+        want, mag, seen, vmax = (np.zeros((16, 4, 128)),
+                                 np.zeros((16, 4, 128)), np.full(16, -1),
+                                 np.zeros(16))
+        for b in range(2):
+            q0 = min(max(cu[b], 0), 16)
+            n = min(max(cu[b + 1], q0), 16) - q0
+            if n == 0 or n > max_q:
+                continue
+            part = chunk_attention(c.pages, c.q.double().numpy()[q0:q0 + n],
+                                   c.table[b:b + 1], [0, n], c.lens[b:b + 1],
+                                   KS, VS, c.scale)
+            for to, x in zip((want, mag, seen, vmax), part):
+                to[q0:q0 + n] = x
+        c.check(got, (want, mag, seen, vmax), what=cu)
+
+
+@pytest.mark.parametrize("new", [[64, 1, 200], [3, 1, 4]],
+                         ids=["tiles", "short"])
+def test_dependent_launches_behind_the_writers(new):
+    """Extend, store, attention, step after step with dependent launches: the
+    same bits as launched without and waited for after each call."""
+    B, H, hq, steps, rows = 16, 2, 8, 12, len(new)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(sum(new))
+    total = sum(new)
+    k, v = (torch.randn(steps, total, H, 128, device="cuda",
+                        generator=gen).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(steps, total, hq, 128, device="cuda",
+                    generator=gen).to(torch.bfloat16)
+    width = -(-max(new) * steps // B)
+    ids = torch.arange(rows, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0] + np.cumsum(new).tolist(), dtype=torch.int32,
+                      device="cuda")
+    ks, vs = (torch.tensor([x], device="cuda") for x in (KS, VS))
+    ws = kvq.chunk_attention_workspace()
+
+    def run(pdl):
+        ref, table, lens = kvq.alloc_page_pool(rows * width, rows, width)
+        kv, kc, vc = kvq.alloc_nvfp4_cache(rows * width, B, H, 128, fill=0x7F)
+        out = torch.full((steps, total, hq, 128), 77.0, dtype=q.dtype,
+                         device="cuda")
+        slots = torch.zeros(total, dtype=torch.int64, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        f = dict(flags=kvq.KVQ_F_PDL if pdl else 0, dev_error=err)
+        wait = (lambda: None) if pdl else torch.cuda.synchronize
+        torch.cuda.synchronize()
+        for i in range(steps):
+            kvq.kvq_extend_sequences(ref, table, lens, ids, cu, slots, B, **f)
+            wait()
+            kvq.kvq_store_nvfp4(k[i], v[i], kc, vc, slots, ks, vs, **f)
+            wait()
+            kvq.kvq_chunk_attention_nvfp4(
+                q[i], kc, vc, table, cu, lens, ks, vs, 128 ** -0.5, out[i],
+                max(new), workspace=ws, **f)
+            wait()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        return out, kv, table, lens
+
+    want = run(False)
+    assert bool(torch.isfinite(want[0]).all())
+    for _ in range(4):
+        for a, b in zip(run(True), want):
+            assert torch.equal(a, b)
