@@ -473,7 +473,16 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  * max_context_len  the batch's longest context, as known on the host, or 0
  *                for the block table's width.  Sizes the launch for chunks
  *                of a few tokens (as for kvq_paged_attention_nvfp4: a loose
- *                bound costs time).
+ *                bound costs time).  Chunks of up to 4 tokens (up to 8 with
+ *                no more (sequence, KV head) pairs than multiprocessors), and
+ *                single tokens beside longer chunks, go token by token
+ *                through the decode kernel if its partial results fit the
+ *                workspace: no context above 512, or num_seqs * tokens *
+ *                num_q_heads * ceil(max_context_len / 512) * 520 bytes.
+ *                Else they take the longer chunks' kernel, which for single
+ *                tokens is up to five times slower; several calls with fewer
+ *                sequences, or kvq_paged_attention_nvfp4 with scratch of its
+ *                own, avoid it.
  * workspace      workspace_bytes of device memory, 32-byte aligned; at
  *                least kvq_chunk_attention_workspace_bytes() (the same for
  *                every call on a device), else KVQ_ERR_SCRATCH.  Nothing in

@@ -25,17 +25,20 @@
 // few rows over a long context use every SM; a second kernel joins the parts.
 //
 // Measured: 2048 tokens over 8192 with 64 query and 8 KV heads (481 GFLOP)
-// 0.40 ms, 1196 TFLOP/s, 61 % of the measured bf16 rate; 500 over 131000 1.53
-// ms, 1396 TFLOP/s, 71 %.  The tensor cores are active half of the time on
-// the first (by their counter), and two slots are all that tensor memory
-// holds.  What bounds it is the softmax: with half of its exponentials left
-// out (wrong results, a copy of an earlier step) the second case took 1.34 ms
-// where that step took 1.60, without the dequantisation's conversions 1.60.
-// Alone, a softmax step of 128 x 128 takes 1200 cycles with one slot's warps
-// running and 1650 with both (the exponentials' unit takes one warp's in 4
-// cycles), and each hand-over between the units some 340 for both ways.
+// 0.40 ms, 1202 TFLOP/s, 61 % of the measured bf16 rate; 500 over 131000 1.54
+// ms, 1393 TFLOP/s, 71 %.  No pipe is saturated (on the first, by the
+// counters: tensor cores 53 %, issue 49 %, exponentials and conversions 27 %).
+// What bounds it is a slot's round, a chain of logits, softmax, weights and
+// product through units that hand over to one another, with two slots in all:
+// more do not fit tensor memory.  The softmax is the chain's longest link:
+// with half of its exponentials left out (wrong results, a copy of an earlier
+// step) the second case took 1.34 ms where that step took 1.60, without the
+// dequantisation's conversions 1.60.  Alone, a softmax step of 128 x 128
+// takes 1200 cycles with one slot's warps running and 1650 with both (the
+// exponentials' unit takes one warp's in 4 cycles), and each hand-over some
+// 340 for both ways.
 // Sixteen softmax warps of half a row each were slower, 2.02 ms against 1.65.
-// 16 tokens of 32 sequences over 2000 to 4000: 0.115 ms for 0.13 GB.  Chunks
+// 16 tokens of 32 sequences over 2000 to 4000: 0.117 to 0.124 ms for 0.13 GB.  Chunks
 // of a few tokens go through the decode kernel instead (short_chunk).
 #include <cuda_runtime.h>
 #include <math.h>
