@@ -271,3 +271,50 @@ def test_dependent_launches_behind_the_writers(new):
     for _ in range(4):
         for a, b in zip(run(True), want):
             assert torch.equal(a, b)
+
+
+def test_nan_scales_under_many_segments():
+    """The lists of V scales that are not numbers, segment after segment:
+    NaN in their group's columns of the rows that see the token, nowhere
+    else."""
+    rng = np.random.default_rng(61)
+    q = rng.integers(5, 40, 700)
+    lens = q + rng.integers(0, 260, q.size)
+    c = Case(q.tolist(), lens.tolist(), hq=4, hkv=1, seed=61)
+    clean, ref = c.run(), c.ref()
+    c.check(clean, ref)
+    want = np.zeros(clean.shape, dtype=bool)
+    for b in rng.permutation(q.size)[:250]:
+        t, group = int(rng.integers(0, lens[b])), int(rng.integers(0, 8))
+        c.pages.set_scale(1, c.table[b, t // 16], t % 16, 0, group,
+                          int(rng.choice([0x7F, 0xFF])))
+        sees = np.arange(q[b]) + lens[b] - q[b] >= t
+        want[c.cu[b]:c.cu[b + 1]][sees, :, 16 * group:16 * group + 16] = True
+    for _ in range(5):
+        got = c.run()
+        assert np.array_equal(np.isnan(got), want)
+        c.check(np.where(want, clean, got), ref)
+
+
+def test_many_heads():
+    """64 KV heads of 16 query heads: the most that a call may have."""
+    c = Case([1, 19, 5], [40, 33, 140], hq=1024, hkv=64, seed=62)
+    c.check(c.run())
+
+
+def test_rows_far_into_the_query():
+    """More than 2^31 elements of queries: 18 million rows, of which the last
+    1000 see something."""
+    n, L = 18_000_000, 1000
+    c = Case([L], [L], hq=1, hkv=1, seed=63)
+    ref = c.ref()
+    c.upload()
+    c.qd = torch.zeros(n, 1, 128, dtype=c.dt, device="cuda")
+    c.qd[-L:] = c.q.cuda()
+    c.cud = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    out = torch.full_like(c.qd, 77.0)
+    c.call(out=out, max_q=n)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    assert not bool(out[:-L].any())
+    c.check(out[-L:].double().cpu().numpy(), ref)
