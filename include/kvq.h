@@ -453,7 +453,9 @@ kvq_status kvq_paged_attention_nvfp4_noalloc(
  *
  * query          bf16 / fp16 (dtype) [total_q, num_q_heads, 128], rows
  *                query_stride0 elements apart (multiple of 8), 16-byte
- *                aligned; |q| < 65504 (fp16 range).  0 <= total_q <= 2^25.
+ *                aligned; |q| < 65504 (fp16 range), and logits |s_t| below
+ *                2^26 (an fp32 logit of that size is off by several units
+ *                itself).  0 <= total_q <= 2^25.
  * cu_q_lens      int32 [num_seqs + 1], cu_q_lens[0] >= 0, non-decreasing,
  *                at most total_q (values that break this are clamped and
  *                flagged KVQ_DEVERR_SEQ).  Rows that no sequence covers
