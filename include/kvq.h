@@ -24,6 +24,14 @@
  *   kvq_chunk_attention_nvfp4  causal attention of chunks of new tokens
  *                         (pieces of prompts, drafts to verify, single
  *                         tokens, in one ragged batch) over the NVFP4 pages.
+ *   kvq_tree_attention_nvfp4  the same for trees of drafted tokens: a mask
+ *                         says which drafts each of them sees.
+ *   kvq_quantize_indexer_q, kvq_score_blocks_indexer_k, kvq_select_blocks
+ *                         the indexer's queries in fp8, its scores of the
+ *                         blocks of the context over the indexer cache, and
+ *                         the blocks that each query attends to.
+ *   kvq_sparse_attention_nvfp4  attention over the selected blocks of the
+ *                         NVFP4 pages.
  *   kvq_extend_sequences, kvq_fork_sequences, kvq_compact_sequences,
  *   kvq_free_sequences    the state of a paged cache on the device: page
  *                         counts, block tables and lengths.
@@ -64,7 +72,9 @@ typedef enum {
   KVQ_ERR_ARG = -7,     /* unknown flag bits or inconsistent arguments */
   KVQ_ERR_SCRATCH = -8  /* kvq_paged_attention_nvfp4_noalloc: the call needs
                            more scratch than the built-in array holds;
-                           kvq_chunk_attention_nvfp4: the workspace is too
+                           kvq_chunk_attention_nvfp4,
+                           kvq_tree_attention_nvfp4 and
+                           kvq_sparse_attention_nvfp4: the workspace is too
                            small */
 } kvq_status;
 
@@ -515,6 +525,212 @@ kvq_status kvq_chunk_attention_nvfp4(
 
 /* Workspace of a kvq_chunk_attention_nvfp4 call on the current device. */
 int64_t kvq_chunk_attention_workspace_bytes(void);
+
+/*
+ * kvq_tree_attention_nvfp4 -- attention of trees of drafted tokens over the
+ * NVFP4 cache, the drafts' own K and V included (store them first).  The
+ * source material has no counterpart; this entry point is an addition of this
+ * library, kvq_chunk_attention_nvfp4 with a mask among the new tokens.
+ *
+ * Sequence b has the n query rows cu_q_lens[b] .. cu_q_lens[b+1] - 1, its
+ * drafts, which are the last n of its L = context_lens[b] cached tokens.  Row
+ * r = cu_q_lens[b] + i sees the tokens t < L - n and those drafts j (token
+ * L - n + j) whose bit is set: bit j % 32 of tree_mask[r *
+ * tree_mask_stride0 + j / 32].  Its own bit is no exception.  Bits from n on
+ * are ignored.  A row that sees nothing gets zeros.  What a row does not see
+ * cannot reach it, whatever its bytes.  With the bits of each draft's
+ * ancestors and its own, the rows are what kvq_chunk_attention_nvfp4 gives on
+ * each path of the tree; accepted drafts stay by kvq_compact_sequences and
+ * kvq_move_tokens_nvfp4.
+ * Arithmetic: as for the longer chunks of kvq_chunk_attention_nvfp4.
+ *
+ * tree_mask       int32 [total_q, mask_words], device, 4-byte aligned, rows
+ *                 tree_mask_stride0 (>= mask_words) words apart; 0 <
+ *                 mask_words <= 32.  Drafts behind 32 * mask_words are seen
+ *                 by nobody (KVQ_DEVERR_SEQ).
+ * All other arguments, the workspace, flags, errors and limits as for
+ * kvq_chunk_attention_nvfp4.
+ */
+kvq_status kvq_tree_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, const int32_t* tree_mask,
+    int64_t tree_mask_stride0, int32_t mask_words, const float* k_scale,
+    const float* v_scale, float scale, void* workspace,
+    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, void* stream);
+
+/*
+ * Sparse attention over blocks of the context that an indexer selects for
+ * each query row.  The context of a sequence is cut into blocks of
+ * select_block tokens, block j holding the tokens j * select_block ..; the
+ * indexer's queries (kvq_quantize_indexer_q) score them over the indexer
+ * cache that kvq_store_indexer_k writes (kvq_score_blocks_indexer_k), a list
+ * of blocks is taken for each row (kvq_select_blocks), and the attention
+ * reads those alone (kvq_sparse_attention_nvfp4).  The source material has
+ * the indexer cache (vLLM PR #25931, PR #26456) and no more of it; these
+ * entry points are additions of this library.
+ *
+ * The query rows of the last three are those of kvq_chunk_attention_nvfp4:
+ * sequence b has the rows cu_q_lens[b] .. cu_q_lens[b+1] - 1, n of them, the
+ * last n of its L = context_lens[b] cached tokens, and row cu_q_lens[b] + i
+ * sees L - n + i + 1 of them (none where that is not positive).  cu_q_lens and
+ * context_lens are clamped and flagged as there (KVQ_DEVERR_SEQ), and rows
+ * that no sequence covers are left as they were.
+ */
+
+/*
+ * kvq_quantize_indexer_q -- the indexer's queries to fp8 e4m3, by the rule of
+ * kvq_store_indexer_k, with each head's scale folded into its weight.
+ *
+ * For row t and head h:
+ *   amax = max |q[t, h, d]|;  s = amax / 448   (fp32 IEEE division)
+ *   q_fp8[t, h, d] = amax == 0 ? 0 : e4m3_rn_satfinite(q[t, h, d] / s)
+ *   weights_out[t, h] = (weights[t, h] * scale) * s   (fp32 products)
+ *
+ * q              bf16 or fp16 [total_q, num_heads, head_dim], finite; heads
+ *                and elements contiguous, rows q_stride0 elements apart
+ *                (multiple of 8); 16-byte aligned.
+ * num_heads      1 .. 1024.   head_dim 16, 32, 64, 128 or 256.
+ * weights        fp32 [total_q, num_heads], rows weights_stride0 apart.
+ * scale          finite.
+ * q_fp8          [total_q, num_heads, head_dim] bytes, contiguous, 16-byte
+ *                aligned.   weights_out  fp32 [total_q, num_heads],
+ *                contiguous.
+ * flags          KVQ_F_PDL or 0.
+ * total_q == 0 returns KVQ_OK without launching.
+ */
+kvq_status kvq_quantize_indexer_q(const void* q, int64_t q_stride0,
+                                  int32_t dtype, const float* weights,
+                                  int64_t weights_stride0, float scale,
+                                  int64_t total_q, int32_t num_heads,
+                                  int32_t head_dim, uint8_t* q_fp8,
+                                  float* weights_out, uint32_t flags,
+                                  void* stream);
+
+/*
+ * kvq_score_blocks_indexer_k -- every block's score for every query row, over
+ * the paged indexer cache.
+ *
+ * For a row r and a token t that it sees, with the token's e4m3 row k_t and
+ * fp32 scale c_t (block layout as for kvq_gather_indexer_k):
+ *   s_t = c_t * sum_h weights[r, h] * max(0, q_fp8[r, h, :] . k_t)
+ *   scores[r, j] = max of s_t over the tokens of block j that the row sees
+ * and -inf for a block of which it sees none, up to num_columns.  A token
+ * whose page is not a page (KVQ_DEVERR_BLOCK) or whose s_t is NaN is left
+ * out.
+ * Arithmetic: products of e4m3 are exact; their sums, the weights' and the
+ * scales' products are in fp32 (the dot products on the tensor cores), in an
+ * order that depends on nothing but the sizes.
+ *
+ * q_fp8          e4m3 [total_q, num_heads, head_dim]; heads and elements
+ *                contiguous, rows q_stride0 bytes apart (multiple of 16);
+ *                16-byte aligned.   0 <= total_q <= 2^25.
+ * weights        fp32 [total_q, num_heads], rows weights_stride0 apart.
+ * num_heads      1 .. 128.   head_dim 32, 64 or 128.
+ * max_q_len      the longest chunk of the batch, as known on the host (sizes
+ *                the launch: a larger value costs time, a smaller one too).
+ * kv_cache, block_stride, num_blocks, block_size, block_table,
+ * block_table_stride, max_blocks_per_seq   as for kvq_gather_indexer_k.
+ * context_lens   values above min(max_blocks_per_seq * block_size,
+ *                num_columns * select_block) are clamped to it and flagged.
+ * select_block   16, 32, 64 or 128 tokens.
+ * scores         fp32 [total_q, num_columns], rows scores_stride0 apart;
+ *                num_columns * select_block <= 2^26.
+ * flags          KVQ_F_PDL or 0.
+ * dev_error      nullable (KVQ_DEVERR_BLOCK, KVQ_DEVERR_SEQ,
+ *                KVQ_DEVERR_TIMEOUT: a bounded wait gave up, scores may be
+ *                missing).
+ * total_q, num_seqs or num_columns == 0 returns KVQ_OK without launching.
+ */
+kvq_status kvq_score_blocks_indexer_k(
+    const uint8_t* q_fp8, int64_t q_stride0, const float* weights,
+    int64_t weights_stride0, int64_t total_q, int32_t num_seqs,
+    const int32_t* cu_q_lens, int32_t max_q_len, int32_t num_heads,
+    int32_t head_dim, const uint8_t* kv_cache, int64_t block_stride,
+    int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+    int64_t block_table_stride, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, int32_t select_block, float* scores,
+    int64_t scores_stride0, int32_t num_columns, uint32_t flags,
+    int32_t* dev_error, void* stream);
+
+/*
+ * kvq_select_blocks -- the blocks that each query row attends to.
+ *
+ * A row that sees `seen` tokens has nb = ceil(seen / select_block) blocks and
+ * gets the k = min(max_selected, nb) of them that come first in this order:
+ * the first num_first and the last num_last ones, then the others by falling
+ * score, NaN as -inf; among equal scores the lower index.  selected[r, :] is
+ * their indices in rising order, then -1.
+ *
+ * scores         fp32 [total_q, num_columns], rows scores_stride0 apart; only
+ *                the first nb of a row are read.
+ * context_lens   values above num_columns * select_block are clamped to it
+ *                and flagged (KVQ_DEVERR_SEQ).
+ * select_block   > 0; num_columns * select_block <= 2^26.
+ * num_first, num_last  >= 0, num_first + num_last <= max_selected (else
+ *                KVQ_ERR_ARG).
+ * selected       int32 [total_q, max_selected], rows selected_stride0 apart.
+ * flags          KVQ_F_PDL or 0.
+ * total_q == 0 or num_seqs == 0 returns KVQ_OK without launching.
+ */
+kvq_status kvq_select_blocks(const float* scores, int64_t scores_stride0,
+                             int32_t num_columns, int64_t total_q,
+                             int32_t num_seqs, const int32_t* cu_q_lens,
+                             const int32_t* context_lens,
+                             int32_t select_block, int32_t num_first,
+                             int32_t num_last, int32_t* selected,
+                             int64_t selected_stride0, int32_t max_selected,
+                             uint32_t flags, int32_t* dev_error,
+                             void* stream);
+
+/*
+ * kvq_sparse_attention_nvfp4 -- attention of each query row over the blocks
+ * of its list, for all of its heads, over the NVFP4 cache.
+ *
+ * Row r sees, of the tokens that kvq_chunk_attention_nvfp4 would let it see,
+ * those in the blocks selected[r, 0 .. max_selected - 1]; the rest of the
+ * computation is the same.  A row that sees none gets zeros.  Negative
+ * entries are skipped.  Entries rise: one that does not lie above all entries
+ * before it, or whose block holds nothing that the row could see, is skipped
+ * and flagged (KVQ_DEVERR_SEQ).
+ * Arithmetic: as for kvq_chunk_attention_nvfp4.
+ *
+ * selected       int32 [total_q, max_selected], rows selected_stride0 apart
+ *                (those of kvq_select_blocks).
+ * select_block   a multiple of block_size; max_selected * select_block <=
+ *                2^20.
+ * workspace      at least kvq_sparse_attention_workspace_bytes(...) of the
+ *                call's sizes (else KVQ_ERR_SCRATCH), 32-byte aligned;
+ *                otherwise as for kvq_chunk_attention_nvfp4.
+ * All other arguments, flags, errors and limits as for
+ * kvq_chunk_attention_nvfp4.
+ */
+kvq_status kvq_sparse_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, const int32_t* selected,
+    int64_t selected_stride0, int32_t max_selected, int32_t select_block,
+    const float* k_scale, const float* v_scale, float scale, void* workspace,
+    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, void* stream);
+
+/* Workspace of a kvq_sparse_attention_nvfp4 call on the current device (-1:
+   sizes that the call refuses). */
+int64_t kvq_sparse_attention_workspace_bytes(
+    int64_t total_q, int32_t num_seqs, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t max_selected, int32_t select_block,
+    int32_t block_size, int32_t max_blocks_per_seq);
 
 /*
  * The page pool: the state of a paged cache on the device, for callers that

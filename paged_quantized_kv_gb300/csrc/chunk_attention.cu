@@ -485,6 +485,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
 // floor((row + G (L - n + 128)) / (128 G)) tiles.  From block to block the
 // row grows by 256, and the quotient is carried along.  (Rows are below 2^29,
 // contexts at most 2^26 tokens, groups at most 16: 32 bits.)
+template <bool kTree>
 struct Blocks {
   int left;   // rows from this block on
   int step;   // 128 G
@@ -495,12 +496,18 @@ struct Blocks {
                                         int i) {
     step = 128 * p.G;
     left = s.n * p.G - i * kRows;
+    if constexpr (kTree) {  // any row may see the last draft
+      tiles = (s.L + kKeys - 1) / kKeys;
+      rest = 0;
+      return;
+    }
     const int top = i * kRows + kRows - 1 + p.G * (s.L - s.n + 128);
     tiles = max(top, 0) / step;
     rest = top - tiles * step;
   }
   __device__ __forceinline__ void next() {
     left -= kRows;
+    if constexpr (kTree) return;
     rest += kRows;
     while (rest >= step) {
       rest -= step;
@@ -509,6 +516,7 @@ struct Blocks {
   }
   // Tiles of this block (a last block that is not full ends earlier).
   __device__ __forceinline__ int width() const {
+    if constexpr (kTree) return max(tiles, 1);
     const int short_by = max(kRows - left, 0) - rest;
     return max(tiles - (short_by > 0) - (short_by > step), 1);
   }
@@ -540,8 +548,9 @@ struct Walk {
   int seg, tiles;  // segments and tiles of the share before this one
   int there;       // (in the ring) this segment exists
 
+  template <bool kTree>
   __device__ __forceinline__ void enter(const ChunkParams& p) {
-    Blocks k;
+    Blocks<kTree> k;
     k.begin(p, s, block);
     W = k.width();
     two = k.left > 128;
@@ -551,6 +560,7 @@ struct Walk {
   }
   // To the next segment that has a tile (the first one: from a position with
   // rem set and kv0 == kv1); false: there is none.
+  template <bool kTree>
   __device__ __forceinline__ bool next(const ChunkParams& p, bool first) {
     if (!first) {
       ++seg;
@@ -573,7 +583,7 @@ struct Walk {
         }
       }
       first = false;
-      enter(p);
+      enter<kTree>(p);
     } while (kv0 >= kv1);
     return true;
   }
@@ -584,12 +594,13 @@ struct Walk {
 // each role would be larger than the loops it serves.  True for the whole
 // warp if there is another segment.  (The softmax warps take theirs from the
 // product warp, through a ring: a call would cost them registers.)
+template <bool kTree>
 __device__ __noinline__ bool advance(const ChunkParams& p, Walk* walk) {
   bool more = false;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     Walk w = *walk;
-    more = w.next(p, false);
+    more = w.next<kTree>(p, false);
     *walk = w;
   }
   __syncwarp();
@@ -628,6 +639,49 @@ __device__ __noinline__ void note_cut(const ChunkParams& p, const Walk& w,
   } while (end < size && snap(static_cast<int>(end), size) < size);
   *(reinterpret_cast<Cut*>(p.workspace) + cta) = {
       w.b, w.block, w.h, w.seg > 0, more, 0, {0, 0}};
+}
+
+// ---------------------------------------------------------------------------
+// Trees of drafts
+// ---------------------------------------------------------------------------
+// A row's word w, bit k: it sees draft 32 w + k of its sequence's n.
+struct Drafts {
+  const uint32_t* row;
+  int words, n;
+
+  // The bits of drafts d .. d + 31 (those below 0 and behind n - 1 are none).
+  __device__ __forceinline__ uint32_t bits(int d) const {
+    const int w = d >> 5, shift = d & 31;
+    const uint32_t lo = w >= 0 && w < words ? __ldg(row + w) : 0u;
+    const uint32_t hi = w >= -1 && w + 1 < words ? __ldg(row + w + 1) : 0u;
+    return __funnelshift_r(lo, hi, shift) & first_bits(n - 1 - d);
+  }
+};
+
+// Whether a row sees no draft from d0 >= 0 on.
+__device__ __noinline__ bool none_of(Drafts drafts, int d0) {
+  for (int d = d0; d < drafts.n && d < 32 * drafts.words; d += 32)
+    if (drafts.bits(d) != 0u) return false;
+  return true;
+}
+
+// Whether a draft that a row sees has NaN for its V scale of a group.
+__device__ __noinline__ bool draft_nan(const ChunkParams& p, const Walk& w,
+                                       Drafts drafts, int group) {
+  const int first = w.s.L - w.s.n;  // the drafts' first position
+  const int32_t* table = p.block_table + w.b * p.bt_stride;
+  for (int j = max(-first, 0); j < w.s.n && j < 32 * p.mask_words; ++j) {
+    if ((drafts.bits(j) & 1u) == 0u) continue;
+    const int page = (first + j) / p.B, off = first + j - page * p.B;
+    const int32_t blk = __ldg(table + page);
+    if (blk < 0 || blk >= p.num_blocks) continue;
+    const uint8_t code =
+        p.side[1][blk * p.page_stride + p.scale_off + w.h * p.shs +
+                  ((off & ~3) + (group >> 1)) * p.sts + (group & 1) * 4 +
+                  (off & 3)];
+    if ((code & 0x7F) == 0x7F) return true;
+  }
+  return false;
 }
 
 // ---------------------------------------------------------------------------
@@ -721,7 +775,7 @@ static_assert(kSmemBytes <= 227 * 1024 && kRawBytes % 16 == 0 &&
 // of the two slots.
 constexpr uint32_t kOCol = 256;
 
-template <bool kF16>
+template <bool kF16, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(16) uint8_t raw_smem[];
@@ -792,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (b < p.num_seqs) {
         s = seq_of(p, b);
         if (s.n > 0) {
-          Blocks k;
+          Blocks<kTree> k;
           k.begin(p, s, 0);
 #pragma unroll 1
           for (; k.left > 0; k.next()) units += k.units();
@@ -801,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r < rounds && blockIdx.x == 0) {
           const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
           if (c0 < 0 || c1 < c0 || c1 > p.total_q ||
-              __ldg(p.lens + b) > p.len_cap)
+              __ldg(p.lens + b) > p.len_cap ||
+              (kTree && c1 - c0 > 32 * p.mask_words))
             flag(p.dev_error, KVQ_DEVERR_SEQ);
         }
       }
@@ -839,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < incl - units || u >= incl) continue;
         int64_t rem = u - (incl - units);
         Walk w = {};
-        Blocks k;
+        Blocks<kTree> k;
         k.begin(p, s, 0);
 #pragma unroll 1
         for (; rem >= static_cast<int64_t>(k.units()) * p.Hkv; k.next()) {
@@ -860,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && units_kept[2] < units_kept[1]) {
       Walk w = ring[0];
       w.left = units_kept[1] - units_kept[2];
-      w.there = w.next(p, true);
+      w.there = w.next<kTree>(p, true);
       ring[0] = w;
       misc[2] = w.there;
     }
@@ -887,7 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cnt0 = 0, cnt1 = 0;  // tiles of the slots so far
 #pragma unroll 1
     for (uint32_t seg = 0; any;) {
+      // pos: the last token that the row sees (a tree: of those before the
+      // drafts; then the bits of `drafts`, its row of the mask)
       int kv0, kv1, pos, tiles, rows;
+      [[maybe_unused]] Drafts drafts;
       {
         const Walk& w = ring[seg & 3];
         kv0 = w.kv0;
@@ -900,7 +958,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = w.block * kRows + at;  // row of the sequence
         const int tok = r / p.G;
         // (a row that is none sees all, so that it does not slow the others)
-        pos = at < rows ? w.s.L - w.s.n + tok : INT32_MAX;
+        if constexpr (kTree) {
+          pos = at < rows ? w.s.L - w.s.n - 1 : INT32_MAX;
+          drafts = {p.mask + (w.s.q0 + (at < rows ? tok : 0)) * p.mask_stride,
+                    p.mask_words, w.s.n};
+        } else {
+          pos = at < rows ? w.s.L - w.s.n + tok : INT32_MAX;
+        }
         if (m == 0 || rows > 128) {
           // the query rows, rounded to fp16, their sign folded with the
           // scale's: two rows of the warp at a time, 16 bytes per lane (a
@@ -973,8 +1037,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             if (!__all_sync(0xFFFFFFFFu,
                             lim >= 63 && (valid.x & valid.y) == ~0u)) {
-              mask32(s, valid.x & first_bits(lim));
-              mask32(s + 32, valid.y & first_bits(lim - 32));
+              uint32_t see0 = first_bits(lim), see1 = first_bits(lim - 32);
+              if constexpr (kTree) {
+                // (column 0 is draft -1 - lim)
+                if (lim < 63) {
+                  see0 |= drafts.bits(-1 - lim);
+                  see1 |= drafts.bits(31 - lim);
+                }
+              }
+              mask32(s, valid.x & see0);
+              mask32(s + 32, valid.y & see1);
             }
             if (look) {
               const float top = max64(s) * c - kBelow;
@@ -1069,6 +1141,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = kv0 == 0 && kv1 == w.W;
       const float inv = sum > 0.0f ? __ldg(p.v_scale) / sum
                                    : (sum == 0.0f ? 0.0f : sum);
+      bool blind = pos < 0;
+      if constexpr (kTree) blind = blind && none_of(drafts, -1 - pos);
       float* slot = slot_of(p, blockIdx.x, seg > 0);
       const int r = w.block * kRows + at, tok = r / p.G;
       uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
@@ -1099,7 +1173,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
           const int4 x = nan_row[col / 16 + g];
-          if (min(min(x.x, x.y), min(x.z, x.w)) <= pos) {
+          const int first_nan = min(min(x.x, x.y), min(x.z, x.w));
+          bool nan = first_nan <= pos;
+          if constexpr (kTree) {
+            if (!nan && first_nan != INT32_MAX)
+              nan = draft_nan(p, w, drafts, col / 16 + g);
+          }
+          if (nan) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[16 * g + j] = 0x7FFFFFFFu;
           }
@@ -1111,7 +1191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float a = __uint_as_float(o[2 * g]) * inv;
             const float b = __uint_as_float(o[2 * g + 1]) * inv;
             // (a row that sees nothing gets zeros whatever the scales are)
-            x[g] = pos < 0 ? 0u
+            x[g] = blind ? 0u
                            : kF16 ? pack_f16x2(a, b) : pack_bf16x2(a, b);
           }
           if (wide) {
@@ -1226,7 +1306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++cnt;
           first = false;
           if (++kt == kv1) {
-            more = advance(p, walk);
+            more = advance<kTree>(p, walk);
             first = true;
             ++seg;
             kt = walk->kv0;
@@ -1411,7 +1491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the softmax warps too)
           if (m == 0 && lane == 0 && walk->kv0 == 0 && walk->kv1 < walk->W)
             note_cut(p, *walk, units_kept[0], units_kept[1]);
-          go = advance(p, walk);
+          go = advance<kTree>(p, walk);
           if (lane == 0) {
             if (m == 0) {
               Walk* next = ring + ((segs + 1) & 3);
@@ -1474,7 +1554,7 @@ gone:
 // ---------------------------------------------------------------------------
 constexpr int kMergeRows = 32;  // rows of a CTA, four to a warp
 
-template <bool kF16>
+template <bool kF16, bool kTree>
 __global__ void __launch_bounds__(256)
     chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1519,7 +1599,13 @@ __global__ void __launch_bounds__(256)
     uint16_t* dst = p.out + (s.q0 + tok) * p.out_stride0 + head * kD +
                     4 * lane;
     uint2 w = make_uint2(0, 0);
-    if (tok < blind) {
+    bool none = tok < blind;
+    if constexpr (kTree) {
+      const Drafts drafts = {p.mask + (s.q0 + tok) * p.mask_stride,
+                             p.mask_words, s.n};
+      none = blind >= 0 && none_of(drafts, blind);
+    }
+    if (none) {
       *reinterpret_cast<uint2*>(dst) = w;
       continue;
     }
@@ -1531,19 +1617,19 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <bool kF16>
+template <bool kF16, bool kTree>
 cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
   const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      chunk_kernel<kF16, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
       kSmemBytes);
   if (set != cudaSuccess) return set;
   const unsigned ctas = static_cast<unsigned>(sm_count());
   if (ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
-  const cudaError_t err = launch_kernel(chunk_kernel<kF16>, dim3(ctas),
-                                        kThreads, kSmemBytes, stream, p.pdl,
-                                        p);
+  const cudaError_t err = launch_kernel(chunk_kernel<kF16, kTree>,
+                                        dim3(ctas), kThreads, kSmemBytes,
+                                        stream, p.pdl, p);
   if (err != cudaSuccess) return err;
-  return launch_kernel(chunk_merge_kernel<kF16>,
+  return launch_kernel(chunk_merge_kernel<kF16, kTree>,
                        dim3(ctas, kRows / kMergeRows), 256, 0, stream, true,
                        p);
 }
@@ -1567,6 +1653,11 @@ static int short_chunk(const ChunkParams& p) {
   return few && p.max_q_len <= 8 ? p.max_q_len : 1;
 }
 
+cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream) {
+  return p.f16 ? launch<true, true>(p, stream)
+               : launch<false, true>(p, stream);
+}
+
 cudaError_t launch_chunk_attention(const ChunkParams& caller,
                                    cudaStream_t stream) {
   ChunkParams p = caller;
@@ -1582,7 +1673,8 @@ cudaError_t launch_chunk_attention(const ChunkParams& caller,
   cudaError_t err = cudaSuccess;
   const bool tiles = p.skip == 0 || p.max_q_len > p.skip;
   if (tiles)
-    err = p.f16 ? launch<true>(p, stream) : launch<false>(p, stream);
+    err = p.f16 ? launch<true, false>(p, stream)
+                : launch<false, false>(p, stream);
   if (err != cudaSuccess || p.skip == 0) return err;
   AttnParams a{};
   a.q = p.q;

@@ -492,7 +492,11 @@ int64_t kvq_chunk_attention_workspace_bytes(void) {
   return kvq::chunk_workspace_bytes(kvq::sm_count());
 }
 
-kvq_status kvq_chunk_attention_nvfp4(
+namespace {
+
+// The checks that the attentions of many query tokens per sequence share,
+// and their parameters; *empty: there is nothing to do.
+kvq_status chunk_check(
     const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
     int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
     int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
@@ -501,10 +505,10 @@ kvq_status kvq_chunk_attention_nvfp4(
     const int32_t* block_table, int64_t block_table_stride,
     int32_t max_blocks_per_seq, const int32_t* context_lens,
     int32_t max_context_len, const float* k_scale, const float* v_scale,
-    float scale, void* workspace,
-    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
-    int32_t* dev_error, void* stream) {
+    float scale, void* workspace, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, kvq::ChunkParams* params, bool* empty) {
   using namespace kvq;
+  *empty = false;
   if (dtype != KVQ_DTYPE_BF16 && dtype != KVQ_DTYPE_FP16) return KVQ_ERR_DTYPE;
   if (layout != KVQ_LAYOUT_HND && layout != KVQ_LAYOUT_NHD)
     return KVQ_ERR_LAYOUT;
@@ -530,7 +534,10 @@ kvq_status kvq_chunk_attention_nvfp4(
     return KVQ_ERR_SHAPE;
   if (total_q > kChunkMaxRows || num_seqs > kChunkMaxSeqs)
     return KVQ_ERR_SHAPE;
-  if (total_q == 0 || num_seqs == 0) return KVQ_OK;
+  if (total_q == 0 || num_seqs == 0) {
+    *empty = true;
+    return KVQ_OK;
+  }
   if (query == nullptr || cu_q_lens == nullptr || key_cache == nullptr ||
       value_cache == nullptr || block_table == nullptr ||
       context_lens == nullptr || k_scale == nullptr || v_scale == nullptr ||
@@ -543,10 +550,8 @@ kvq_status kvq_chunk_attention_nvfp4(
       !aligned(context_lens, 4) || !aligned(k_scale, 4) ||
       !aligned(v_scale, 4) || !aligned(workspace, 32))
     return KVQ_ERR_ALIGN;
-  if (workspace_bytes < chunk_workspace_bytes(sm_count()))
-    return KVQ_ERR_SCRATCH;
 
-  ChunkParams p{};
+  ChunkParams& p = *params;
   p.q = static_cast<const uint16_t*>(query);
   p.q_stride0 = query_stride0;
   p.side[0] = key_cache;
@@ -591,8 +596,308 @@ kvq_status kvq_chunk_attention_nvfp4(
   p.swizzle_k = (flags & KVQ_F_SWIZZLE_K_SCALE) != 0u;
   p.f16 = dtype == KVQ_DTYPE_FP16;
   p.pdl = (flags & KVQ_F_PDL) != 0u;
+  return KVQ_OK;
+}
+
+}  // namespace
+
+kvq_status kvq_chunk_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, const float* k_scale, const float* v_scale,
+    float scale, void* workspace,
+    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, void* stream) {
+  using namespace kvq;
+  ChunkParams p{};
+  bool empty;
+  const kvq_status st = chunk_check(
+      query, query_stride0, dtype, total_q, num_seqs, cu_q_lens, max_q_len,
+      num_q_heads, num_kv_heads, head_size, key_cache, value_cache,
+      page_stride, block_size, num_blocks, layout, block_table,
+      block_table_stride, max_blocks_per_seq, context_lens, max_context_len,
+      k_scale, v_scale, scale, workspace, out, out_stride0, flags, dev_error,
+      &p, &empty);
+  if (st != KVQ_OK || empty) return st;
+  if (workspace_bytes < chunk_workspace_bytes(sm_count()))
+    return KVQ_ERR_SCRATCH;
   const cudaError_t err =
       launch_chunk_attention(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_tree_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, const int32_t* tree_mask,
+    int64_t tree_mask_stride0, int32_t mask_words, const float* k_scale,
+    const float* v_scale, float scale,
+    void* workspace, int64_t workspace_bytes, void* out, int64_t out_stride0,
+    uint32_t flags, int32_t* dev_error, void* stream) {
+  using namespace kvq;
+  ChunkParams p{};
+  bool empty;
+  const kvq_status st = chunk_check(
+      query, query_stride0, dtype, total_q, num_seqs, cu_q_lens, max_q_len,
+      num_q_heads, num_kv_heads, head_size, key_cache, value_cache,
+      page_stride, block_size, num_blocks, layout, block_table,
+      block_table_stride, max_blocks_per_seq, context_lens, max_context_len,
+      k_scale, v_scale, scale, workspace, out, out_stride0, flags, dev_error,
+      &p, &empty);
+  if (st != KVQ_OK) return st;
+  if (mask_words <= 0 || mask_words > kTreeMaxWords ||
+      tree_mask_stride0 < mask_words)
+    return KVQ_ERR_SHAPE;
+  if (empty) return KVQ_OK;
+  if (tree_mask == nullptr) return KVQ_ERR_NULL;
+  if (!aligned(tree_mask, 4)) return KVQ_ERR_ALIGN;
+  if (workspace_bytes < chunk_workspace_bytes(sm_count()))
+    return KVQ_ERR_SCRATCH;
+  p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.mask_stride = tree_mask_stride0;
+  p.mask_words = mask_words;
+  const cudaError_t err =
+      launch_tree_attention(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+namespace {
+
+// Whether lists of max_selected blocks of select_block tokens can be.
+bool selection_ok(int32_t max_selected, int32_t select_block,
+                  int32_t block_size) {
+  return max_selected > 0 && select_block > 0 && block_size > 0 &&
+         select_block % block_size == 0 &&
+         static_cast<int64_t>(max_selected) * select_block <=
+             kvq::kSparseMaxTokens;
+}
+
+}  // namespace
+
+int64_t kvq_sparse_attention_workspace_bytes(
+    int64_t total_q, int32_t num_seqs, int32_t num_q_heads,
+    int32_t num_kv_heads, int32_t max_selected, int32_t select_block,
+    int32_t block_size, int32_t max_blocks_per_seq) {
+  using namespace kvq;
+  if (total_q < 0 || total_q > kChunkMaxRows || num_seqs < 0 ||
+      num_seqs > kChunkMaxSeqs || num_kv_heads <= 0 || num_q_heads <= 0 ||
+      num_q_heads > 1024 || num_q_heads % num_kv_heads != 0 ||
+      max_blocks_per_seq < 0 ||
+      !selection_ok(max_selected, select_block, block_size))
+    return -1;
+  return sparse_workspace_bytes(sm_count(), total_q, num_q_heads,
+                                max_selected, select_block, block_size);
+}
+
+kvq_status kvq_sparse_attention_nvfp4(
+    const void* query, int64_t query_stride0, int32_t dtype, int64_t total_q,
+    int32_t num_seqs, const int32_t* cu_q_lens, int32_t max_q_len,
+    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_size,
+    const uint8_t* key_cache, const uint8_t* value_cache, int64_t page_stride,
+    int32_t block_size, int64_t num_blocks, int32_t layout,
+    const int32_t* block_table, int64_t block_table_stride,
+    int32_t max_blocks_per_seq, const int32_t* context_lens,
+    int32_t max_context_len, const int32_t* selected,
+    int64_t selected_stride0, int32_t max_selected, int32_t select_block,
+    const float* k_scale, const float* v_scale, float scale, void* workspace,
+    int64_t workspace_bytes, void* out, int64_t out_stride0, uint32_t flags,
+    int32_t* dev_error, void* stream) {
+  using namespace kvq;
+  SparseParams p{};
+  bool empty;
+  const kvq_status st = chunk_check(
+      query, query_stride0, dtype, total_q, num_seqs, cu_q_lens, max_q_len,
+      num_q_heads, num_kv_heads, head_size, key_cache, value_cache,
+      page_stride, block_size, num_blocks, layout, block_table,
+      block_table_stride, max_blocks_per_seq, context_lens, max_context_len,
+      k_scale, v_scale, scale, workspace, out, out_stride0, flags, dev_error,
+      &p.chunk, &empty);
+  if (st != KVQ_OK) return st;
+  if (!selection_ok(max_selected, select_block, block_size) ||
+      selected_stride0 < max_selected)
+    return KVQ_ERR_SHAPE;
+  if (empty) return KVQ_OK;
+  if (selected == nullptr) return KVQ_ERR_NULL;
+  if (!aligned(selected, 4)) return KVQ_ERR_ALIGN;
+  if (workspace_bytes < sparse_workspace_bytes(sm_count(), total_q,
+                                               num_q_heads, max_selected,
+                                               select_block, block_size))
+    return KVQ_ERR_SCRATCH;
+  p.rows = {cu_q_lens, context_lens, total_q,
+            num_seqs,  p.chunk.len_cap, dev_error};
+  p.selected = selected;
+  p.selected_stride0 = selected_stride0;
+  p.top = max_selected;
+  p.sel = select_block;
+  const cudaError_t err =
+      launch_sparse_attention(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_quantize_indexer_q(
+    const void* q, int64_t q_stride0, int32_t dtype, const float* weights,
+    int64_t weights_stride0, float scale, int64_t total_q, int32_t num_heads,
+    int32_t head_dim, uint8_t* q_fp8, float* weights_out, uint32_t flags,
+    void* stream) {
+  using namespace kvq;
+  if (dtype != KVQ_DTYPE_BF16 && dtype != KVQ_DTYPE_FP16) return KVQ_ERR_DTYPE;
+  if ((flags & ~static_cast<uint32_t>(KVQ_F_PDL)) != 0u) return KVQ_ERR_ARG;
+  if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
+    return KVQ_ERR_ARG;
+  if (total_q < 0 || total_q > kChunkMaxRows || num_heads <= 0 ||
+      num_heads > 1024)
+    return KVQ_ERR_SHAPE;
+  if (head_dim != 16 && head_dim != 32 && head_dim != 64 && head_dim != 128 &&
+      head_dim != 256)
+    return KVQ_ERR_SHAPE;
+  if (q_stride0 < static_cast<int64_t>(num_heads) * head_dim ||
+      weights_stride0 < num_heads)
+    return KVQ_ERR_SHAPE;
+  if (total_q == 0) return KVQ_OK;
+  if (q == nullptr || weights == nullptr || q_fp8 == nullptr ||
+      weights_out == nullptr)
+    return KVQ_ERR_NULL;
+  if (!aligned(q, 16) || q_stride0 % 8 != 0 || !aligned(weights, 4) ||
+      !aligned(q_fp8, 16) || !aligned(weights_out, 4))
+    return KVQ_ERR_ALIGN;
+  QuantizeQParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride0 = q_stride0;
+  p.weights = weights;
+  p.w_stride0 = weights_stride0;
+  p.scale = scale;
+  p.q_fp8 = q_fp8;
+  p.w_out = weights_out;
+  p.total = total_q;
+  p.heads = num_heads;
+  p.D = head_dim;
+  p.f16 = dtype == KVQ_DTYPE_FP16;
+  p.pdl = (flags & KVQ_F_PDL) != 0u;
+  const cudaError_t err =
+      launch_quantize_q(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_score_blocks_indexer_k(
+    const uint8_t* q_fp8, int64_t q_stride0, const float* weights,
+    int64_t weights_stride0, int64_t total_q, int32_t num_seqs,
+    const int32_t* cu_q_lens, int32_t max_q_len, int32_t num_heads,
+    int32_t head_dim, const uint8_t* kv_cache, int64_t block_stride,
+    int64_t num_blocks, int32_t block_size, const int32_t* block_table,
+    int64_t block_table_stride, int32_t max_blocks_per_seq,
+    const int32_t* context_lens, int32_t select_block, float* scores,
+    int64_t scores_stride0, int32_t num_columns, uint32_t flags,
+    int32_t* dev_error, void* stream) {
+  using namespace kvq;
+  if ((flags & ~static_cast<uint32_t>(KVQ_F_PDL)) != 0u) return KVQ_ERR_ARG;
+  if (total_q < 0 || total_q > kChunkMaxRows || num_seqs < 0 ||
+      num_seqs > kChunkMaxSeqs || max_q_len < 0 || num_heads <= 0 ||
+      num_heads > kScoreMaxHeads || block_size <= 0 || num_blocks < 0 ||
+      max_blocks_per_seq < 0 || block_table_stride < max_blocks_per_seq ||
+      num_columns < 0 || scores_stride0 < num_columns)
+    return KVQ_ERR_SHAPE;
+  if (head_dim != 32 && head_dim != 64 && head_dim != 128)
+    return KVQ_ERR_SHAPE;
+  if (select_block != 16 && select_block != 32 && select_block != 64 &&
+      select_block != 128)
+    return KVQ_ERR_SHAPE;
+  if (static_cast<int64_t>(num_columns) * select_block > kChunkMaxContext)
+    return KVQ_ERR_SHAPE;
+  if (q_stride0 < static_cast<int64_t>(num_heads) * head_dim ||
+      weights_stride0 < num_heads ||
+      block_stride < static_cast<int64_t>(block_size) * (head_dim + 4))
+    return KVQ_ERR_SHAPE;
+  if (total_q == 0 || num_seqs == 0 || num_columns == 0) return KVQ_OK;
+  if (q_fp8 == nullptr || weights == nullptr || cu_q_lens == nullptr ||
+      kv_cache == nullptr || block_table == nullptr ||
+      context_lens == nullptr || scores == nullptr)
+    return KVQ_ERR_NULL;
+  if (!aligned(q_fp8, 16) || q_stride0 % 16 != 0 || !aligned(weights, 4) ||
+      !aligned(kv_cache, 16) || block_stride % 16 != 0 ||
+      !aligned(cu_q_lens, 4) || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4) || !aligned(scores, 4))
+    return KVQ_ERR_ALIGN;
+  ScoreParams p{};
+  p.rows = {cu_q_lens, context_lens, total_q, num_seqs, 0, dev_error};
+  p.rows.len_cap = static_cast<int32_t>(
+      std::min(static_cast<int64_t>(max_blocks_per_seq) * block_size,
+               static_cast<int64_t>(num_columns) * select_block));
+  p.q = q_fp8;
+  p.q_stride0 = q_stride0;
+  p.weights = weights;
+  p.w_stride0 = weights_stride0;
+  p.cache = kv_cache;
+  p.block_stride = block_stride;
+  p.num_blocks = num_blocks;
+  p.block_table = block_table;
+  p.bt_stride = block_table_stride;
+  p.scores = scores;
+  p.scores_stride0 = scores_stride0;
+  p.heads = num_heads;
+  p.D = head_dim;
+  p.B = block_size;
+  p.b_shift = ilog2_exact(block_size);
+  p.sel = select_block;
+  p.columns = num_columns;
+  p.max_q_len = max_q_len;
+  p.pdl = (flags & KVQ_F_PDL) != 0u;
+  const cudaError_t err =
+      launch_score_blocks(p, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
+}
+
+kvq_status kvq_select_blocks(const float* scores, int64_t scores_stride0,
+                             int32_t num_columns, int64_t total_q,
+                             int32_t num_seqs, const int32_t* cu_q_lens,
+                             const int32_t* context_lens,
+                             int32_t select_block, int32_t num_first,
+                             int32_t num_last, int32_t* selected,
+                             int64_t selected_stride0, int32_t max_selected,
+                             uint32_t flags, int32_t* dev_error,
+                             void* stream) {
+  using namespace kvq;
+  if ((flags & ~static_cast<uint32_t>(KVQ_F_PDL)) != 0u) return KVQ_ERR_ARG;
+  if (num_columns < 0 || scores_stride0 < num_columns || total_q < 0 ||
+      total_q > kChunkMaxRows || num_seqs < 0 || num_seqs > kChunkMaxSeqs ||
+      select_block <= 0 || max_selected <= 0 ||
+      selected_stride0 < max_selected)
+    return KVQ_ERR_SHAPE;
+  if (static_cast<int64_t>(num_columns) * select_block > kChunkMaxContext)
+    return KVQ_ERR_SHAPE;
+  if (num_first < 0 || num_last < 0 || num_first > max_selected ||
+      num_last > max_selected - num_first)
+    return KVQ_ERR_ARG;
+  if (total_q == 0 || num_seqs == 0) return KVQ_OK;
+  if ((scores == nullptr && num_columns > 0) || cu_q_lens == nullptr ||
+      context_lens == nullptr || selected == nullptr)
+    return KVQ_ERR_NULL;
+  if (!aligned(scores, 4) || !aligned(cu_q_lens, 4) ||
+      !aligned(context_lens, 4) || !aligned(selected, 4))
+    return KVQ_ERR_ALIGN;
+  SelectParams p{};
+  p.rows = {cu_q_lens, context_lens, total_q, num_seqs,
+            num_columns * select_block, dev_error};
+  p.scores = scores;
+  p.scores_stride0 = scores_stride0;
+  p.selected = selected;
+  p.selected_stride0 = selected_stride0;
+  p.sel = select_block;
+  p.top = max_selected;
+  p.first = num_first;
+  p.last = num_last;
+  p.pdl = (flags & KVQ_F_PDL) != 0u;
+  const cudaError_t err =
+      launch_select_blocks(p, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;
 }
 

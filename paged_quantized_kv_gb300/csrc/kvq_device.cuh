@@ -6,6 +6,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kvq.h"
+#include "kvq_internal.h"
+
 namespace kvq {
 namespace dev {
 
@@ -169,6 +172,49 @@ __device__ __forceinline__ bool stage_meta(uint8_t* smem, uint64_t* bar,
   }
   __syncthreads();
   return ok;
+}
+
+// ---------------------------------------------------------------------------
+// Query rows of a ragged batch
+// ---------------------------------------------------------------------------
+// A row's sequence (-1: none), its place in it, the tokens that it sees.
+struct QueryRow {
+  int seq, i, seen;
+};
+
+// The row's sequence by a search in cu, 32 places at a time; every lane of
+// the warp calls it with the same row.
+__device__ __forceinline__ QueryRow query_row(const QueryRows& q, int row) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = q.num_seqs;  // between them: how many begin at row or before
+  while (lo < hi) {
+    const int step = (hi - lo + 31) >> 5;
+    const int at = lo + lane * step;
+    const int n = __popc(
+        __ballot_sync(0xFFFFFFFFu, at < hi && __ldg(q.cu + at) <= row));
+    hi = min(hi, lo + n * step);
+    if (n > 0) lo += (n - 1) * step + 1;
+  }
+  if (lo == 0) return {-1, 0, 0};
+  const int b = lo - 1, c0 = __ldg(q.cu + b);
+  const int c1 = static_cast<int>(
+      min(static_cast<int64_t>(__ldg(q.cu + b + 1)), q.total));
+  const int L = min(max(__ldg(q.lens + b), 0), q.len_cap);
+  if (row < c0 || row >= c1) return {-1, 0, 0};
+  return {b, row - c0, max(L - (c1 - row) + 1, 0)};
+}
+
+// Offsets out of order or out of range, and contexts that are too long: a
+// flag, by the threads tid of n.
+__device__ __forceinline__ void check_rows(const QueryRows& q, int tid,
+                                           int n) {
+  if (q.dev_error == nullptr) return;
+  bool bad = false;
+  for (int b = tid; b < q.num_seqs; b += n) {
+    const int c0 = __ldg(q.cu + b), c1 = __ldg(q.cu + b + 1);
+    bad |= c0 < 0 || c1 < c0 || c1 > q.total || __ldg(q.lens + b) > q.len_cap;
+  }
+  if (bad) atomicOr(q.dev_error, KVQ_DEVERR_SEQ);
 }
 
 }  // namespace dev

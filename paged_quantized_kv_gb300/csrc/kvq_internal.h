@@ -151,6 +151,9 @@ struct AttnParams {
   int64_t total_q;
   int32_t per_seq;
   bool only_short;         // a longer chunk is an error
+  // Rows of block lists (kvq_sparse_attention_nvfp4; cu set too): row b has
+  // block-table row b and length lens[b], below 0 for a row that is none.
+  bool listed;
 };
 
 cudaError_t launch_paged_attention_mma(const AttnParams& p,
@@ -196,6 +199,11 @@ struct ChunkParams {
   int32_t max_q_len;
   int32_t len_cap;         // min(max_context_len, max_blocks * B)
   int32_t skip;            // chunks of up to this many tokens are left out
+  // Trees of drafts (kvq_tree_attention_nvfp4): rows of mask_words words,
+  // mask_stride apart.
+  const uint32_t* mask;
+  int64_t mask_stride;
+  int32_t mask_words;
   bool swizzle_k;
   bool f16;
   bool pdl;
@@ -207,8 +215,93 @@ constexpr int kChunkMaxContext = 1 << 26;
 constexpr int kChunkMaxRows = 1 << 25;
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream);
 // Workspace bytes of a call on a device of `sms` multiprocessors.
 int64_t chunk_workspace_bytes(int sms);
+
+// ---------------------------------------------------------------------------
+// Query rows of a ragged batch
+// ---------------------------------------------------------------------------
+struct QueryRows {
+  const int32_t* cu;       // cu_q_lens [num_seqs + 1]
+  const int32_t* lens;     // context_lens [num_seqs]
+  int64_t total;           // rows
+  int32_t num_seqs;
+  int32_t len_cap;         // longest context allowed
+  int32_t* dev_error;      // nullable
+};
+
+// ---------------------------------------------------------------------------
+// Indexer queries, block scores, block selection
+// ---------------------------------------------------------------------------
+struct QuantizeQParams {
+  const uint16_t* q;       // [total, heads, D] bf16/fp16 bits
+  int64_t q_stride0;       // elements
+  const float* weights;    // [total, heads]
+  int64_t w_stride0;
+  float scale;
+  uint8_t* q_fp8;          // [total, heads, D]
+  float* w_out;            // [total, heads]
+  int64_t total;
+  int32_t heads, D;
+  bool f16, pdl;
+};
+cudaError_t launch_quantize_q(const QuantizeQParams& p, cudaStream_t stream);
+
+struct ScoreParams {
+  QueryRows rows;
+  const uint8_t* q;        // [total, heads, D] e4m3
+  int64_t q_stride0;
+  const float* weights;    // [total, heads]
+  int64_t w_stride0;
+  const uint8_t* cache;    // block 0: [B*D e4m3 | B*4 scale bytes]
+  int64_t block_stride;
+  int64_t num_blocks;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  float* scores;           // [total, columns]
+  int64_t scores_stride0;
+  int32_t heads, D, B;
+  int32_t b_shift;         // log2(B) when B is a power of two, else -1
+  int32_t sel, columns;
+  int32_t max_q_len;
+  bool pdl;
+};
+constexpr int kTreeMaxWords = 32;  // (1024 drafts)
+constexpr int kScoreMaxHeads = 128;
+cudaError_t launch_score_blocks(const ScoreParams& p, cudaStream_t stream);
+
+struct SelectParams {
+  QueryRows rows;
+  const float* scores;     // [total, columns]
+  int64_t scores_stride0;
+  int32_t* selected;       // [total, top]
+  int64_t selected_stride0;
+  int32_t sel, top, first, last;
+  bool pdl;
+};
+cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t stream);
+
+// ---------------------------------------------------------------------------
+// Attention over selected blocks of the NVFP4 cache
+// ---------------------------------------------------------------------------
+constexpr int64_t kSparseMaxTokens = 1 << 20;  // of a list's blocks
+struct SparseParams {
+  ChunkParams chunk;       // (query, pages, output, workspace)
+  QueryRows rows;
+  const int32_t* selected;  // [total, top]
+  int64_t selected_stride0;
+  int32_t top, sel;
+  // a round of rows: the first, how many, their lengths and tables
+  int64_t row0;
+  int32_t num_rows;
+  int32_t* row_lens;
+  int32_t* row_table;
+};
+cudaError_t launch_sparse_attention(const SparseParams& p,
+                                    cudaStream_t stream);
+int64_t sparse_workspace_bytes(int sms, int64_t total, int32_t Hq,
+                               int32_t top, int32_t sel, int32_t B);
 
 // ---------------------------------------------------------------------------
 // Page pool: growing, forking, compacting and freeing sequences

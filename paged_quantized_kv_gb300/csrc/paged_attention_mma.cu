@@ -191,7 +191,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ---------------------------------------------------------------------------
 // Row b of a launch: its query and output row, its sequence (block-table
 // row) and its context length.  A decode step's row b is sequence b.  In a
-// launch for chunks (kChunk) it is new token b % per_seq of sequence b / per_seq, which sees the
+// launch for chunks (kChunk) that is not one of block lists it is new token b % per_seq of sequence b / per_seq, which sees the
 // context up to itself; a token that the sequence does not have, or whose
 // sequence has more than per_seq of them, is none (live false).
 struct Row {
@@ -207,6 +207,11 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
     r.L = __ldg(p.lens + b);
     r.bad = r.L < 0 || r.L > p.len_cap;
     r.L = max(0, min(r.L, p.len_cap));
+    return r;
+  }
+  if (p.listed) {
+    r.L = __ldg(p.lens + b);
+    r.live = r.L >= 0;
     return r;
   }
   r.seq = b / p.per_seq;

@@ -27,6 +27,10 @@ Additions of this library (no counterpart in the pages):
 
 * ``kvq_chunk_attention_nvfp4`` -- causal attention of chunks of new tokens
   over the NVFP4 pages.
+* ``kvq_tree_attention_nvfp4`` -- the same for trees of drafted tokens.
+* ``kvq_quantize_indexer_q``, ``kvq_score_blocks_indexer_k``,
+  ``kvq_select_blocks``, ``kvq_sparse_attention_nvfp4`` -- attention over
+  blocks of the context that an indexer selects for each query.
 * ``kvq_extend_sequences``, ``kvq_fork_sequences``,
   ``kvq_compact_sequences``, ``kvq_free_sequences`` -- the state of a paged
   cache (``alloc_page_pool``) on the device.
@@ -134,6 +138,30 @@ def lib() -> ctypes.CDLL:
         L.kvq_chunk_attention_nvfp4.restype = c.c_int
         L.kvq_chunk_attention_workspace_bytes.argtypes = []
         L.kvq_chunk_attention_workspace_bytes.restype = c.c_int64
+        attention = L.kvq_chunk_attention_nvfp4.argtypes
+        L.kvq_tree_attention_nvfp4.argtypes = attention[:21] + [
+            P, c.c_int64, c.c_int32] + attention[21:]
+        L.kvq_tree_attention_nvfp4.restype = c.c_int
+        L.kvq_sparse_attention_nvfp4.argtypes = attention[:21] + [
+            P, c.c_int64, c.c_int32, c.c_int32] + attention[21:]
+        L.kvq_sparse_attention_nvfp4.restype = c.c_int
+        L.kvq_sparse_attention_workspace_bytes.argtypes = [
+            c.c_int64] + [c.c_int32] * 7
+        L.kvq_sparse_attention_workspace_bytes.restype = c.c_int64
+        L.kvq_quantize_indexer_q.argtypes = [
+            P, c.c_int64, c.c_int32, P, c.c_int64, c.c_float, c.c_int64,
+            c.c_int32, c.c_int32, P, P, c.c_uint32, P]
+        L.kvq_quantize_indexer_q.restype = c.c_int
+        L.kvq_score_blocks_indexer_k.argtypes = [
+            P, c.c_int64, P, c.c_int64, c.c_int64, c.c_int32, P, c.c_int32,
+            c.c_int32, c.c_int32, P, c.c_int64, c.c_int64, c.c_int32, P,
+            c.c_int64, c.c_int32, P, c.c_int32, P, c.c_int64, c.c_int32,
+            c.c_uint32, P, P]
+        L.kvq_score_blocks_indexer_k.restype = c.c_int
+        L.kvq_select_blocks.argtypes = [
+            P, c.c_int64, c.c_int32, c.c_int64, c.c_int32, P, P, c.c_int32,
+            c.c_int32, c.c_int32, P, c.c_int64, c.c_int32, c.c_uint32, P, P]
+        L.kvq_select_blocks.restype = c.c_int
         pool = [P, c.c_int64, P, c.c_int64, c.c_int32, c.c_int32, P]
         L.kvq_extend_sequences.argtypes = pool + [
             c.c_int32, P, P, c.c_int32, P, c.c_int64, c.c_uint32, P, P]
@@ -479,30 +507,32 @@ def chunk_attention_workspace(device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
-                              value_cache: torch.Tensor,
-                              block_table: torch.Tensor,
-                              cu_q_lens: torch.Tensor,
-                              context_lens: torch.Tensor,
-                              k_scale: torch.Tensor, v_scale: torch.Tensor,
-                              scale: float, out: torch.Tensor,
-                              max_q_len: int,
-                              workspace: torch.Tensor | None = None,
-                              max_context_len: int = 0, flags: int = 0,
-                              dev_error: torch.Tensor | None = None,
-                              stream: int | None = None) -> None:
-    """Causal attention of chunks of new tokens over the NVFP4 cache (see
-    ``include/kvq.h``).
+def _rows_of(fn: str, t: torch.Tensor, dtype: torch.dtype, total: int) -> int:
+    """The row stride of a matrix [total, width] with contiguous rows."""
+    if t.dtype is not dtype:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if (t.dim() != 2 or t.size(0) != total
+            or (t.size(1) > 1 and t.stride(1) != 1 and t.numel() > 0)):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    return t.stride(0) if total > 1 else t.size(1)
 
-    query / out: bf16 or fp16 [total_q, Hq, 128] (last two dims contiguous);
-    sequence b's new tokens are rows cu_q_lens[b] .. cu_q_lens[b+1] - 1 and
-    the last of its context_lens[b] cached tokens.  key_cache / value_cache:
-    the store's 4-D page views; block_table int32 [num_seqs, max_blocks];
-    cu_q_lens int32 [num_seqs + 1]; context_lens int32 [num_seqs];
-    max_q_len: the longest chunk; max_context_len: the longest context (0:
-    the block table's width).  The workspace (``chunk_attention_workspace``)
-    is allocated here when it is not given."""
-    fn = "kvq_chunk_attention_nvfp4"
+
+def _record(t: torch.Tensor, here: int, stream: int | None) -> None:
+    """Memory allocated here is not handed out again before `stream` is past
+    it."""
+    if stream is not None and stream != here:
+        t.record_stream(torch.cuda.ExternalStream(
+            stream, device=t.device) if stream else
+            torch.cuda.default_stream(t.device))
+
+
+def _attend(fn: str, query, key_cache, value_cache, block_table, cu_q_lens,
+            context_lens, tensors, extra, k_scale, v_scale, scale, out,
+            max_q_len, workspace, make_workspace, max_context_len, flags,
+            dev_error, stream) -> None:
+    """What the attentions of many query tokens per sequence share: checks
+    and the call, with the arguments `extra` (of `tensors`) behind the
+    contexts'."""
     dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
     if query.dtype not in dtypes or out.dtype != query.dtype:
         raise KvqError(fn, KVQ_ERR_DTYPE)
@@ -528,17 +558,14 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     _dev_error_ok(fn, dev_error)
     here = _here(fn, query, out, key_cache, value_cache, block_table,
                  cu_q_lens, context_lens, k_scale, v_scale, workspace,
-                 dev_error)
+                 dev_error, *tensors)
     if workspace is None:
-        workspace = chunk_attention_workspace(query.device)
-        if stream is not None and stream != here:
-            # (not to be handed out again before that stream is past it)
-            workspace.record_stream(torch.cuda.ExternalStream(
-                stream, device=query.device) if stream else
-                torch.cuda.default_stream(query.device))
+        workspace = (make_workspace() if make_workspace is not None
+                     else chunk_attention_workspace(query.device))
+        _record(workspace, here, stream)
     if not workspace.is_contiguous():
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    st = lib().kvq_chunk_attention_nvfp4(
+    st = getattr(lib(), fn)(
         query.data_ptr(), query.stride(0) if total > 1 else Hq * D,
         dtypes[query.dtype], total, n, cu_q_lens.data_ptr(), int(max_q_len),
         Hq, key_cache.size(2), D, key_cache.data_ptr(),
@@ -546,11 +573,237 @@ def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
         key_cache.size(0), layout, block_table.data_ptr(),
         block_table.stride(0) if n > 1 else block_table.size(1),
         block_table.size(1), context_lens.data_ptr(), int(max_context_len),
-        k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
+        *extra, k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         out.data_ptr(), out.stride(0) if total > 1 else Hq * D, int(flags),
         _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
+
+
+def kvq_chunk_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
+                              value_cache: torch.Tensor,
+                              block_table: torch.Tensor,
+                              cu_q_lens: torch.Tensor,
+                              context_lens: torch.Tensor,
+                              k_scale: torch.Tensor, v_scale: torch.Tensor,
+                              scale: float, out: torch.Tensor,
+                              max_q_len: int,
+                              workspace: torch.Tensor | None = None,
+                              max_context_len: int = 0, flags: int = 0,
+                              dev_error: torch.Tensor | None = None,
+                              stream: int | None = None) -> None:
+    """Causal attention of chunks of new tokens over the NVFP4 cache (see
+    ``include/kvq.h``).
+
+    query / out: bf16 or fp16 [total_q, Hq, 128] (last two dims contiguous);
+    sequence b's new tokens are rows cu_q_lens[b] .. cu_q_lens[b+1] - 1 and
+    the last of its context_lens[b] cached tokens.  key_cache / value_cache:
+    the store's 4-D page views; block_table int32 [num_seqs, max_blocks];
+    cu_q_lens int32 [num_seqs + 1]; context_lens int32 [num_seqs];
+    max_q_len: the longest chunk; max_context_len: the longest context (0:
+    the block table's width).  The workspace (``chunk_attention_workspace``)
+    is allocated here when it is not given."""
+    _attend("kvq_chunk_attention_nvfp4", query, key_cache, value_cache,
+            block_table, cu_q_lens, context_lens, (), (), k_scale, v_scale,
+            scale, out, max_q_len, workspace, None, max_context_len, flags,
+            dev_error, stream)
+
+
+def kvq_tree_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
+                             value_cache: torch.Tensor,
+                             block_table: torch.Tensor,
+                             cu_q_lens: torch.Tensor,
+                             context_lens: torch.Tensor,
+                             tree_mask: torch.Tensor, k_scale: torch.Tensor,
+                             v_scale: torch.Tensor, scale: float,
+                             out: torch.Tensor, max_q_len: int,
+                             workspace: torch.Tensor | None = None,
+                             max_context_len: int = 0, flags: int = 0,
+                             dev_error: torch.Tensor | None = None,
+                             stream: int | None = None) -> None:
+    """Attention of trees of drafted tokens over the NVFP4 cache (see
+    ``include/kvq.h``): sequence b's drafts are rows cu_q_lens[b] ..
+    cu_q_lens[b+1] - 1 and the last of its context_lens[b] cached tokens;
+    bit j % 32 of tree_mask[r, j // 32] (int32 [total_q, words]) lets row r
+    see its sequence's draft j.  Everything else as for
+    ``kvq_chunk_attention_nvfp4``."""
+    fn = "kvq_tree_attention_nvfp4"
+    stride = _rows_of(fn, tree_mask, torch.int32, query.size(0))
+    _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
+            context_lens, (tree_mask,),
+            (tree_mask.data_ptr(), stride, tree_mask.size(1)), k_scale,
+            v_scale, scale, out, max_q_len, workspace, None, max_context_len,
+            flags, dev_error, stream)
+
+
+def kvq_quantize_indexer_q(q: torch.Tensor, weights: torch.Tensor,
+                           scale: float, q_fp8: torch.Tensor,
+                           weights_out: torch.Tensor, flags: int = 0,
+                           stream: int | None = None) -> None:
+    """The indexer's queries to fp8 (see ``include/kvq.h``): q bf16 or fp16
+    [total_q, heads, head_dim] into q_fp8 (1-byte elements, the same shape,
+    contiguous), weights fp32 [total_q, heads] times scale and each head's
+    scale into weights_out (contiguous)."""
+    fn = "kvq_quantize_indexer_q"
+    dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
+    if q.dtype not in dtypes or q_fp8.element_size() != 1:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if weights_out.dtype is not torch.float32:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if q.dim() != 3 or q_fp8.shape != q.shape:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    total, heads, D = q.shape
+    stride = _rows_of(fn, weights, torch.float32, total)
+    if (q.stride(2) != 1 or q.stride(1) != D or weights.size(1) != heads
+            or tuple(weights_out.shape) != (total, heads)
+            or not q_fp8.is_contiguous() or not weights_out.is_contiguous()):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    here = _here(fn, q, weights, q_fp8, weights_out)
+    st = lib().kvq_quantize_indexer_q(
+        q.data_ptr(), q.stride(0) if total > 1 else heads * D,
+        dtypes[q.dtype], weights.data_ptr(), stride, float(scale), total,
+        heads, D, q_fp8.data_ptr(), weights_out.data_ptr(), int(flags),
+        here if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_score_blocks_indexer_k(q_fp8: torch.Tensor, weights: torch.Tensor,
+                               kv_cache: torch.Tensor,
+                               block_table: torch.Tensor,
+                               cu_q_lens: torch.Tensor,
+                               context_lens: torch.Tensor,
+                               scores: torch.Tensor, select_block: int,
+                               max_q_len: int,
+                               block_size: int | None = None, flags: int = 0,
+                               dev_error: torch.Tensor | None = None,
+                               stream: int | None = None) -> None:
+    """The indexer's score of every block of select_block tokens for every
+    query row (see ``include/kvq.h``): q_fp8 e4m3 [total_q, heads, head_dim]
+    and weights fp32 [total_q, heads] (``kvq_quantize_indexer_q``) against
+    kv_cache uint8 [num_blocks, block_size, head_dim + 4] (or [num_blocks,
+    bytes] with ``block_size`` given), into scores fp32 [total_q, columns];
+    block_table, cu_q_lens, context_lens, max_q_len as for
+    ``kvq_chunk_attention_nvfp4``."""
+    fn = "kvq_score_blocks_indexer_k"
+    if kv_cache.element_size() != 1 or q_fp8.element_size() != 1:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if block_table.dtype is not torch.int32:
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    if q_fp8.dim() != 3 or kv_cache.dim() not in (2, 3):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    total, heads, D = q_fp8.shape
+    if block_size is None:
+        if kv_cache.dim() != 3:
+            raise KvqError(fn, KVQ_ERR_SHAPE)
+        block_size = kv_cache.size(1)
+    # (a block's bytes lie together)
+    held = kv_cache.size(1) * (kv_cache.size(2) if kv_cache.dim() == 3 else 1)
+    if (kv_cache.stride(-1) != 1 or held < block_size * (D + 4)
+            or (kv_cache.dim() == 3
+                and kv_cache.stride(1) != kv_cache.size(2))):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    w_stride = _rows_of(fn, weights, torch.float32, total)
+    s_stride = _rows_of(fn, scores, torch.float32, total)
+    _vector(fn, torch.int32, cu_q_lens, context_lens)
+    n = context_lens.numel()
+    if (q_fp8.stride(2) != 1 or q_fp8.stride(1) != D
+            or weights.size(1) != heads or cu_q_lens.numel() != n + 1
+            or block_table.dim() != 2 or block_table.size(0) < n
+            or (block_table.numel() > 1 and block_table.size(1) > 1
+                and block_table.stride(1) != 1)):
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _dev_error_ok(fn, dev_error)
+    here = _here(fn, q_fp8, weights, kv_cache, block_table, cu_q_lens,
+                 context_lens, scores, dev_error)
+    st = lib().kvq_score_blocks_indexer_k(
+        q_fp8.data_ptr(), q_fp8.stride(0) if total > 1 else heads * D,
+        weights.data_ptr(), w_stride, total, n, cu_q_lens.data_ptr(),
+        int(max_q_len), heads, D, kv_cache.data_ptr(),
+        kv_cache.stride(0) if kv_cache.size(0) > 1 else held,
+        kv_cache.size(0), int(block_size), block_table.data_ptr(),
+        block_table.stride(0) if n > 1 else block_table.size(1),
+        block_table.size(1), context_lens.data_ptr(), int(select_block),
+        scores.data_ptr(), s_stride, scores.size(1), int(flags),
+        _ptr(dev_error), here if stream is None else stream)
+    _check(fn, st)
+
+
+def kvq_select_blocks(scores: torch.Tensor, cu_q_lens: torch.Tensor,
+                      context_lens: torch.Tensor, selected: torch.Tensor,
+                      select_block: int, num_first: int = 0,
+                      num_last: int = 0, flags: int = 0,
+                      dev_error: torch.Tensor | None = None,
+                      stream: int | None = None) -> None:
+    """The blocks that each query row attends to (see ``include/kvq.h``): of
+    scores fp32 [total_q, columns] into selected int32 [total_q,
+    max_selected], rising, then -1; the first num_first and the last num_last
+    blocks always."""
+    fn = "kvq_select_blocks"
+    if scores.dim() != 2:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    total = scores.size(0)
+    s_stride = _rows_of(fn, scores, torch.float32, total)
+    l_stride = _rows_of(fn, selected, torch.int32, total)
+    _vector(fn, torch.int32, cu_q_lens, context_lens)
+    n = context_lens.numel()
+    if cu_q_lens.numel() != n + 1:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    _dev_error_ok(fn, dev_error)
+    here = _here(fn, scores, cu_q_lens, context_lens, selected, dev_error)
+    st = lib().kvq_select_blocks(
+        scores.data_ptr(), s_stride, scores.size(1), total, n,
+        cu_q_lens.data_ptr(), context_lens.data_ptr(), int(select_block),
+        int(num_first), int(num_last), selected.data_ptr(), l_stride,
+        selected.size(1), int(flags), _ptr(dev_error),
+        here if stream is None else stream)
+    _check(fn, st)
+
+
+def sparse_attention_workspace(query: torch.Tensor, selected: torch.Tensor,
+                               key_cache: torch.Tensor,
+                               block_table: torch.Tensor,
+                               select_block: int) -> torch.Tensor:
+    """Workspace of kvq_sparse_attention_nvfp4 for calls with these sizes
+    (calls that may overlap each need their own)."""
+    with torch.cuda.device(query.device):
+        n = lib().kvq_sparse_attention_workspace_bytes(
+            query.size(0), block_table.size(0), query.size(1),
+            key_cache.size(2), selected.size(1), int(select_block),
+            key_cache.size(1), block_table.size(1))
+    if n < 0:
+        raise KvqError("sparse_attention_workspace", KVQ_ERR_SHAPE)
+    return torch.empty(n, dtype=torch.uint8, device=query.device)
+
+
+def kvq_sparse_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor,
+                               block_table: torch.Tensor,
+                               cu_q_lens: torch.Tensor,
+                               context_lens: torch.Tensor,
+                               selected: torch.Tensor, select_block: int,
+                               k_scale: torch.Tensor, v_scale: torch.Tensor,
+                               scale: float, out: torch.Tensor,
+                               max_q_len: int,
+                               workspace: torch.Tensor | None = None,
+                               max_context_len: int = 0, flags: int = 0,
+                               dev_error: torch.Tensor | None = None,
+                               stream: int | None = None) -> None:
+    """Attention of each query row over the blocks of select_block tokens
+    that selected int32 [total_q, max_selected] lists for it (see
+    ``include/kvq.h``; rising, negative entries skipped:
+    ``kvq_select_blocks``).  Everything else as for
+    ``kvq_chunk_attention_nvfp4``; the workspace
+    (``sparse_attention_workspace``) is allocated here when it is not
+    given."""
+    fn = "kvq_sparse_attention_nvfp4"
+    stride = _rows_of(fn, selected, torch.int32, query.size(0))
+    _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
+            context_lens, (selected,),
+            (selected.data_ptr(), stride, selected.size(1),
+             int(select_block)), k_scale, v_scale, scale, out, max_q_len,
+            workspace, lambda: sparse_attention_workspace(
+                query, selected, key_cache, block_table, select_block),
+            max_context_len, flags, dev_error, stream)
 
 
 def alloc_page_pool(num_blocks: int, num_rows: int, max_blocks_per_seq: int,
