@@ -1,102 +1,632 @@
 // score_blocks.cu -- the indexer's score of every block of the context for
 // every query row, over the paged e4m3 cache, sm_103a.
 //
-// For a query row and a token t that it sees, s_t = scale_t * sum over heads
-// of w_h relu(q_h . k_t); a block's score is the largest of its tokens'.
+// For a query row and a token t that it sees, s_t = c_t * sum over heads of
+// w_h max(0, q_h . k_t); a block's score is the largest of its tokens'.
+//
+// The dot products of a tile of 128 tokens with the heads of some rows are
+// one tcgen05 product X = K Q^T (e4m3, M = 128 tokens, N = rows x heads, up
+// to 256): a token is a lane of tensor memory, so that the sum over the heads
+// stays in a thread, and the token's scale is multiplied once.  One CTA per
+// SM:
+//   * Loaders (4 warps) copy a tile's rows out of the pages into the
+//     operands' 128-byte swizzle, a few tiles ahead (cp.async: pages of any
+//     size), with the scales, and the queries and weights of a new row tile.
+//   * One warp issues the products, into two accumulators of 256 columns.
+//   * Two warpgroups take turns: each reads an accumulator, one token per
+//     thread, adds up w_h max(0, x_h) for each row in packed fp32, and takes
+//     the largest token of each block over the lanes.
+// Rows of one sequence share a tile: up to 512 columns for longer chunks, so
+// that a tile is read once for 8 rows of 64 heads.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kvq.h"
 #include "kvq_device.cuh"
 #include "kvq_internal.h"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
 
-constexpr int kThreads = 128;  // tokens of a thread block
+using namespace dev;
 
-__device__ __forceinline__ float2 widen(uint32_t pair) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;"
-      : "=r"(h)
-      : "h"(static_cast<uint16_t>(pair)));
-  float2 f;
-  asm("{ .reg .f16 a, b;\n"
-      "  mov.b32 {a, b}, %2;\n"
-      "  cvt.f32.f16 %0, a;\n"
-      "  cvt.f32.f16 %1, b; }"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
+constexpr int kTokens = 128;            // of a tile
+constexpr int kTile = kTokens * 128;    // bytes of its rows, 128 apart
+constexpr int kColumns = 256;           // of an accumulator
+constexpr int kEpiWarps = 8;            // two warpgroups, one accumulator each
+constexpr int kLoadWarps = 4;
+constexpr int kThreads = 32 * (kEpiWarps + kLoadWarps + 1);
+constexpr int kMaxRows = kColumns / 16;  // of an accumulator
+
+// Test builds only: in every other thread block an epilogue warp gives up at
+// its third tile as if its wait there had run out (0 in the library).
+#ifndef KVQ_TEST_SCORE_GIVE_UP
+#define KVQ_TEST_SCORE_GIVE_UP 0
+#endif
+
+// kTiles: accumulators that share a tile of tokens (1, or 2 for longer
+// chunks, with queries of twice the size in shared memory).
+template <int kTiles>
+struct Smem {
+  static constexpr int kStages = kTiles == 1 ? 8 : 5;
+  // tiles that are issued but not announced: what is in flight; the rest of
+  // the stages are being multiplied or wait for it
+  static constexpr int kAhead = kTiles == 1 ? 5 : 2;
+  static constexpr int kQueries = kTiles * kColumns * 128;
+  static constexpr int kQ = 0;  // two row tiles, in turn
+  static constexpr int kK = kQ + 2 * kQueries;
+  static constexpr int kWeights = kK + kStages * kTile;
+  static constexpr int kScales = kWeights + 2 * kTiles * kColumns * 4;
+  static constexpr int kBest = kScales + kStages * kTokens * 4;
+  static constexpr int kBar = kBest + 2 * 2 * 4 * kMaxRows * 4;
+  // [stage] filled, [stage] read, [accumulator] written, [accumulator] read,
+  // [row tile & 1] begun, [row tile & 1] read, [warpgroup] the warps' maxima
+  // are there, the last
+  static constexpr int kFull = 0, kEmpty = kStages, kDone = 2 * kStages,
+                       kFree = kDone + 2, kBegun = kFree + 2,
+                       kRead = kBegun + 2, kJoined = kRead + 2,
+                       kLast = kJoined + 2;
+  static constexpr int kMisc = kBar + (kLast + 1) * 8;  // abort, tmem address
+  static constexpr int kScan = (kMisc + 16 + 7) / 8 * 8;
+  static constexpr int kStart = kScan + 32 * 8;  // total, place, sequence
+  static constexpr int kBytes = kStart + 32 + 1024;
+  static_assert(kBytes <= 227 * 1024, "");
+};
+
+// kind::f8f6f4, e4m3 operands, fp32 accumulator, M = 128, K-major; N to add.
+constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
+  return ((addr >> 4) & 0x3FFFu) | (1u << 16);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{ .reg .pred p;\n"
+      "  .reg .b64 da, db;\n"
+      "  setp.ne.b32 p, %4, 0;\n"
+      "  mov.b64 da, {%1, %5};\n"
+      "  mov.b64 db, {%2, %5};\n"
+      "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p; }" ::"r"(
+          d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+      : "memory");
 }
 
-// One query row and 128 tokens, a thread for each.
-__global__ void __launch_bounds__(kThreads)
-    score_kernel(const ScoreParams p) {
-  pdl_prologue();
-  __shared__ float q[128], best[kThreads];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x;
-  const dev::QueryRow r = dev::query_row(p.rows, static_cast<int>(row));
-  if (row == 0 && blockIdx.y == 0) dev::check_rows(p.rows, tid, kThreads);
-  if (r.seq < 0) return;
-  const int t = blockIdx.y * kThreads + tid;
-  const uint8_t* key = nullptr;
-  float scale = 0.0f;
-  if (t < r.seen) {
-    const int page = t / p.B, off = t - page * p.B;
-    const int32_t blk = __ldg(p.block_table + r.seq * p.bt_stride + page);
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (p.rows.dev_error != nullptr)
-        atomicOr(p.rows.dev_error, KVQ_DEVERR_BLOCK);
-    } else {
-      const uint8_t* base = p.cache + blk * p.block_stride;
-      key = base + off * p.D;
-      scale = *reinterpret_cast<const float*>(
-          base + static_cast<int64_t>(p.B) * p.D + 4 * off);
-    }
+// ---------------------------------------------------------------------------
+// The schedule
+// ---------------------------------------------------------------------------
+// An item is a row tile (R consecutive rows) of a sequence, and spans the
+// tiles of tokens that its last row sees (one at least, so that rows that see
+// nothing are written).  Its length is measured in tokens: kItem for its own,
+// and as many as its last row sees, were the row tile full.  Item i of a
+// sequence of n rows and L tokens so begins at i (kItem + max(L - n, 0)) + R
+// i (i + 1) / 2: sums in closed form.  The lengths of all items one after the
+// other are cut into equal shares, and a tile belongs to the share in which
+// its first token falls.  (Blocks of scores lie within a tile: nothing is to
+// be joined.)
+constexpr int kItem = 256;
+
+struct Seq {
+  int q0, n, L;
+};
+__device__ __forceinline__ Seq seq_of(const ScoreParams& p, int b) {
+  const int total = static_cast<int>(p.rows.total);
+  Seq s;
+  s.q0 = min(max(__ldg(p.rows.cu + b), 0), total);
+  s.n = min(max(__ldg(p.rows.cu + b + 1), s.q0), total) - s.q0;
+  s.L = min(max(__ldg(p.rows.lens + b), 0), p.rows.len_cap);
+  return s;
+}
+__device__ __forceinline__ int64_t begin_of(const Seq& s, int R, int64_t i) {
+  return i * (kItem + max(s.L - s.n, 0)) + R * (i * (i + 1) / 2);
+}
+__device__ __forceinline__ int items_of(const Seq& s, int R) {
+  return (s.n + R - 1) / R;
+}
+
+// A warp's place in its share: the tiles t0 .. t1 - 1 of item i of sequence
+// b; `at`: where the item begins.
+struct Walk {
+  int64_t at, u0, u1;
+  Seq s;
+  int b, i, items, W, t0, t1;
+
+  __device__ __forceinline__ void enter(int R) {
+    const int last = min((i + 1) * R, s.n);
+    W = max((s.L - s.n + last + kTokens - 1) / kTokens, 1);
+    const int64_t x0 = u0 - at - kItem, x1 = u1 - at - kItem;
+    t0 = x0 <= 0 ? 0
+                 : static_cast<int>(min((x0 + kTokens - 1) / kTokens,
+                                        static_cast<int64_t>(W)));
+    t1 = x1 <= 0 ? 0
+                 : static_cast<int>(min((x1 + kTokens - 1) / kTokens,
+                                        static_cast<int64_t>(W)));
   }
-  float sum = 0.0f;
-  for (int h = 0; h < p.heads; ++h) {
-    __syncthreads();
-    if (tid < p.D / 2) {
-      const uint16_t pair = *reinterpret_cast<const uint16_t*>(
-          p.q + row * p.q_stride0 + h * p.D + 2 * tid);
-      const float2 f = widen(pair);
-      q[2 * tid] = f.x;
-      q[2 * tid + 1] = f.y;
-    }
-    __syncthreads();
-    if (key == nullptr) continue;
-    float x = 0.0f;
-    for (int d = 0; d < p.D; d += 4) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(key + d);
-      const float2 a = widen(w & 0xFFFFu), b = widen(w >> 16);
-      x += a.x * q[d] + a.y * q[d + 1] + b.x * q[d + 2] + b.y * q[d + 3];
-    }
-    x = x < 0.0f ? 0.0f : x;  // (NaN stays)
-    sum += __ldg(p.weights + row * p.w_stride0 + h) * x;
+  // To the next item with a tile in the share (the first time: this one).
+  __device__ __forceinline__ bool next(const ScoreParams& p, int R,
+                                       bool first) {
+    do {
+      if (!first) {
+        at += kItem + max(s.L - s.n, 0) + static_cast<int64_t>(R) * (i + 1);
+        if (at >= u1) return false;
+        if (++i == items) {
+          do {
+            if (++b >= p.rows.num_seqs) return false;
+            s = seq_of(p, b);
+          } while (s.n == 0);
+          i = 0;
+          items = items_of(s, R);
+        }
+      }
+      first = false;
+      enter(R);
+    } while (t0 >= t1);
+    return true;
   }
-  sum *= scale;
-  best[tid] = key != nullptr && sum == sum ? sum : -INFINITY;
+};
+
+// w max(0, x) added up, two columns at a time.  (NaN stays NaN.)
+__device__ __forceinline__ float relu(uint32_t x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
+  return y;
+}
+__device__ __forceinline__ void add_columns(const uint32_t* x, uint32_t w,
+                                            uint64_t (&sum)[2]) {
+#pragma unroll
+  for (int k = 0; k < 16; k += 4) {
+    uint64_t a, b;
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                 : "=l"(a), "=l"(b)
+                 : "r"(w + 4 * k));
+    sum[0] = fma2(pack2(relu(x[k]), relu(x[k + 1])), a, sum[0]);
+    sum[1] = fma2(pack2(relu(x[k + 2]), relu(x[k + 3])), b, sum[1]);
+  }
+}
+
+template <int kTiles>
+__global__ void __launch_bounds__(kThreads, 1)
+    score_kernel(const __grid_constant__ ScoreParams p, int R, int Hp) {
+  using S = Smem<kTiles>;
+  extern __shared__ __align__(16) uint8_t raw_smem[];
+  uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+  const uint32_t base = smem_addr(smem);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* misc = reinterpret_cast<volatile int*>(smem + S::kMisc);
+  volatile int* abort = misc;
+  auto bar = [&](int i) { return base + S::kBar + 8 * i; };
+  const int per = R / kTiles;  // rows of an accumulator
+
+  if (warp == 0) {
+    asm volatile(
+        "tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+        ::"r"(base + S::kMisc + 4)
+        : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 32) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(bar(S::kFull + s), kLoadWarps);
+      mbar_init(bar(S::kEmpty + s), 4 * kTiles);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(bar(S::kDone + a), 2);
+      mbar_init(bar(S::kFree + a), 4);
+      mbar_init(bar(S::kBegun + a), kLoadWarps);
+      mbar_init(bar(S::kRead + a), kEpiWarps);
+      mbar_init(bar(S::kJoined + a), 4);
+    }
+    mbar_init(bar(S::kLast), 1);
+    misc[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x == 0) check_rows(p.rows, tid, kThreads);
+
+  // --- this CTA's share -----------------------------------------------------
+  // (twice over the sequences: the total, then where the share begins)
+  Walk walk;
+  walk.u0 = walk.u1 = 0;
+  {
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + S::kScan);
+    volatile int64_t* start =
+        reinterpret_cast<volatile int64_t*>(smem + S::kStart);
+    const int rounds = (p.rows.num_seqs + kThreads - 1) / kThreads;
+    int64_t U = 0, length = 0, incl = 0;
+    if (tid == 0) start[1] = -1;
+#pragma unroll 1
+    for (int r = 0; r < (rounds > 1 ? 2 * rounds : 1); ++r) {
+      if (r == rounds) U = 0;
+      const int b = r % rounds * kThreads + tid;
+      length = 0;
+      if (b < p.rows.num_seqs) {
+        const Seq s = seq_of(p, b);
+        length = begin_of(s, R, items_of(s, R));
+      }
+      int64_t x = length;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+        if (lane >= d) x += y;
+      }
+      __syncthreads();
+      if (lane == 31) scan[warp] = x;
+      __syncthreads();
+      incl = U + x;
+#pragma unroll 1
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) incl += scan[w];
+        U += scan[w];
+      }
+      if (r == rounds - 1) {
+        // shares of a tile and a half at least
+        const int64_t n = max(
+            min(static_cast<int64_t>(gridDim.x), U / (kTokens + kTokens / 2)),
+            int64_t{1});
+        const int64_t cta = min(static_cast<int64_t>(blockIdx.x), n);
+        walk.u0 = U / n * cta + min(cta, U % n);
+        walk.u1 = min(cta + 1, n);
+        walk.u1 = U / n * walk.u1 + min(walk.u1, U % n);
+      }
+      if ((rounds > 1 && r < rounds) || length == 0) continue;
+      if (walk.u0 >= incl - length && walk.u0 < incl) {
+        start[0] = incl - length;
+        start[1] = b;
+      }
+    }
+    __syncthreads();
+    walk.b = static_cast<int>(start[1]);
+    walk.at = start[0];
+  }
+  bool any = walk.u0 < walk.u1 && walk.b >= 0;
+  if (any) {
+    walk.s = seq_of(p, walk.b);
+    walk.items = items_of(walk.s, R);
+    // the item in which the share begins: the largest i whose begin is not
+    // behind it
+    const int64_t off = walk.u0 - walk.at;
+    const double half = 0.5 * R, lin = kItem + max(walk.s.L - walk.s.n, 0) +
+                                       half;
+    int64_t i = static_cast<int64_t>(
+        (sqrt(lin * lin + 4.0 * half * static_cast<double>(off)) - lin) /
+        (2.0 * half));
+    i = min(max(i, int64_t{0}), static_cast<int64_t>(walk.items - 1));
+    while (i > 0 && begin_of(walk.s, R, i) > off) --i;
+    while (i + 1 < walk.items && begin_of(walk.s, R, i + 1) <= off) ++i;
+    walk.i = static_cast<int>(i);
+    walk.at += begin_of(walk.s, R, i);
+    any = walk.next(p, R, true);
+  }
+  fence_before();
   __syncthreads();
-  if (tid < kThreads / p.sel) {
-    float top = -INFINITY;
-    for (int i = 0; i < p.sel; ++i) top = fmaxf(top, best[tid * p.sel + i]);
-    const int column = blockIdx.y * (kThreads / p.sel) + tid;
-    if (column < p.columns) p.scores[row * p.scores_stride0 + column] = top;
+  fence_after();
+  const uint32_t tmem = static_cast<uint32_t>(misc[1]);
+  const int N = per * Hp;  // columns of an accumulator
+
+  if (any && warp < kEpiWarps) {
+    // --- scores ---------------------------------------------------------------
+    const int g = warp >> 2, part = warp & 3;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(part * 32) << 16) +
+                         g * kColumns;
+    float* best = reinterpret_cast<float*>(smem + S::kBest) +
+                  g * 2 * 4 * kMaxRows;
+    const int in_tile = kTokens / p.sel;
+    const float none = -INFINITY;
+    uint32_t cnt = 0, job = 0;  // tiles; jobs of this warpgroup
+    for (uint32_t seg = 0;; ++seg) {
+      // A warp that has no tile in a row tile would run ahead, and arrive
+      // twice for another's part in kRead: the loaders begin row tile seg
+      // only once all have read seg - 2.
+      if (!warp_wait(bar(S::kBegun + (seg & 1)), (seg >> 1) & 1, abort))
+        goto done;
+      const uint32_t weights = base + S::kWeights +
+                               (seg & 1) * kTiles * kColumns * 4 +
+                               (kTiles == 2 ? g : 0) * N * 4;
+      const int row0 = walk.i * R + (kTiles == 2 ? g * per : 0);
+      const int rows = min(per, walk.s.n - row0);  // (may be 0 or less)
+      float* out = p.scores + (walk.s.q0 + row0) * p.scores_stride0;
+      if (walk.t0 == 0) {  // columns behind the last tile
+        const int from = min(walk.W * in_tile, p.columns);
+        const int wide = p.columns - from;
+        if (kTiles == 2 || g == 0)
+          for (int r = part; r < rows; r += 4)
+            for (int c = lane; c < wide; c += 32)
+              out[r * p.scores_stride0 + from + c] = none;
+      }
+      for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
+        if (kTiles == 1 && (cnt & 1) != static_cast<uint32_t>(g)) continue;
+        if (!warp_wait(bar(S::kDone + g), job & 1, abort)) goto done;
+        fence_after();
+        if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 && job == 2 &&
+            part == 1) {
+          *abort = 1;
+          goto done;
+        }
+        const int stage = cnt % S::kStages;
+        const float scale = *reinterpret_cast<const float*>(
+            smem + S::kScales + (stage * kTokens + part * 32 + lane) * 4);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::kEmpty + stage));
+        // tokens of the tile that row 0 sees, and one more for each row
+        const int seen = walk.s.L - walk.s.n + row0 + 1 - t * kTokens;
+        float mine = none;  // lane r (and 16 + r): row r's
+        uint32_t x[2][16];
+        __syncwarp();
+        tmem_ld16(acc, x[0]);
+        tmem_wait_ld16(x[0]);
+        int col = 0;
+        for (int r = 0; r < rows; ++r) {
+          uint64_t sum[2] = {0, 0};
+          for (int c = 0; c < Hp; c += 32) {
+            if (col + 16 < N) tmem_ld16(acc + col + 16, x[1]);
+            add_columns(x[0], weights + 4 * col, sum);
+            tmem_wait_ld16(x[1]);
+            col += 16;
+            if (c + 16 < Hp) {
+              if (col + 16 < N) tmem_ld16(acc + col + 16, x[0]);
+              add_columns(x[1], weights + 4 * col, sum);
+              tmem_wait_ld16(x[0]);
+              col += 16;
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) x[0][k] = x[1][k];
+            }
+          }
+          float a, b;
+          unpack2(add2(sum[0], sum[1]), a, b);
+          float s = (a + b) * scale;
+          s = part * 32 + lane < seen + r && s == s ? s : none;
+          if (p.sel == 16) {
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1)
+              s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
+            if ((lane & 15) == r) mine = s;
+          } else {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+              s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
+            if (lane == r) mine = s;
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::kFree + g));
+        const int first = t * in_tile;
+        if (p.sel <= 32) {
+          const int r = lane & 15;
+          const int c = first + (p.sel == 16 ? 2 * part + (lane >> 4) : part);
+          if (r < rows && c < p.columns && (p.sel == 16 || lane < 16))
+            out[r * p.scores_stride0 + c] = mine;
+        } else {
+          // (a warp is at most one job ahead of another: two places in turn)
+          float* x_best = best + (job & 1) * 4 * kMaxRows;
+          if (lane < kMaxRows) x_best[part * kMaxRows + lane] = mine;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(S::kJoined + g));
+          if (!warp_wait(bar(S::kJoined + g), job & 1, abort)) goto done;
+          const int at = tid & 127, r = at & 15, c = at >> 4;
+          if (r < rows && c < in_tile && first + c < p.columns) {
+            const int n = 4 / in_tile;  // warps of a block
+            float s = none;
+            for (int w = 0; w < n; ++w)
+              s = fmaxf(s, x_best[(c * n + w) * kMaxRows + r]);
+            out[r * p.scores_stride0 + first + c] = s;
+          }
+        }
+        ++job;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::kRead + (seg & 1)));
+      if (!walk.next(p, R, false)) break;
+    }
+  } else if (any && warp < kEpiWarps + kLoadWarps) {
+    // --- copies ---------------------------------------------------------------
+    const int w = warp - kEpiWarps, here = 32 * w + lane;
+    const int chunk = lane & 7, chunks = p.D / 16;
+    uint32_t cnt = 0, told = 0;  // tiles issued, announced
+    auto announce = [&]() {
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(S::kFull + told % S::kStages));
+      ++told;
+    };
+    auto announce_all = [&]() {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      while (told < cnt) announce();
+    };
+    for (uint32_t seg = 0;; ++seg) {
+      const int buf = seg & 1;
+      if (seg >= 2) {
+        // (its tiles may be among those that are not announced yet)
+        const uint32_t parity = ((seg >> 1) - 1) & 1;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try(bar(S::kRead + buf), parity)))
+          announce_all();
+        if (!warp_wait(bar(S::kRead + buf), parity, abort)) goto done;
+      }
+      if (lane == 0) mbar_arrive(bar(S::kBegun + buf));
+      __syncwarp();
+      // the row tile's queries (heads behind the last one and rows behind the
+      // last are zeros) and weights
+      const int row0 = walk.i * R, rows = min(R, walk.s.n - row0);
+      const uint32_t q_to = base + S::kQ + buf * S::kQueries;
+      const uint32_t w_to = base + S::kWeights + buf * kTiles * kColumns * 4;
+      for (int c = here; c < R * Hp * 8; c += 32 * kLoadWarps) {
+        const int line = c >> 3, r = line / Hp, h = line - r * Hp;
+        if ((c & 7) >= chunks) continue;
+        const bool in = r < rows && h < p.heads;
+        const uint8_t* from =
+            in ? p.q + (walk.s.q0 + row0 + r) * p.q_stride0 + h * p.D +
+                     16 * (c & 7)
+               : p.q;
+        asm volatile(
+            "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                q_to + line * 128 + (((c & 7) ^ (line & 7)) << 4)),
+            "l"(from), "r"(in ? 16 : 0)
+            : "memory");
+      }
+      for (int c = here; c < R * Hp; c += 32 * kLoadWarps) {
+        const int r = c / Hp, h = c - r * Hp;
+        const bool in = r < rows && h < p.heads;
+        const float* from =
+            in ? p.weights + (walk.s.q0 + row0 + r) * p.w_stride0 + h
+               : p.weights;
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                         w_to + 4 * c),
+                     "l"(from), "r"(in ? 4 : 0)
+                     : "memory");
+      }
+      const int32_t* table = p.block_table + walk.b * p.bt_stride;
+      int off = 0;
+      // the page of this lane's token of tile t
+      auto look_up = [&](int t) {
+        const int pos = t * kTokens + here;
+        if (t >= walk.t1 || pos >= walk.s.L) return -1;
+        const int j = p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B;
+        off = pos - j * p.B;
+        return __ldg(table + j);
+      };
+      int32_t blk = look_up(walk.t0);
+      for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
+        const int stage = cnt % S::kStages;
+        if (cnt >= S::kStages &&
+            !warp_wait(bar(S::kEmpty + stage), (cnt / S::kStages - 1) & 1,
+                       abort))
+          goto done;
+        const bool seen = t * kTokens + here < walk.s.L;
+        const bool ok = seen && blk >= 0 && blk < p.num_blocks;
+        if (seen && !ok) flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
+        const uint8_t* page = p.cache + (ok ? blk * p.block_stride : 0);
+        const uint8_t* row = ok ? page + off * p.D : p.q;
+        const uint32_t s_to = base + S::kScales +
+                              (stage * kTokens + here) * 4;
+        if (ok)
+          asm volatile(
+              "cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_to),
+              "l"(page + static_cast<int64_t>(p.B) * p.D + 4 * off)
+              : "memory");
+        else  // (left out: NaN is)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s_to),
+                       "r"(0x7FFFFFFF)
+                       : "memory");
+        blk = look_up(t + 1);
+        const uint32_t to = base + S::kK + stage * kTile + 32 * w * 128;
+        const uint32_t oks = __ballot_sync(0xFFFFFFFFu, ok);
+        // eight lanes to a row: 128 bytes at a time
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3);
+          const uint8_t* from = reinterpret_cast<const uint8_t*>(__shfl_sync(
+              0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row), r));
+          const bool some = (oks >> r) & 1u;
+          if (chunk < chunks)
+            asm volatile(
+                "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                    to + r * 128 + ((chunk ^ (r & 7)) << 4)),
+                "l"(some ? from + 16 * chunk : from), "r"(some ? 16 : 0)
+                : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (cnt - told >= S::kAhead) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(S::kAhead) : "memory");
+          announce();
+        }
+      }
+      if (!walk.next(p, R, false)) break;
+    }
+    announce_all();
+  } else if (any) {
+    // --- products ---------------------------------------------------------------
+    const uint32_t idesc = kIdesc | (static_cast<uint32_t>(N >> 3) << 17);
+    uint32_t cnt = 0, job = 0;
+    for (uint32_t seg = 0;; ++seg) {
+      const uint32_t q = base + S::kQ + (seg & 1) * S::kQueries;
+      for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
+        const int stage = cnt % S::kStages;
+        if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort))
+          goto done;
+        for (int m = 0; m < kTiles; ++m, ++job) {
+          const int a = job & 1;
+          if (job >= 2 &&
+              !warp_wait(bar(S::kFree + a), ((job >> 1) - 1) & 1, abort))
+            goto done;
+          fence_after();
+          if (elect()) {
+            const uint32_t k = desc_lo(base + S::kK + stage * kTile);
+            const uint32_t qd = desc_lo(q + m * N * 128);
+            for (int x = 0; x < p.D / 32; ++x)
+              mma_f8(tmem + a * kColumns, k + 2 * x, qd + 2 * x, idesc, x > 0);
+            mma_commit(bar(S::kDone + a));
+            // (for what the loaders wrote by ordinary stores, too)
+            mbar_arrive(bar(S::kDone + a));
+          }
+          __syncwarp();
+        }
+      }
+      if (!walk.next(p, R, false)) break;
+    }
   }
+done:
+  __syncwarp();
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (*abort != 0) {  // (the same in every thread: all waits are over)
+    // products in flight end by themselves; wait for them before the tensor
+    // memory goes
+    if (warp == kEpiWarps + kLoadWarps) {
+      if (elect()) {
+        mma_commit(bar(S::kLast));
+        const uint64_t since = global_ns();
+        while (!mbar_try(bar(S::kLast), 0) &&
+               global_ns() - since < KVQ_WAIT_LIMIT_NS) {
+        }
+      }
+      __syncwarp();
+    }
+    if (tid == 0) flag(p.rows.dev_error, KVQ_DEVERR_TIMEOUT);
+    fence_before();
+    __syncthreads();
+    fence_after();
+  }
+  if (warp == 0)
+    asm volatile(
+        "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+template <int kTiles>
+cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
+  auto kernel = score_kernel<kTiles>;
+  cudaError_t err = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      Smem<kTiles>::kBytes);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Smem<kTiles>::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.pdl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, R, Hp);
 }
 
 }  // namespace
 
 cudaError_t launch_score_blocks(const ScoreParams& p, cudaStream_t stream) {
-  const unsigned tiles = static_cast<unsigned>(
-      (static_cast<int64_t>(p.columns) * p.sel + kThreads - 1) / kThreads);
-  return launch_kernel(score_kernel,
-                       dim3(static_cast<unsigned>(p.rows.total), tiles), kThreads,
-                       0, stream, p.pdl, p);
+  const int Hp = (p.heads + 15) / 16 * 16;
+  const int per = std::min(kColumns / Hp, std::max(p.max_q_len, 1));
+  return p.max_q_len > kColumns / Hp ? launch<2>(p, 2 * per, Hp, stream)
+                                     : launch<1>(p, per, Hp, stream);
 }
 
 }  // namespace kvq
