@@ -6,23 +6,27 @@
 //
 // The dot products of a tile of 128 tokens with the heads of some rows are
 // one tcgen05 product X = K Q^T (e4m3, M = 128 tokens, N = rows x heads, up
-// to 256): a token is a lane of tensor memory, so that the sum over the heads
+// to 128): a token is a lane of tensor memory, so that the sum over the heads
 // stays in a thread, and the token's scale is multiplied once.  One CTA per
 // SM:
-//   * Loaders (4 warps) copy a tile's rows out of the pages into the
-//     operands' 128-byte swizzle, a few tiles ahead (cp.async: pages of any
-//     size), with the scales, and the queries and weights of a new row tile.
-//   * One warp issues the products, into two accumulators of 256 columns.
-//   * Two warpgroups take turns: each reads an accumulator, one token per
-//     thread, adds up w_h max(0, x_h) for each row in packed fp32, and takes
-//     the largest token of each block over the lanes.
+//   * One warp has the pages' rows copied by TMA, a few tiles ahead, in boxes
+//     of as many rows as divide both a page and a tile (whole pages of up to
+//     128 tokens, mostly); two warps copy the scales, and the queries and
+//     weights of a new row tile.
+//   * One warp issues the products, into four accumulators of 128 columns in
+//     turn.
+//   * A warpgroup for each accumulator reads it, one token per thread, adds
+//     up w_h max(0, x_h) for each row in packed fp32, and takes the largest
+//     token of each block over the lanes.
 // Rows of one sequence share a tile: up to 512 columns for longer chunks, so
 // that a tile is read once for 8 rows of 64 heads.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "kvq.h"
 #include "kvq_device.cuh"
@@ -36,10 +40,13 @@ using namespace dev;
 
 constexpr int kTokens = 128;            // of a tile
 constexpr int kTile = kTokens * 128;    // bytes of its rows, 128 apart
-constexpr int kColumns = 256;           // of an accumulator
-constexpr int kEpiWarps = 8;            // two warpgroups, one accumulator each
-constexpr int kLoadWarps = 4;
-constexpr int kThreads = 32 * (kEpiWarps + kLoadWarps + 1);
+constexpr int kColumns = 128;           // of an accumulator
+constexpr int kAccs = 4;
+constexpr int kEpiWarps = 4 * kAccs;    // a warpgroup for each accumulator
+constexpr int kScaleWarps = 2;          // scales, queries, weights
+constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kMmaWarp = kTmaWarp + 1;
+// (20 warps: 96 registers each)
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxRows = kColumns / 16;  // of an accumulator
 
 // Test builds only: in every other thread block an epilogue warp gives up at
@@ -48,28 +55,27 @@ constexpr int kMaxRows = kColumns / 16;  // of an accumulator
 #define KVQ_TEST_SCORE_GIVE_UP 0
 #endif
 
-// kTiles: accumulators that share a tile of tokens (1, or 2 for longer
-// chunks, with queries of twice the size in shared memory).
+// kTiles: accumulators that share a tile of tokens (1, or 2 or 4 for longer
+// chunks, with queries of as many times the size in shared memory).
 template <int kTiles>
 struct Smem {
-  static constexpr int kStages = kTiles == 1 ? 8 : 5;
-  // tiles that are issued but not announced: what is in flight; the rest of
-  // the stages are being multiplied or wait for it
-  static constexpr int kAhead = kTiles == 1 ? 5 : 2;
+  static constexpr int kStages = kTiles == 4 ? 5 : 8;
   static constexpr int kQueries = kTiles * kColumns * 128;
   static constexpr int kQ = 0;  // two row tiles, in turn
   static constexpr int kK = kQ + 2 * kQueries;
   static constexpr int kWeights = kK + kStages * kTile;
   static constexpr int kScales = kWeights + 2 * kTiles * kColumns * 4;
   static constexpr int kBest = kScales + kStages * kTokens * 4;
-  static constexpr int kBar = kBest + 2 * 2 * 4 * kMaxRows * 4;
-  // [stage] filled, [stage] read, [accumulator] written, [accumulator] read,
-  // [row tile & 1] begun, [row tile & 1] read, [warpgroup] the warps' maxima
-  // are there, the last
-  static constexpr int kFull = 0, kEmpty = kStages, kDone = 2 * kStages,
-                       kFree = kDone + 2, kBegun = kFree + 2,
-                       kRead = kBegun + 2, kJoined = kRead + 2,
-                       kLast = kJoined + 2;
+  static constexpr int kBar = kBest + kAccs * 2 * 4 * kMaxRows * 4;
+  // [stage] its rows are there, [stage] its scales (and what came with them),
+  // [stage] read, [accumulator] written, [accumulator] read,
+  // [accumulator] its warps' maxima are there, [row tile & 1] begun, [row tile
+  // & 1] read, the last
+  static constexpr int kFull = 0, kScaled = kStages, kEmpty = 2 * kStages,
+                       kDone = 3 * kStages,
+                       kFree = kDone + kAccs, kJoined = kFree + kAccs,
+                       kBegun = kJoined + kAccs, kRead = kBegun + 2,
+                       kLast = kRead + 2;
   static constexpr int kMisc = kBar + (kLast + 1) * 8;  // abort, tmem address
   static constexpr int kScan = (kMisc + 16 + 7) / 8 * 8;
   static constexpr int kStart = kScan + 32 * 8;  // total, place, sequence
@@ -79,21 +85,28 @@ struct Smem {
 
 // kind::f8f6f4, e4m3 operands, fp32 accumulator, M = 128, K-major; N to add.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Shared-memory matrix descriptors, high word: rows of D bytes swizzled over
+// D bytes, 8 D from one group of 8 rows to the next.  (The tokens' rows; the
+// queries' are 128 bytes apart whatever D is.)
+__device__ __forceinline__ uint32_t desc_hi(int D) {
+  const uint32_t swizzle = D == 128 ? 2u : D == 64 ? 4u : 6u;
+  return (8u * D >> 4) | (1u << 14) | (swizzle << 29);
+}
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
   return ((addr >> 4) & 0x3FFFu) | (1u << 16);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b,
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t a_hi,
+                                       uint32_t b, uint32_t b_hi,
                                        uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{ .reg .pred p;\n"
       "  .reg .b64 da, db;\n"
       "  setp.ne.b32 p, %4, 0;\n"
       "  mov.b64 da, {%1, %5};\n"
-      "  mov.b64 db, {%2, %5};\n"
+      "  mov.b64 db, {%2, %6};\n"
       "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p; }" ::"r"(
           d),
-      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(a_hi), "r"(b_hi)
       : "memory");
 }
 
@@ -170,28 +183,84 @@ struct Walk {
   }
 };
 
-// w max(0, x) added up, two columns at a time.  (NaN stays NaN.)
+// max(0, x); NaN stays NaN.
 __device__ __forceinline__ float relu(uint32_t x) {
   float y;
   asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
   return y;
 }
-__device__ __forceinline__ void add_columns(const uint32_t* x, uint32_t w,
-                                            uint64_t (&sum)[2]) {
+
+// kWide columns of the accumulator at `acc`, and w max(0, x) of them added to
+// `sum`, two at a time; w in shared memory.  (The weights are loaded while
+// the columns are on their way: one after the other the two cost 10 %.)
+template <int kWide>
+__device__ __forceinline__ void add_columns(uint32_t acc, uint32_t weights,
+                                            uint64_t (&sum)[4]) {
+  uint32_t x[kWide];
+  uint64_t w[kWide / 2];
+  if constexpr (kWide == 32)
+    tmem_ld32(acc, x);
+  else
+    tmem_ld16(acc, x);
 #pragma unroll
-  for (int k = 0; k < 16; k += 4) {
-    uint64_t a, b;
+  for (int k = 0; k < kWide / 2; k += 2)
     asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
-                 : "=l"(a), "=l"(b)
-                 : "r"(w + 4 * k));
-    sum[0] = fma2(pack2(relu(x[k]), relu(x[k + 1])), a, sum[0]);
-    sum[1] = fma2(pack2(relu(x[k + 2]), relu(x[k + 3])), b, sum[1]);
+                 : "=l"(w[k]), "=l"(w[k + 1])
+                 : "r"(weights + 8 * k));
+  tmem_wait_ld16(x);
+  if constexpr (kWide == 32) tmem_wait_ld16(x + 16);
+#pragma unroll
+  for (int k = 0; k < kWide / 2; ++k)
+    sum[k & 3] =
+        fma2(pack2(relu(x[2 * k]), relu(x[2 * k + 1])), w[k], sum[k & 3]);
+}
+
+// The largest value over the warp's lanes (over each half's, for blocks of 16
+// tokens).  No value is NaN.
+__device__ __forceinline__ float largest(float s, bool halves) {
+  if (!halves) {
+    float m;
+    asm("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(m) : "f"(s));
+    return m;
   }
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1)
+    s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
+  return s;
+}
+
+// One accumulator: the score of this lane's token for each of `rows` rows of
+// Hp columns, and the largest over the lanes, lane r (and 16 + r) keeping row
+// r's.  seen: this lane's token is seen by rows r > -seen.
+template <int kWide>
+__device__ __forceinline__ float score_rows(uint32_t acc, uint32_t weights,
+                                            int rows, int Hp, float scale,
+                                            int seen, bool halves) {
+  const int lane = threadIdx.x & 31, key = halves ? lane & 15 : lane;
+  float mine = -INFINITY;
+#pragma unroll 1
+  for (int r = 0; r < rows; ++r) {
+    uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int c = 0; c < Hp; c += kWide) {
+      add_columns<kWide>(acc, weights, sum);
+      acc += kWide;
+      weights += 4 * kWide;
+    }
+    float a, b;
+    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    const float s = (a + b) * scale;
+    const float m = largest(seen + r > 0 && s == s ? s : -INFINITY, halves);
+    if (key == r) mine = m;
+  }
+  return mine;
 }
 
 template <int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
-    score_kernel(const __grid_constant__ ScoreParams p, int R, int Hp) {
+    score_kernel(const __grid_constant__ ScoreParams p,
+                 const __grid_constant__ CUtensorMap pages, int R, int Hp,
+                 int box) {
   using S = Smem<kTiles>;
   extern __shared__ __align__(16) uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -211,15 +280,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (tid == 32) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(bar(S::kFull + s), kLoadWarps);
+      mbar_init(bar(S::kFull + s), 1);
+      // (each thread's copies, and each warp's ordinary stores)
+      mbar_init(bar(S::kScaled + s), 33 * kScaleWarps);
       mbar_init(bar(S::kEmpty + s), 4 * kTiles);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kAccs; ++a) {
       mbar_init(bar(S::kDone + a), 2);
       mbar_init(bar(S::kFree + a), 4);
-      mbar_init(bar(S::kBegun + a), kLoadWarps);
-      mbar_init(bar(S::kRead + a), kEpiWarps);
       mbar_init(bar(S::kJoined + a), 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(S::kBegun + i), kScaleWarps);
+      mbar_init(bar(S::kRead + i), kEpiWarps);
     }
     mbar_init(bar(S::kLast), 1);
     misc[0] = 0;
@@ -308,10 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
   const int N = per * Hp;  // columns of an accumulator
+  uint32_t issued = 0;     // (the TMA warp: tiles)
 
   if (any && warp < kEpiWarps) {
     // --- scores ---------------------------------------------------------------
+    // accumulator g: columns m of the tiles `turn`, turn + kAccs / kTiles, ..
     const int g = warp >> 2, part = warp & 3;
+    const int m = g % kTiles, turn = g / kTiles;
     const uint32_t acc = tmem + (static_cast<uint32_t>(part * 32) << 16) +
                          g * kColumns;
     float* best = reinterpret_cast<float*>(smem + S::kBest) +
@@ -321,26 +397,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t cnt = 0, job = 0;  // tiles; jobs of this warpgroup
     for (uint32_t seg = 0;; ++seg) {
       // A warp that has no tile in a row tile would run ahead, and arrive
-      // twice for another's part in kRead: the loaders begin row tile seg
+      // twice for another's part in kRead: the copies begin row tile seg
       // only once all have read seg - 2.
       if (!warp_wait(bar(S::kBegun + (seg & 1)), (seg >> 1) & 1, abort))
         goto done;
       const uint32_t weights = base + S::kWeights +
-                               (seg & 1) * kTiles * kColumns * 4 +
-                               (kTiles == 2 ? g : 0) * N * 4;
-      const int row0 = walk.i * R + (kTiles == 2 ? g * per : 0);
+                               (seg & 1) * kTiles * kColumns * 4 + m * N * 4;
+      const int row0 = walk.i * R + m * per;
       const int rows = min(per, walk.s.n - row0);  // (may be 0 or less)
       float* out = p.scores + (walk.s.q0 + row0) * p.scores_stride0;
       if (walk.t0 == 0) {  // columns behind the last tile
         const int from = min(walk.W * in_tile, p.columns);
         const int wide = p.columns - from;
-        if (kTiles == 2 || g == 0)
+        if (turn == 0)
           for (int r = part; r < rows; r += 4)
             for (int c = lane; c < wide; c += 32)
               out[r * p.scores_stride0 + from + c] = none;
       }
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
-        if (kTiles == 1 && (cnt & 1) != static_cast<uint32_t>(g)) continue;
+        if (cnt % (kAccs / kTiles) != static_cast<uint32_t>(turn)) continue;
         if (!warp_wait(bar(S::kDone + g), job & 1, abort)) goto done;
         fence_after();
         if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 && job == 2 &&
@@ -353,47 +428,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             smem + S::kScales + (stage * kTokens + part * 32 + lane) * 4);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kEmpty + stage));
-        // tokens of the tile that row 0 sees, and one more for each row
+        // tokens of the tile that row 0 sees (one more for each row)
         const int seen = walk.s.L - walk.s.n + row0 + 1 - t * kTokens;
-        float mine = none;  // lane r (and 16 + r): row r's
-        uint32_t x[2][16];
         __syncwarp();
-        tmem_ld16(acc, x[0]);
-        tmem_wait_ld16(x[0]);
-        int col = 0;
-        for (int r = 0; r < rows; ++r) {
-          uint64_t sum[2] = {0, 0};
-          for (int c = 0; c < Hp; c += 32) {
-            if (col + 16 < N) tmem_ld16(acc + col + 16, x[1]);
-            add_columns(x[0], weights + 4 * col, sum);
-            tmem_wait_ld16(x[1]);
-            col += 16;
-            if (c + 16 < Hp) {
-              if (col + 16 < N) tmem_ld16(acc + col + 16, x[0]);
-              add_columns(x[1], weights + 4 * col, sum);
-              tmem_wait_ld16(x[0]);
-              col += 16;
-            } else {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) x[0][k] = x[1][k];
-            }
-          }
-          float a, b;
-          unpack2(add2(sum[0], sum[1]), a, b);
-          float s = (a + b) * scale;
-          s = part * 32 + lane < seen + r && s == s ? s : none;
-          if (p.sel == 16) {
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1)
-              s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
-            if ((lane & 15) == r) mine = s;
-          } else {
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-              s = fmaxf(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
-            if (lane == r) mine = s;
-          }
-        }
+        const float mine =
+            Hp % 32 == 0
+                ? score_rows<32>(acc, weights, rows, Hp, scale,
+                                 seen - part * 32 - lane, p.sel == 16)
+                : score_rows<16>(acc, weights, rows, Hp, scale,
+                                 seen - part * 32 - lane, p.sel == 16);
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kFree + g));
@@ -425,30 +468,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(S::kRead + (seg & 1)));
       if (!walk.next(p, R, false)) break;
     }
-  } else if (any && warp < kEpiWarps + kLoadWarps) {
-    // --- copies ---------------------------------------------------------------
-    const int w = warp - kEpiWarps, here = 32 * w + lane;
-    const int chunk = lane & 7, chunks = p.D / 16;
-    uint32_t cnt = 0, told = 0;  // tiles issued, announced
-    auto announce = [&]() {
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(S::kFull + told % S::kStages));
-      ++told;
-    };
-    auto announce_all = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      while (told < cnt) announce();
-    };
+  } else if (any && warp < kTmaWarp) {
+    // --- scales, queries, weights ---------------------------------------------
+    constexpr int kPer = kTokens / (32 * kScaleWarps);  // tokens of a thread
+    const int here = tid - 32 * kEpiWarps;
+    uint32_t cnt = 0;
     for (uint32_t seg = 0;; ++seg) {
       const int buf = seg & 1;
-      if (seg >= 2) {
-        // (its tiles may be among those that are not announced yet)
-        const uint32_t parity = ((seg >> 1) - 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_try(bar(S::kRead + buf), parity)))
-          announce_all();
-        if (!warp_wait(bar(S::kRead + buf), parity, abort)) goto done;
-      }
+      if (seg >= 2 &&
+          !warp_wait(bar(S::kRead + buf), ((seg >> 1) - 1) & 1, abort))
+        goto done;
       if (lane == 0) mbar_arrive(bar(S::kBegun + buf));
       __syncwarp();
       // the row tile's queries (heads behind the last one and rows behind the
@@ -456,9 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row0 = walk.i * R, rows = min(R, walk.s.n - row0);
       const uint32_t q_to = base + S::kQ + buf * S::kQueries;
       const uint32_t w_to = base + S::kWeights + buf * kTiles * kColumns * 4;
-      for (int c = here; c < R * Hp * 8; c += 32 * kLoadWarps) {
+      for (int c = here; c < R * Hp * 8; c += 32 * kScaleWarps) {
         const int line = c >> 3, r = line / Hp, h = line - r * Hp;
-        if ((c & 7) >= chunks) continue;
+        if ((c & 7) >= p.D / 16) continue;
         const bool in = r < rows && h < p.heads;
         const uint8_t* from =
             in ? p.q + (walk.s.q0 + row0 + r) * p.q_stride0 + h * p.D +
@@ -470,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             "l"(from), "r"(in ? 16 : 0)
             : "memory");
       }
-      for (int c = here; c < R * Hp; c += 32 * kLoadWarps) {
+      for (int c = here; c < R * Hp; c += 32 * kScaleWarps) {
         const int r = c / Hp, h = c - r * Hp;
         const bool in = r < rows && h < p.heads;
         const float* from =
@@ -482,85 +511,156 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
       }
       const int32_t* table = p.block_table + walk.b * p.bt_stride;
-      int off = 0;
-      // the page of this lane's token of tile t
+      // the pages of this thread's tokens of tile t
+      int32_t blk[kPer];
       auto look_up = [&](int t) {
-        const int pos = t * kTokens + here;
-        if (t >= walk.t1 || pos >= walk.s.L) return -1;
-        const int j = p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B;
-        off = pos - j * p.B;
-        return __ldg(table + j);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int pos = t * kTokens + i * 32 * kScaleWarps + here;
+          blk[i] = -1;
+          if (t < walk.t1 && pos < walk.s.L)
+            blk[i] = __ldg(table +
+                           (p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B));
+        }
       };
-      int32_t blk = look_up(walk.t0);
+      look_up(walk.t0);
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
         const int stage = cnt % S::kStages;
         if (cnt >= S::kStages &&
             !warp_wait(bar(S::kEmpty + stage), (cnt / S::kStages - 1) & 1,
                        abort))
           goto done;
-        const bool seen = t * kTokens + here < walk.s.L;
-        const bool ok = seen && blk >= 0 && blk < p.num_blocks;
-        if (seen && !ok) flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
-        const uint8_t* page = p.cache + (ok ? blk * p.block_stride : 0);
-        const uint8_t* row = ok ? page + off * p.D : p.q;
-        const uint32_t s_to = base + S::kScales +
-                              (stage * kTokens + here) * 4;
-        if (ok)
-          asm volatile(
-              "cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_to),
-              "l"(page + static_cast<int64_t>(p.B) * p.D + 4 * off)
-              : "memory");
-        else  // (left out: NaN is)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(s_to),
-                       "r"(0x7FFFFFFF)
-                       : "memory");
-        blk = look_up(t + 1);
-        const uint32_t to = base + S::kK + stage * kTile + 32 * w * 128;
-        const uint32_t oks = __ballot_sync(0xFFFFFFFFu, ok);
-        // eight lanes to a row: 128 bytes at a time
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3);
-          const uint8_t* from = reinterpret_cast<const uint8_t*>(__shfl_sync(
-              0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row), r));
-          const bool some = (oks >> r) & 1u;
-          if (chunk < chunks)
-            asm volatile(
-                "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                    to + r * 128 + ((chunk ^ (r & 7)) << 4)),
-                "l"(some ? from + 16 * chunk : from), "r"(some ? 16 : 0)
-                : "memory");
+        for (int i = 0; i < kPer; ++i) {
+          const int r = i * 32 * kScaleWarps + here, pos = t * kTokens + r;
+          const uint32_t to = base + S::kScales + (stage * kTokens + r) * 4;
+          if (blk[i] >= 0 && blk[i] < p.num_blocks) {
+            const int off = p.b_shift >= 0 ? pos & (p.B - 1) : pos % p.B;
+            const uint8_t* from = p.cache + blk[i] * p.block_stride +
+                                  static_cast<int64_t>(p.B) * p.D + 4 * off;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to),
+                         "l"(from)
+                         : "memory");
+          } else {  // (left out: NaN is)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0x7FFFFFFF)
+                         : "memory");
+            if (pos < walk.s.L) flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
+          }
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (cnt - told >= S::kAhead) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(S::kAhead) : "memory");
-          announce();
-        }
+        look_up(t + 1);
+        // (the barrier counts this thread's copies when they land)
+        asm volatile(
+            "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                bar(S::kScaled + stage))
+            : "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(S::kScaled + stage));
       }
       if (!walk.next(p, R, false)) break;
     }
-    announce_all();
+  } else if (any && warp == kTmaWarp) {
+    // --- the pages' rows --------------------------------------------------------
+    // A box for each lane (boxes of fewer than 4 rows: several, in turn); one
+    // whose page is not a page lies outside the tensor and becomes zeros.
+    // Boxes of fewer than 128 bytes (box == 0), which TMA cannot place, go by
+    // rows of 16-byte copies, a tile at a time.
+    const bool rows = box == 0;
+    if (rows) box = 1;
+    const int boxes = kTokens / box;
+    uint32_t& cnt = issued;
+    do {
+      const int32_t* table = p.block_table + walk.b * p.bt_stride;
+      auto look_up = [&](int t, int i) -> int32_t {
+        const int pos = t * kTokens + i * box;
+        return i < boxes && t < walk.t1 && pos < walk.s.L
+                   ? __ldg(table +
+                           (p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B))
+                   : -1;
+      };
+      int32_t blk = look_up(walk.t0, lane);
+      for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
+        const int stage = cnt % S::kStages;
+        if (cnt >= S::kStages &&
+            !warp_wait(bar(S::kEmpty + stage), (cnt / S::kStages - 1) & 1,
+                       abort))
+          goto done;
+        const uint32_t to = base + S::kK + stage * kTile;
+        const uint32_t full = bar(S::kFull + stage);
+        // (rows behind the context stay as they are: nobody sees them)
+        const int n = min(boxes, (max(walk.s.L - t * kTokens, 0) + box - 1) /
+                                     box);
+        if (rows) {
+          for (int i = lane; i < n; i += 32) {
+            if (i >= 32) blk = look_up(t, i);
+            const bool ok = blk >= 0 && blk < p.num_blocks;
+            const uint8_t* from = p.q;
+            if (ok)
+              from = p.cache + blk * p.block_stride +
+                     (t * kTokens + i) % p.B * p.D;
+            for (int c = 0; c < p.D; c += 16) {
+              const int at = i * p.D + c;
+              asm volatile(
+                  "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                      to + (at ^ (at >> 3 & (p.D - 16)))),
+                  "l"(ok ? from + c : from), "r"(ok ? 16 : 0)
+                  : "memory");
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(full);
+          blk = look_up(t + 1, lane);
+          continue;
+        }
+        if (lane == 0)
+          asm volatile(
+              "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0],"
+              " %1;" ::"r"(full),
+              "r"(n * box * p.D)
+              : "memory");
+        __syncwarp();
+        for (int i = lane; i < n; i += 32) {
+          if (i >= 32) blk = look_up(t, i);
+          const int pos = t * kTokens + i * box;
+          const int off = p.b_shift >= 0 ? pos & (p.B - 1) : pos % p.B;
+          asm volatile(
+              "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::"
+              "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                  to + i * box * p.D),
+              "l"(&pages), "r"(0), "r"(off),
+              "r"(blk >= 0 && blk < p.num_blocks ? blk : -1), "r"(full)
+              : "memory");
+        }
+        blk = look_up(t + 1, lane);
+      }
+    } while (walk.next(p, R, false));
   } else if (any) {
     // --- products ---------------------------------------------------------------
+    const uint32_t k_hi = desc_hi(p.D), q_hi = desc_hi(128);
     const uint32_t idesc = kIdesc | (static_cast<uint32_t>(N >> 3) << 17);
     uint32_t cnt = 0, job = 0;
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t q = base + S::kQ + (seg & 1) * S::kQueries;
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
         const int stage = cnt % S::kStages;
-        if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort))
+        if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort) ||
+            !warp_wait(bar(S::kScaled + stage), (cnt / S::kStages) & 1,
+                       abort))
           goto done;
+        fence_async_smem();  // (the queries' copies are ordinary writes)
         for (int m = 0; m < kTiles; ++m, ++job) {
-          const int a = job & 1;
-          if (job >= 2 &&
-              !warp_wait(bar(S::kFree + a), ((job >> 1) - 1) & 1, abort))
+          const int a = job % kAccs;
+          if (job >= kAccs &&
+              !warp_wait(bar(S::kFree + a), (job / kAccs - 1) & 1, abort))
             goto done;
           fence_after();
           if (elect()) {
             const uint32_t k = desc_lo(base + S::kK + stage * kTile);
             const uint32_t qd = desc_lo(q + m * N * 128);
             for (int x = 0; x < p.D / 32; ++x)
-              mma_f8(tmem + a * kColumns, k + 2 * x, qd + 2 * x, idesc, x > 0);
+              mma_f8(tmem + a * kColumns, k + 2 * x, k_hi, qd + 2 * x, q_hi,
+                     idesc, x > 0);
             mma_commit(bar(S::kDone + a));
             // (for what the loaders wrote by ordinary stores, too)
             mbar_arrive(bar(S::kDone + a));
@@ -578,9 +678,13 @@ done:
   __syncthreads();
   fence_after();
   if (*abort != 0) {  // (the same in every thread: all waits are over)
-    // products in flight end by themselves; wait for them before the tensor
-    // memory goes
-    if (warp == kEpiWarps + kLoadWarps) {
+    // copies and products in flight end by themselves; wait for them before
+    // the shared and the tensor memory go
+    if (warp == kTmaWarp && box > 0)
+      for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0;
+           k < issued; ++k)
+        mbar_wait(bar(S::kFull + k % S::kStages), k / S::kStages & 1);
+    if (warp == kMmaWarp) {
       if (elect()) {
         mma_commit(bar(S::kLast));
         const uint64_t since = global_ns();
@@ -600,12 +704,54 @@ done:
         "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
+// The pages as a tensor [num_blocks, B, D] of bytes, copied in boxes of `box`
+// rows of a page.
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+cudaError_t tensor_of_pages(const ScoreParams& p, int box, CUtensorMap* map) {
+  static const EncodeTiled encode = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                         cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t sizes[3] = {static_cast<cuuint64_t>(p.D),
+                               static_cast<cuuint64_t>(p.B),
+                               static_cast<cuuint64_t>(std::max<int64_t>(
+                                   std::min<int64_t>(p.num_blocks, INT32_MAX),
+                                   1))};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.D),
+                                 static_cast<cuuint64_t>(p.block_stride)};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(p.D),
+                               static_cast<cuuint32_t>(box), 1};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult got = encode(
+      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.cache),
+      sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      p.D == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+      : p.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                  : CU_TENSOR_MAP_SWIZZLE_32B,
+      CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return got == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int kTiles>
 cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
   auto kernel = score_kernel<kTiles>;
   cudaError_t err = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
       Smem<kTiles>::kBytes);
+  if (err != cudaSuccess) return err;
+  int box = std::gcd(p.B, kTokens);
+  CUtensorMap pages{};
+  if (box * p.D % 128 != 0)
+    box = 0;
+  else
+    err = tensor_of_pages(p, box, &pages);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
@@ -617,16 +763,17 @@ cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, R, Hp);
+  return cudaLaunchKernelEx(&cfg, kernel, p, pages, R, Hp, box);
 }
 
 }  // namespace
 
 cudaError_t launch_score_blocks(const ScoreParams& p, cudaStream_t stream) {
   const int Hp = (p.heads + 15) / 16 * 16;
-  const int per = std::min(kColumns / Hp, std::max(p.max_q_len, 1));
-  return p.max_q_len > kColumns / Hp ? launch<2>(p, 2 * per, Hp, stream)
-                                     : launch<1>(p, per, Hp, stream);
+  const int most = kColumns / Hp, q = std::max(p.max_q_len, 1);
+  if (q <= most) return launch<1>(p, q, Hp, stream);
+  if (q <= 2 * most) return launch<2>(p, 2 * most, Hp, stream);
+  return launch<4>(p, 4 * most, Hp, stream);
 }
 
 }  // namespace kvq

@@ -166,6 +166,15 @@ def test_score_block_sizes(block):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [32, 64])
+@pytest.mark.parametrize("block", [1, 2, 3, 4, 6, 20, 32, 200])
+def test_score_block_sizes_of_short_rows(block, D):
+    pad = -(block * (D + 4)) % 16
+    c = Scores([4, 2], [333, 129], D=D, block=block, sel=32, seed=block,
+               pad_block=pad)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("q_lens,lens", [
     ([0, 1, 0], [5, 9, 700]), ([7, 0, 3], [7, 0, 500]),
     ([130], [130]), ([300], [1000]), ([1] * 40, list(range(1, 1200, 30))),
