@@ -816,7 +816,7 @@ kvq_status kvq_score_blocks_indexer_k(
   if (q_stride0 < static_cast<int64_t>(num_heads) * head_dim ||
       weights_stride0 < num_heads ||
       block_stride < static_cast<int64_t>(block_size) * (head_dim + 4) ||
-      block_stride >= int64_t{1} << 40)
+      block_stride >= int64_t{1} << 40 || q_stride0 >= int64_t{1} << 40)
     return KVQ_ERR_SHAPE;
   if (total_q == 0 || num_seqs == 0 || num_columns == 0) return KVQ_OK;
   if (q_fp8 == nullptr || weights == nullptr || cu_q_lens == nullptr ||

@@ -5,19 +5,19 @@
 // w_h max(0, q_h . k_t); a block's score is the largest of its tokens'.
 //
 // The dot products of a tile of 128 tokens with the heads of some rows are
-// one tcgen05 product X = K Q^T (e4m3, M = 128 tokens, N = rows x heads, up
-// to 128): a token is a lane of tensor memory, so that the sum over the heads
-// stays in a thread, and the token's scale is multiplied once.  One CTA per
-// SM:
-//   * One warp has the pages' rows copied by TMA, a few tiles ahead, in boxes
-//     of as many rows as divide both a page and a tile (whole pages of up to
-//     128 tokens, mostly); two warps copy the scales, and the queries and
-//     weights of a new row tile.
-//   * One warp issues the products, into four accumulators of 128 columns in
-//     turn.
-//   * A warpgroup for each accumulator reads it, one token per thread, adds
-//     up w_h max(0, x_h) for each row in packed fp32, and takes the largest
-//     token of each block over the lanes.
+// one tcgen05 product X = K Q^T (e4m3, M = 128 tokens, N = rows x heads): a
+// token is a lane of tensor memory, so that the sum over the heads stays in a
+// thread, and the token's scale is multiplied once.  One CTA per SM:
+//   * One warp has the pages' rows and scales copied by TMA and bulk copies, a
+//     few tiles ahead, in boxes of as many rows as divide both a page and a
+//     tile (whole pages of up to 128 tokens, mostly).
+//   * Two warps take turns to issue the products (what one spends between
+//     two batches, 470 cycles of waits and commits, is hidden by the other's).
+//   * Four warpgroups read the accumulators, one token per thread, add up w_h
+//     max(0, x_h) for each row in packed fp32, and take the largest token over
+//     the lanes.
+//   * One warp has the queries and weights of the next row tile copied, joins
+//     the warps' largest tokens of each block, and writes the scores.
 // Rows of one sequence share a tile: up to 512 columns for longer chunks, so
 // that a tile is read once for 8 rows of 64 heads.
 #include <cuda.h>
@@ -40,14 +40,15 @@ using namespace dev;
 
 constexpr int kTokens = 128;            // of a tile
 constexpr int kTile = kTokens * 128;    // bytes of its rows, 128 apart
-constexpr int kColumns = 128;           // of an accumulator
-constexpr int kAccs = 4;
-constexpr int kEpiWarps = 4 * kAccs;    // a warpgroup for each accumulator
-constexpr int kScaleWarps = 2;          // scales, queries, weights
-constexpr int kTmaWarp = kEpiWarps + kScaleWarps, kMmaWarp = kTmaWarp + 1;
+constexpr int kColumns = 128;           // of a warpgroup's part of a product
+constexpr int kGroups = 4;              // warpgroups that read accumulators
+constexpr int kEpiWarps = 4 * kGroups;
+constexpr int kMmaWarps = 2;
+constexpr int kRowWarp = kEpiWarps, kTmaWarp = kRowWarp + 1,
+              kMmaWarp = kTmaWarp + 1;
 // (20 warps: 96 registers each)
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr int kMaxRows = kColumns / 16;  // of an accumulator
+constexpr int kThreads = 32 * (kMmaWarp + kMmaWarps);
+constexpr int kMaxRows = kColumns / 16;  // of a warpgroup
 
 // Test builds only: in every other thread block an epilogue warp gives up at
 // its third tile as if its wait there had run out (0 in the library).
@@ -55,10 +56,15 @@ constexpr int kMaxRows = kColumns / 16;  // of an accumulator
 #define KVQ_TEST_SCORE_GIVE_UP 0
 #endif
 
-// kTiles: accumulators that share a tile of tokens (1, or 2 or 4 for longer
-// chunks, with queries of as many times the size in shared memory).
+// kTiles: column tiles (a warpgroup's) that share a tile of tokens: 1, or 2 or
+// 4 for longer chunks, with queries of as many times the size in shared
+// memory.  One column tile is a product of its own, into one of four
+// accumulators; two are one product, into one of two.
 template <int kTiles>
 struct Smem {
+  static constexpr int kAccs = kTiles == 1 ? 4 : 2;
+  static constexpr int kShare = kGroups / kAccs;  // warpgroups of one
+  static constexpr int kJobs = kTiles / kShare > 0 ? kTiles / kShare : 1;
   static constexpr int kStages = kTiles == 4 ? 5 : 8;
   static constexpr int kQueries = kTiles * kColumns * 128;
   static constexpr int kQ = 0;  // two row tiles, in turn
@@ -66,16 +72,16 @@ struct Smem {
   static constexpr int kWeights = kK + kStages * kTile;
   static constexpr int kScales = kWeights + 2 * kTiles * kColumns * 4;
   static constexpr int kBest = kScales + kStages * kTokens * 4;
-  static constexpr int kBar = kBest + kAccs * 2 * 4 * kMaxRows * 4;
-  // [stage] its rows are there, [stage] its scales (and what came with them),
-  // [stage] read, [accumulator] written, [accumulator] read,
-  // [accumulator] its warps' maxima are there, [row tile & 1] begun, [row tile
-  // & 1] read, the last
-  static constexpr int kFull = 0, kScaled = kStages, kEmpty = 2 * kStages,
+  // (of a stage's tile: [warpgroup][half of the lanes][warp][row])
+  static constexpr int kBestTile = kGroups * 2 * 4 * kMaxRows;
+  static constexpr int kBar = kBest + kStages * kBestTile * 4;
+  // [stage] filled, [stage] its tile's maxima are there, [stage] empty,
+  // [accumulator] written, [accumulator] read, [row tile & 1] its queries are
+  // there, [row tile & 1] read, the last ones
+  static constexpr int kFull = 0, kScored = kStages, kEmpty = 2 * kStages,
                        kDone = 3 * kStages,
-                       kFree = kDone + kAccs, kJoined = kFree + kAccs,
-                       kBegun = kJoined + kAccs, kRead = kBegun + 2,
-                       kLast = kRead + 2;
+                       kFree = kDone + kAccs, kQuery = kFree + kAccs,
+                       kRead = kQuery + 2, kLast = kRead + 2;
   static constexpr int kMisc = kBar + (kLast + 1) * 8;  // abort, tmem address
   static constexpr int kScan = (kMisc + 16 + 7) / 8 * 8;
   static constexpr int kStart = kScan + 32 * 8;  // total, place, sequence
@@ -86,8 +92,7 @@ struct Smem {
 // kind::f8f6f4, e4m3 operands, fp32 accumulator, M = 128, K-major; N to add.
 constexpr uint32_t kIdesc = (1u << 4) | ((128u >> 4) << 24);
 // Shared-memory matrix descriptors, high word: rows of D bytes swizzled over
-// D bytes, 8 D from one group of 8 rows to the next.  (The tokens' rows; the
-// queries' are 128 bytes apart whatever D is.)
+// D bytes, 8 D from one group of 8 rows to the next.
 __device__ __forceinline__ uint32_t desc_hi(int D) {
   const uint32_t swizzle = D == 128 ? 2u : D == 64 ? 4u : 6u;
   return (8u * D >> 4) | (1u << 14) | (swizzle << 29);
@@ -95,18 +100,18 @@ __device__ __forceinline__ uint32_t desc_hi(int D) {
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) {
   return ((addr >> 4) & 0x3FFFu) | (1u << 16);
 }
-__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t a_hi,
-                                       uint32_t b, uint32_t b_hi,
-                                       uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma_f8(uint32_t d, uint32_t a, uint32_t b,
+                                       uint32_t hi, uint32_t idesc,
+                                       uint32_t acc) {
   asm volatile(
       "{ .reg .pred p;\n"
       "  .reg .b64 da, db;\n"
       "  setp.ne.b32 p, %4, 0;\n"
       "  mov.b64 da, {%1, %5};\n"
-      "  mov.b64 db, {%2, %6};\n"
+      "  mov.b64 db, {%2, %5};\n"
       "  tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p; }" ::"r"(
           d),
-      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(a_hi), "r"(b_hi)
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(hi)
       : "memory");
 }
 
@@ -259,8 +264,9 @@ __device__ __forceinline__ float score_rows(uint32_t acc, uint32_t weights,
 template <int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     score_kernel(const __grid_constant__ ScoreParams p,
-                 const __grid_constant__ CUtensorMap pages, int R, int Hp,
-                 int box) {
+                 const __grid_constant__ CUtensorMap pages,
+                 const __grid_constant__ CUtensorMap queries, int R, int Hp,
+                 int box_shift) {
   using S = Smem<kTiles>;
   extern __shared__ __align__(16) uint8_t raw_smem[];
   uint8_t* smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -269,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* misc = reinterpret_cast<volatile int*>(smem + S::kMisc);
   volatile int* abort = misc;
   auto bar = [&](int i) { return base + S::kBar + 8 * i; };
-  const int per = R / kTiles;  // rows of an accumulator
+  const int per = R / kTiles;  // rows of a warpgroup
 
   if (warp == 0) {
     asm volatile(
@@ -281,20 +287,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 32) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(bar(S::kFull + s), 1);
-      // (each thread's copies, and each warp's ordinary stores)
-      mbar_init(bar(S::kScaled + s), 33 * kScaleWarps);
-      mbar_init(bar(S::kEmpty + s), 4 * kTiles);
+      mbar_init(bar(S::kScored + s), 4 * kTiles);
+      mbar_init(bar(S::kEmpty + s), 1);
     }
-    for (int a = 0; a < kAccs; ++a) {
-      mbar_init(bar(S::kDone + a), 2);
-      mbar_init(bar(S::kFree + a), 4);
-      mbar_init(bar(S::kJoined + a), 4);
+    for (int a = 0; a < S::kAccs; ++a) {
+      mbar_init(bar(S::kDone + a), 1);
+      mbar_init(bar(S::kFree + a), 4 * S::kShare);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(S::kBegun + i), kScaleWarps);
-      mbar_init(bar(S::kRead + i), kEpiWarps);
+      // (the weights' copies by each lane, and the queries' bytes)
+      mbar_init(bar(S::kQuery + i), 33);
+      mbar_init(bar(S::kRead + i), kEpiWarps + kMmaWarps);
     }
-    mbar_init(bar(S::kLast), 1);
+    mbar_init(bar(S::kLast), kMmaWarps);
     misc[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -380,54 +385,47 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-  const int N = per * Hp;  // columns of an accumulator
-  uint32_t issued = 0;     // (the TMA warp: tiles)
+  const int N = per * Hp;  // columns of a warpgroup
+  uint32_t issued = 0, loads = 0;  // (the TMA warp's tiles; queries)
 
   if (any && warp < kEpiWarps) {
     // --- scores ---------------------------------------------------------------
-    // accumulator g: columns m of the tiles `turn`, turn + kAccs / kTiles, ..
+    // part h of accumulator a: column tile m of every turn-th tile
     const int g = warp >> 2, part = warp & 3;
-    const int m = g % kTiles, turn = g / kTiles;
+    const int a = g / S::kShare, h = g % S::kShare;
+    const int m = kTiles == 4 ? g : h;
+    constexpr int kTurns = S::kAccs / S::kJobs;
     const uint32_t acc = tmem + (static_cast<uint32_t>(part * 32) << 16) +
-                         g * kColumns;
+                         a * (512 / S::kAccs) + h * N;
     float* best = reinterpret_cast<float*>(smem + S::kBest) +
-                  g * 2 * 4 * kMaxRows;
-    const int in_tile = kTokens / p.sel;
-    const float none = -INFINITY;
+                  ((g * 2 + (lane >> 4)) * 4 + part) * kMaxRows + (lane & 15);
+    const bool keeps = (lane & 15) < kMaxRows && (lane < 16 || p.sel == 16);
     uint32_t cnt = 0, job = 0;  // tiles; jobs of this warpgroup
     for (uint32_t seg = 0;; ++seg) {
-      // A warp that has no tile in a row tile would run ahead, and arrive
-      // twice for another's part in kRead: the copies begin row tile seg
-      // only once all have read seg - 2.
-      if (!warp_wait(bar(S::kBegun + (seg & 1)), (seg >> 1) & 1, abort))
+      // (The queries of row tile seg come only once every warp that waits
+      // for them, whether it has a tile in seg - 2 or not, has said that it is
+      // through with that one: none runs ahead, and none misses a phase.)
+      if (!warp_wait(bar(S::kQuery + (seg & 1)), (seg >> 1) & 1, abort))
         goto done;
       const uint32_t weights = base + S::kWeights +
                                (seg & 1) * kTiles * kColumns * 4 + m * N * 4;
       const int row0 = walk.i * R + m * per;
       const int rows = min(per, walk.s.n - row0);  // (may be 0 or less)
-      float* out = p.scores + (walk.s.q0 + row0) * p.scores_stride0;
-      if (walk.t0 == 0) {  // columns behind the last tile
-        const int from = min(walk.W * in_tile, p.columns);
-        const int wide = p.columns - from;
-        if (turn == 0)
-          for (int r = part; r < rows; r += 4)
-            for (int c = lane; c < wide; c += 32)
-              out[r * p.scores_stride0 + from + c] = none;
-      }
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
-        if (cnt % (kAccs / kTiles) != static_cast<uint32_t>(turn)) continue;
-        if (!warp_wait(bar(S::kDone + g), job & 1, abort)) goto done;
+        if (kTurns > 1 && cnt % kTurns != static_cast<uint32_t>(a)) continue;
+        const int stage = cnt % S::kStages;
+        if (!warp_wait(bar(S::kDone + a), job & 1, abort)) goto done;
+        // (over as well: what orders the scales' copies before their reads)
+        if (!warp_wait(bar(S::kFull + stage), cnt / S::kStages & 1, abort))
+          goto done;
         fence_after();
         if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 && job == 2 &&
             part == 1) {
           *abort = 1;
           goto done;
         }
-        const int stage = cnt % S::kStages;
         const float scale = *reinterpret_cast<const float*>(
             smem + S::kScales + (stage * kTokens + part * 32 + lane) * 4);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S::kEmpty + stage));
         // tokens of the tile that row 0 sees (one more for each row)
         const int seen = walk.s.L - walk.s.n + row0 + 1 - t * kTokens;
         __syncwarp();
@@ -437,30 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  seen - part * 32 - lane, p.sel == 16)
                 : score_rows<16>(acc, weights, rows, Hp, scale,
                                  seen - part * 32 - lane, p.sel == 16);
+        if (keeps) best[stage * S::kBestTile] = mine;
         fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S::kFree + g));
-        const int first = t * in_tile;
-        if (p.sel <= 32) {
-          const int r = lane & 15;
-          const int c = first + (p.sel == 16 ? 2 * part + (lane >> 4) : part);
-          if (r < rows && c < p.columns && (p.sel == 16 || lane < 16))
-            out[r * p.scores_stride0 + c] = mine;
-        } else {
-          // (a warp is at most one job ahead of another: two places in turn)
-          float* x_best = best + (job & 1) * 4 * kMaxRows;
-          if (lane < kMaxRows) x_best[part * kMaxRows + lane] = mine;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(S::kJoined + g));
-          if (!warp_wait(bar(S::kJoined + g), job & 1, abort)) goto done;
-          const int at = tid & 127, r = at & 15, c = at >> 4;
-          if (r < rows && c < in_tile && first + c < p.columns) {
-            const int n = 4 / in_tile;  // warps of a block
-            float s = none;
-            for (int w = 0; w < n; ++w)
-              s = fmaxf(s, x_best[(c * n + w) * kMaxRows + r]);
-            out[r * p.scores_stride0 + first + c] = s;
-          }
+        if (lane == 0) {
+          mbar_arrive(bar(S::kFree + a));
+          mbar_arrive(bar(S::kScored + stage));
         }
         ++job;
       }
@@ -468,206 +448,260 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(S::kRead + (seg & 1)));
       if (!walk.next(p, R, false)) break;
     }
-  } else if (any && warp < kTmaWarp) {
-    // --- scales, queries, weights ---------------------------------------------
-    constexpr int kPer = kTokens / (32 * kScaleWarps);  // tokens of a thread
-    const int here = tid - 32 * kEpiWarps;
-    uint32_t cnt = 0;
-    for (uint32_t seg = 0;; ++seg) {
+  } else if (any && warp == kRowWarp) {
+    // --- queries, weights, scores -----------------------------------------------
+    Walk ahead = walk;  // the row tile whose queries come next
+    bool more = true;
+    auto load = [&](uint32_t seg) {
       const int buf = seg & 1;
       if (seg >= 2 &&
           !warp_wait(bar(S::kRead + buf), ((seg >> 1) - 1) & 1, abort))
-        goto done;
-      if (lane == 0) mbar_arrive(bar(S::kBegun + buf));
-      __syncwarp();
-      // the row tile's queries (heads behind the last one and rows behind the
-      // last are zeros) and weights
-      const int row0 = walk.i * R, rows = min(R, walk.s.n - row0);
+        return false;
+      const int row0 = ahead.i * R, rows = min(R, ahead.s.n - row0);
       const uint32_t q_to = base + S::kQ + buf * S::kQueries;
       const uint32_t w_to = base + S::kWeights + buf * kTiles * kColumns * 4;
-      for (int c = here; c < R * Hp * 8; c += 32 * kScaleWarps) {
-        const int line = c >> 3, r = line / Hp, h = line - r * Hp;
-        if ((c & 7) >= p.D / 16) continue;
-        const bool in = r < rows && h < p.heads;
-        const uint8_t* from =
-            in ? p.q + (walk.s.q0 + row0 + r) * p.q_stride0 + h * p.D +
-                     16 * (c & 7)
-               : p.q;
+      // (heads behind the last one are zeros, and so are their weights; rows
+      // behind the sequence's last are not used)
+      if (lane == 0)
         asm volatile(
-            "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                q_to + line * 128 + (((c & 7) ^ (line & 7)) << 4)),
-            "l"(from), "r"(in ? 16 : 0)
+            "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], "
+            "%1;" ::"r"(bar(S::kQuery + buf)),
+            "r"(rows * Hp * p.D)
             : "memory");
-      }
-      for (int c = here; c < R * Hp; c += 32 * kScaleWarps) {
-        const int r = c / Hp, h = c - r * Hp;
-        const bool in = r < rows && h < p.heads;
-        const float* from =
-            in ? p.weights + (walk.s.q0 + row0 + r) * p.w_stride0 + h
-               : p.weights;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                         w_to + 4 * c),
-                     "l"(from), "r"(in ? 4 : 0)
-                     : "memory");
-      }
-      const int32_t* table = p.block_table + walk.b * p.bt_stride;
-      // the pages of this thread's tokens of tile t
-      int32_t blk[kPer];
-      auto look_up = [&](int t) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int pos = t * kTokens + i * 32 * kScaleWarps + here;
-          blk[i] = -1;
-          if (t < walk.t1 && pos < walk.s.L)
-            blk[i] = __ldg(table +
-                           (p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B));
+      __syncwarp();
+      if (lane < rows)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::"
+            "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                q_to + lane * Hp * p.D),
+            "l"(&queries), "r"(0), "r"(0), "r"(ahead.s.q0 + row0 + lane),
+            "r"(bar(S::kQuery + buf))
+            : "memory");
+      __syncwarp();
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r) {
+        const float* w = p.weights + (ahead.s.q0 + row0 + r) * p.w_stride0;
+        for (int h = lane; h < Hp; h += 32) {
+          const bool in = h < p.heads;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           w_to + 4 * (r * Hp + h)),
+                       "l"(in ? w + h : p.weights), "r"(in ? 4 : 0)
+                       : "memory");
         }
-      };
-      look_up(walk.t0);
+      }
+      // (the barrier counts this thread's copies when they land)
+      asm volatile(
+          "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+              bar(S::kQuery + buf))
+          : "memory");
+      loads = seg + 1;
+      more = ahead.next(p, R, false);
+      return true;
+    };
+    if (!load(0)) goto done;
+    const int in_tile = kTokens / p.sel;
+    const int shift = 31 - __clz(in_tile);
+    uint32_t cnt = 0;
+    for (uint32_t seg = 0;; ++seg) {
+      if (more && !load(seg + 1)) goto done;
+      const int row0 = walk.i * R, rows = min(R, walk.s.n - row0);
+      float* out = p.scores + (walk.s.q0 + row0) * p.scores_stride0;
+      if (walk.t0 == 0) {  // columns behind the last tile
+        const int from = min(walk.W * in_tile, p.columns);
+        for (int r = 0; r < rows; ++r)
+          for (int c = from + lane; c < p.columns; c += 32)
+            out[r * p.scores_stride0 + c] = -INFINITY;
+      }
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
         const int stage = cnt % S::kStages;
-        if (cnt >= S::kStages &&
-            !warp_wait(bar(S::kEmpty + stage), (cnt / S::kStages - 1) & 1,
-                       abort))
+        const float* best = reinterpret_cast<const float*>(smem + S::kBest) +
+                            stage * S::kBestTile;
+        if (!warp_wait(bar(S::kScored + stage), cnt / S::kStages & 1, abort))
           goto done;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const int r = i * 32 * kScaleWarps + here, pos = t * kTokens + r;
-          const uint32_t to = base + S::kScales + (stage * kTokens + r) * 4;
-          if (blk[i] >= 0 && blk[i] < p.num_blocks) {
-            const int off = p.b_shift >= 0 ? pos & (p.B - 1) : pos % p.B;
-            const uint8_t* from = p.cache + blk[i] * p.block_stride +
-                                  static_cast<int64_t>(p.B) * p.D + 4 * off;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to),
-                         "l"(from)
-                         : "memory");
-          } else {  // (left out: NaN is)
-            asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(0x7FFFFFFF)
-                         : "memory");
-            if (pos < walk.s.L) flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
+#pragma unroll 1
+        for (int j = 0; j < S::kJobs; ++j) {
+          const int a = (cnt * S::kJobs + j) % S::kAccs;
+          // the product's rows, a block of each for a lane
+          const int first = j * S::kShare * per;
+          const int n = min(S::kShare * per, rows - first) << shift;
+          for (int i = lane; i < n; i += 32) {
+            const int row = i >> shift, c = i & (in_tile - 1);
+            const int h = row >= per;
+            const float* from = best + (a * S::kShare + h) * 8 * kMaxRows +
+                                row - h * per;
+            float s;
+            if (p.sel == 16) {  // half c % 2 of warp c / 2
+              s = from[((c & 1) * 4 + (c >> 1)) * kMaxRows];
+            } else {
+              from += c * (p.sel >> 5) * kMaxRows;
+              s = from[0];
+              if (p.sel >= 64) s = fmaxf(s, from[kMaxRows]);
+              if (p.sel >= 128)
+                s = fmaxf(s, fmaxf(from[2 * kMaxRows], from[3 * kMaxRows]));
+            }
+            if (t * in_tile + c < p.columns)
+              out[(first + row) * p.scores_stride0 + t * in_tile + c] = s;
           }
         }
-        look_up(t + 1);
-        // (the barrier counts this thread's copies when they land)
-        asm volatile(
-            "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                bar(S::kScaled + stage))
-            : "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(S::kScaled + stage));
+        if (lane == 0) mbar_arrive(bar(S::kEmpty + stage));
       }
       if (!walk.next(p, R, false)) break;
     }
   } else if (any && warp == kTmaWarp) {
-    // --- the pages' rows --------------------------------------------------------
-    // A box for each lane (boxes of fewer than 4 rows: several, in turn); one
-    // whose page is not a page lies outside the tensor and becomes zeros.
-    // Boxes of fewer than 128 bytes (box == 0), which TMA cannot place, go by
-    // rows of 16-byte copies, a tile at a time.
-    const bool rows = box == 0;
-    if (rows) box = 1;
-    const int boxes = kTokens / box;
-    uint32_t& cnt = issued;
+    // --- the pages' rows and scales ---------------------------------------------
+    // A box of 2^box_shift rows for each lane; the pages of as many tiles as
+    // there are lanes for are looked up at once.  Tokens whose page is not a
+    // page get NaN for their scale: they are left out.
+    const bool bulk = box_shift >= 0;
+    const int bits = bulk ? 7 - box_shift : 5;  // log2 of a tile's boxes
+    const int batch = 32 >> bits;               // tiles of a look-up
     do {
       const int32_t* table = p.block_table + walk.b * p.bt_stride;
-      auto look_up = [&](int t, int i) -> int32_t {
-        const int pos = t * kTokens + i * box;
-        return i < boxes && t < walk.t1 && pos < walk.s.L
-                   ? __ldg(table +
-                           (p.b_shift >= 0 ? pos >> p.b_shift : pos / p.B))
-                   : -1;
-      };
-      int32_t blk = look_up(walk.t0, lane);
-      for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
-        const int stage = cnt % S::kStages;
-        if (cnt >= S::kStages &&
-            !warp_wait(bar(S::kEmpty + stage), (cnt / S::kStages - 1) & 1,
-                       abort))
-          goto done;
+      // this lane's box of the batch: its page, place in it, its scales
+      int32_t blk = -1;
+      int off = 0;
+      const uint8_t* scales = nullptr;
+      uint32_t oks = 0, bads = 0;  // boxes that are pages, or should be
+#pragma unroll 1
+      for (int t = walk.t0; t < walk.t1; ++t, ++issued) {
+        const int stage = issued % S::kStages;
         const uint32_t to = base + S::kK + stage * kTile;
+        const uint32_t s_to = base + S::kScales + stage * kTokens * 4;
         const uint32_t full = bar(S::kFull + stage);
-        // (rows behind the context stay as they are: nobody sees them)
-        const int n = min(boxes, (max(walk.s.L - t * kTokens, 0) + box - 1) /
-                                     box);
-        if (rows) {
-          for (int i = lane; i < n; i += 32) {
-            if (i >= 32) blk = look_up(t, i);
-            const bool ok = blk >= 0 && blk < p.num_blocks;
-            const uint8_t* from = p.q;
-            if (ok)
-              from = p.cache + blk * p.block_stride +
-                     (t * kTokens + i) % p.B * p.D;
-            for (int c = 0; c < p.D; c += 16) {
-              const int at = i * p.D + c;
-              asm volatile(
-                  "cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                      to + (at ^ (at >> 3 & (p.D - 16)))),
-                  "l"(ok ? from + c : from), "r"(ok ? 16 : 0)
-                  : "memory");
-            }
+        const int turn = (t - walk.t0) & (batch - 1);
+        if (bulk && turn == 0) {
+          const int64_t pos = static_cast<int64_t>(t) * kTokens +
+                              (lane << box_shift);
+          const bool seen = pos < min(walk.s.L, walk.t1 * kTokens);
+          blk = -1;
+          if (seen) {
+            const int at = static_cast<int>(pos);
+            const int page = p.b_shift >= 0 ? at >> p.b_shift : at / p.B;
+            off = at - page * p.B;
+            blk = __ldg(table + page);
           }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_async_smem();
+          const bool ok = blk >= 0 && blk < p.num_blocks;
+          if (ok)
+            scales = p.cache + blk * p.block_stride +
+                     static_cast<int64_t>(p.B) * p.D + 4 * off;
+          oks = __ballot_sync(0xFFFFFFFFu, ok);
+          bads = __ballot_sync(0xFFFFFFFFu, seen && !ok);
+          if (bads != 0 && lane == 0)
+            flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
+        }
+        if (issued >= S::kStages &&
+            !warp_wait(bar(S::kEmpty + stage),
+                       (issued / S::kStages - 1) & 1, abort))
+          goto done;
+        if (bulk) {
+          const uint32_t its =
+              (bits == 5 ? ~0u : (1u << (1 << bits)) - 1u) << (turn << bits);
+          const int i = lane - (turn << bits);  // the box in the tile
+          if ((bads & its) != 0) {
+            if (bads & its & 1u << lane)
+              for (int k = 0; k < 1 << box_shift; ++k)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(
+                                 s_to + 4 * ((i << box_shift) + k)),
+                             "r"(0x7FFFFFFF)
+                             : "memory");
+            __syncwarp();
+          }
+          if (lane == 0)
+            asm volatile(
+                "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, "
+                "[%0], %1;" ::"r"(full),
+                "r"((__popc(oks & its) << box_shift) * (p.D + 4))
+                : "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(full);
-          blk = look_up(t + 1, lane);
+          if (oks & its & 1u << lane) {
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::"
+                "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                    to + (i << box_shift) * p.D),
+                "l"(&pages), "r"(0), "r"(off), "r"(blk), "r"(full)
+                : "memory");
+            asm volatile(
+                "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::"
+                "bytes [%0], [%1], %2, [%3];" ::"r"(
+                    s_to + 4 * (i << box_shift)),
+                "l"(scales), "r"(4 << box_shift), "r"(full)
+                : "memory");
+          }
+          __syncwarp();
           continue;
         }
-        if (lane == 0)
-          asm volatile(
-              "mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0],"
-              " %1;" ::"r"(full),
-              "r"(n * box * p.D)
-              : "memory");
-        __syncwarp();
-        for (int i = lane; i < n; i += 32) {
-          if (i >= 32) blk = look_up(t, i);
-          const int pos = t * kTokens + i * box;
-          const int off = p.b_shift >= 0 ? pos & (p.B - 1) : pos % p.B;
-          asm volatile(
-              "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::"
-              "complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-                  to + i * box * p.D),
-              "l"(&pages), "r"(0), "r"(off),
-              "r"(blk >= 0 && blk < p.num_blocks ? blk : -1), "r"(full)
-              : "memory");
+        // Boxes that the bulk copies cannot place: row by row, a tile at a
+        // time.
+        for (int i = lane; i < kTokens; i += 32) {
+          const int pos = t * kTokens + i;
+          if (pos >= walk.s.L) break;
+          blk = __ldg(table + pos / p.B);
+          const uint32_t s_at = s_to + 4 * i;
+          if (blk < 0 || blk >= p.num_blocks) {
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(s_at),
+                         "r"(0x7FFFFFFF)
+                         : "memory");
+            flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
+            continue;
+          }
+          const uint8_t* page = p.cache + blk * p.block_stride;
+          const int off = pos % p.B;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s_at),
+                       "l"(page + static_cast<int64_t>(p.B) * p.D + 4 * off)
+                       : "memory");
+          for (int c = 0; c < p.D; c += 16) {
+            const int at = i * p.D + c;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             to + (at ^ (at >> 3 & (p.D - 16)))),
+                         "l"(page + off * p.D + c)
+                         : "memory");
+          }
         }
-        blk = look_up(t + 1, lane);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
       }
     } while (walk.next(p, R, false));
   } else if (any) {
     // --- products ---------------------------------------------------------------
-    const uint32_t k_hi = desc_hi(p.D), q_hi = desc_hi(128);
-    const uint32_t idesc = kIdesc | (static_cast<uint32_t>(N >> 3) << 17);
+    const uint32_t hi = desc_hi(p.D);
+    const uint32_t idesc =
+        kIdesc | (static_cast<uint32_t>(S::kShare * N >> 3) << 17);
+    const uint32_t mine = warp - kMmaWarp;
     uint32_t cnt = 0, job = 0;
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t q = base + S::kQ + (seg & 1) * S::kQueries;
+      if (!warp_wait(bar(S::kQuery + (seg & 1)), (seg >> 1) & 1, abort))
+        goto done;
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
         const int stage = cnt % S::kStages;
-        if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort) ||
-            !warp_wait(bar(S::kScaled + stage), (cnt / S::kStages) & 1,
-                       abort))
-          goto done;
-        fence_async_smem();  // (the queries' copies are ordinary writes)
-        for (int m = 0; m < kTiles; ++m, ++job) {
-          const int a = job % kAccs;
-          if (job >= kAccs &&
-              !warp_wait(bar(S::kFree + a), (job / kAccs - 1) & 1, abort))
+#pragma unroll 1
+        for (int j = 0; j < S::kJobs; ++j, ++job) {
+          if (job % kMmaWarps != mine) continue;
+          // (a tile's stage is not filled again before its products are read:
+          // of the tiles that are not its own a warp need not see the phases)
+          if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort))
+            goto done;
+          const int a = job % S::kAccs;
+          if (job >= S::kAccs &&
+              !warp_wait(bar(S::kFree + a), (job / S::kAccs - 1) & 1, abort))
             goto done;
           fence_after();
           if (elect()) {
             const uint32_t k = desc_lo(base + S::kK + stage * kTile);
-            const uint32_t qd = desc_lo(q + m * N * 128);
+            const uint32_t qd = desc_lo(q + j * S::kShare * N * p.D);
             for (int x = 0; x < p.D / 32; ++x)
-              mma_f8(tmem + a * kColumns, k + 2 * x, k_hi, qd + 2 * x, q_hi,
+              mma_f8(tmem + a * (512 / S::kAccs), k + 2 * x, qd + 2 * x, hi,
                      idesc, x > 0);
             mma_commit(bar(S::kDone + a));
-            // (for what the loaders wrote by ordinary stores, too)
-            mbar_arrive(bar(S::kDone + a));
           }
           __syncwarp();
         }
       }
+      if (lane == 0) mbar_arrive(bar(S::kRead + (seg & 1)));
+      __syncwarp();
       if (!walk.next(p, R, false)) break;
     }
   }
@@ -680,11 +714,14 @@ done:
   if (*abort != 0) {  // (the same in every thread: all waits are over)
     // copies and products in flight end by themselves; wait for them before
     // the shared and the tensor memory go
-    if (warp == kTmaWarp && box > 0)
+    if (warp == kRowWarp)
+      for (uint32_t k = loads > 2 ? loads - 2 : 0; k < loads; ++k)
+        mbar_wait(bar(S::kQuery + (k & 1)), k >> 1 & 1);
+    if (warp == kTmaWarp && box_shift >= 0)
       for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0;
            k < issued; ++k)
         mbar_wait(bar(S::kFull + k % S::kStages), k / S::kStages & 1);
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp) {
       if (elect()) {
         mma_commit(bar(S::kLast));
         const uint64_t since = global_ns();
@@ -704,10 +741,11 @@ done:
         "tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
-// The pages as a tensor [num_blocks, B, D] of bytes, copied in boxes of `box`
-// rows of a page.
+// A tensor [outer, rows, D] of bytes, rows D and the outer ones `stride` apart,
+// copied in boxes of `box` rows; what lies outside is zeros.
 using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-cudaError_t tensor_of_pages(const ScoreParams& p, int box, CUtensorMap* map) {
+cudaError_t tensor_of(const uint8_t* at, int D, int64_t rows, int64_t outer,
+                      int64_t stride, int box, CUtensorMap* map) {
   static const EncodeTiled encode = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -719,22 +757,21 @@ cudaError_t tensor_of_pages(const ScoreParams& p, int box, CUtensorMap* map) {
     return reinterpret_cast<EncodeTiled>(f);
   }();
   if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t sizes[3] = {static_cast<cuuint64_t>(p.D),
-                               static_cast<cuuint64_t>(p.B),
-                               static_cast<cuuint64_t>(std::max<int64_t>(
-                                   std::min<int64_t>(p.num_blocks, INT32_MAX),
-                                   1))};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(p.D),
-                                 static_cast<cuuint64_t>(p.block_stride)};
-  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(p.D),
+  const cuuint64_t sizes[3] = {
+      static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows),
+      static_cast<cuuint64_t>(std::max<int64_t>(
+          std::min<int64_t>(outer, INT32_MAX), 1))};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D),
+                                 static_cast<cuuint64_t>(stride)};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(D),
                                static_cast<cuuint32_t>(box), 1};
   const cuuint32_t steps[3] = {1, 1, 1};
   const CUresult got = encode(
-      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(p.cache),
-      sizes, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-      p.D == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
-      : p.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                  : CU_TENSOR_MAP_SWIZZLE_32B,
+      map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(at), sizes,
+      strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      D == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+      : D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                : CU_TENSOR_MAP_SWIZZLE_32B,
       CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return got == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -746,13 +783,19 @@ cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
       Smem<kTiles>::kBytes);
   if (err != cudaSuccess) return err;
-  int box = std::gcd(p.B, kTokens);
-  CUtensorMap pages{};
-  if (box * p.D % 128 != 0)
-    box = 0;
-  else
-    err = tensor_of_pages(p, box, &pages);
+  // (a power of two; the copies' places and sizes are multiples of 128 and 16
+  // bytes)
+  const int box = std::gcd(p.B, kTokens);
+  int box_shift = -1;
+  CUtensorMap pages{}, queries;
+  err = tensor_of(p.q, p.D, p.heads, p.rows.total, p.q_stride0, Hp, &queries);
   if (err != cudaSuccess) return err;
+  if (box >= 4 && box * p.D % 128 == 0) {
+    for (box_shift = 2; 1 << box_shift < box;) ++box_shift;
+    err = tensor_of(p.cache, p.D, p.B, p.num_blocks, p.block_stride, box,
+                    &pages);
+    if (err != cudaSuccess) return err;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sm_count()));
   cfg.blockDim = dim3(kThreads);
@@ -763,7 +806,7 @@ cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.pdl ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, p, pages, R, Hp, box);
+  return cudaLaunchKernelEx(&cfg, kernel, p, pages, queries, R, Hp, box_shift);
 }
 
 }  // namespace
