@@ -12,7 +12,7 @@
 //     few tiles ahead, in boxes of as many rows as divide both a page and a
 //     tile (whole pages of up to 128 tokens, mostly).
 //   * Two warps take turns to issue the products (what one spends between
-//     two batches, 470 cycles of waits and commits, is hidden by the other's).
+//     two, 470 cycles of waits and commits, is hidden by the other's).
 //   * Four warpgroups read the accumulators, one token per thread, add up w_h
 //     max(0, x_h) for each row in packed fp32, and take the largest token over
 //     the lanes.
@@ -20,6 +20,15 @@
 //     the warps' largest tokens of each block, and writes the scores.
 // Rows of one sequence share a tile: up to 512 columns for longer chunks, so
 // that a tile is read once for 8 rows of 64 heads.
+//
+// Measured: 1024 rows of 64 heads over 24576 tokens (404 GFLOP) 285 us, 1.42
+// PFLOP/s; 77 rows of 48 sequences over 9001 to 33333 tokens (130 MB) 37 us,
+// 3.5 TB/s, 53 % of the measured copy rate.  The first is bound by the
+// warpgroups' arithmetic: 3.5 cycles for a column of 32 tokens on each quarter
+// of the SM with four warps at work (2 of them the maximum with 0, whose unit
+// takes a warp's in 2 cycles), against 256 cycles of products for 128 x 128 x
+// 128.  The second by the hand-overs of a tile between the roles, some 700
+// cycles, in which a tile's 16.9 KB would come in 735 at the copy rate.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -40,15 +49,12 @@ using namespace dev;
 
 constexpr int kTokens = 128;            // of a tile
 constexpr int kTile = kTokens * 128;    // bytes of its rows, 128 apart
-constexpr int kColumns = 128;           // of a warpgroup's part of a product
 constexpr int kGroups = 4;              // warpgroups that read accumulators
 constexpr int kEpiWarps = 4 * kGroups;
-constexpr int kMmaWarps = 2;
-constexpr int kRowWarp = kEpiWarps, kTmaWarp = kRowWarp + 1,
-              kMmaWarp = kTmaWarp + 1;
+constexpr int kRowWarp = kEpiWarps, kIssueWarp = kRowWarp + 1;
+constexpr int kIssueWarps = 3;          // of copies and of products
 // (20 warps: 96 registers each)
-constexpr int kThreads = 32 * (kMmaWarp + kMmaWarps);
-constexpr int kMaxRows = kColumns / 16;  // of a warpgroup
+constexpr int kThreads = 32 * (kIssueWarp + kIssueWarps);
 
 // Test builds only: in every other thread block an epilogue warp gives up at
 // its third tile as if its wait there had run out (0 in the library).
@@ -56,24 +62,34 @@ constexpr int kMaxRows = kColumns / 16;  // of a warpgroup
 #define KVQ_TEST_SCORE_GIVE_UP 0
 #endif
 
-// kTiles: column tiles (a warpgroup's) that share a tile of tokens: 1, or 2 or
-// 4 for longer chunks, with queries of as many times the size in shared
-// memory.  One column tile is a product of its own, into one of four
-// accumulators; two are one product, into one of two.
+// The rows that share a tile of tokens are cut into kTiles parts of equal
+// rows, one for a warpgroup each: kShare of them, side by side, are a product
+// and an accumulator, kJobs products a tile.
+//   1: single tokens and few heads; four accumulators of 128 columns.  Bound
+//      by the copies: two warps issue them.
+//   2, 4: two accumulators, half of each a warpgroup's.
+//   8: of heads up to 64; all four warpgroups read one accumulator while the
+//      other is written (1024 rows over 24576 tokens 291 us against 311 by 4).
+// More rows need as many times the queries in shared memory.
 template <int kTiles>
 struct Smem {
+  static constexpr int kShare = kTiles == 8 ? 4 : kTiles == 1 ? 1 : 2;
   static constexpr int kAccs = kTiles == 1 ? 4 : 2;
-  static constexpr int kShare = kGroups / kAccs;  // warpgroups of one
-  static constexpr int kJobs = kTiles / kShare > 0 ? kTiles / kShare : 1;
-  static constexpr int kStages = kTiles == 4 ? 5 : 8;
+  static constexpr int kJobs = kTiles / kShare;
+  static constexpr int kTmaWarps = kTiles == 1 ? 2 : 1;
+  static constexpr int kMmaWarps = kIssueWarps - kTmaWarps;
+  static constexpr int kMmaWarp = kIssueWarp + kTmaWarps;
+  static constexpr int kColumns = kTiles == 8 ? 64 : 128;  // of a part
+  static constexpr int kMaxRows = kColumns / 16;
+  static constexpr int kStages = kTiles >= 4 ? 5 : 8;
   static constexpr int kQueries = kTiles * kColumns * 128;
   static constexpr int kQ = 0;  // two row tiles, in turn
   static constexpr int kK = kQ + 2 * kQueries;
   static constexpr int kWeights = kK + kStages * kTile;
   static constexpr int kScales = kWeights + 2 * kTiles * kColumns * 4;
   static constexpr int kBest = kScales + kStages * kTokens * 4;
-  // (of a stage's tile: [warpgroup][half of the lanes][warp][row])
-  static constexpr int kBestTile = kGroups * 2 * 4 * kMaxRows;
+  // (of a stage's tile: [part][half of the lanes][warp][row])
+  static constexpr int kBestTile = kTiles * 2 * 4 * kMaxRows;
   static constexpr int kBar = kBest + kStages * kBestTile * 4;
   // [stage] filled, [stage] its tile's maxima are there, [stage] empty,
   // [accumulator] written, [accumulator] read, [row tile & 1] its queries are
@@ -275,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* misc = reinterpret_cast<volatile int*>(smem + S::kMisc);
   volatile int* abort = misc;
   auto bar = [&](int i) { return base + S::kBar + 8 * i; };
-  const int per = R / kTiles;  // rows of a warpgroup
+  const int per = R / kTiles;  // rows of a part
 
   if (warp == 0) {
     asm volatile(
@@ -297,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       // (the weights' copies by each lane, and the queries' bytes)
       mbar_init(bar(S::kQuery + i), 33);
-      mbar_init(bar(S::kRead + i), kEpiWarps + kMmaWarps);
+      mbar_init(bar(S::kRead + i), kEpiWarps + S::kMmaWarps);
     }
-    mbar_init(bar(S::kLast), kMmaWarps);
+    mbar_init(bar(S::kLast), S::kMmaWarps);
     misc[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -369,11 +385,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the item in which the share begins: the largest i whose begin is not
     // behind it
     const int64_t off = walk.u0 - walk.at;
-    const double half = 0.5 * R, lin = kItem + max(walk.s.L - walk.s.n, 0) +
-                                       half;
+    // (in fp32: fp64 arithmetic of all threads took 10 us here)
+    const float half = 0.5f * R, x = static_cast<float>(off);
+    const float lin = kItem + max(walk.s.L - walk.s.n, 0) + half;
     int64_t i = static_cast<int64_t>(
-        (sqrt(lin * lin + 4.0 * half * static_cast<double>(off)) - lin) /
-        (2.0 * half));
+        2.0f * x / (lin + sqrtf(lin * lin + 4.0f * half * x)));
     i = min(max(i, int64_t{0}), static_cast<int64_t>(walk.items - 1));
     while (i > 0 && begin_of(walk.s, R, i) > off) --i;
     while (i + 1 < walk.items && begin_of(walk.s, R, i + 1) <= off) ++i;
@@ -385,22 +401,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[1]);
-  const int N = per * Hp;  // columns of a warpgroup
+  const int N = per * Hp;  // columns of a part
   uint32_t issued = 0, loads = 0;  // (the TMA warp's tiles; queries)
 
   if (any && warp < kEpiWarps) {
     // --- scores ---------------------------------------------------------------
-    // part h of accumulator a: column tile m of every turn-th tile
     const int g = warp >> 2, part = warp & 3;
-    const int a = g / S::kShare, h = g % S::kShare;
-    const int m = kTiles == 4 ? g : h;
-    constexpr int kTurns = S::kAccs / S::kJobs;
-    const uint32_t acc = tmem + (static_cast<uint32_t>(part * 32) << 16) +
-                         a * (512 / S::kAccs) + h * N;
+    const int h = g % S::kShare;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(part * 32) << 16) +
+                           h * N;
     float* best = reinterpret_cast<float*>(smem + S::kBest) +
-                  ((g * 2 + (lane >> 4)) * 4 + part) * kMaxRows + (lane & 15);
-    const bool keeps = (lane & 15) < kMaxRows && (lane < 16 || p.sel == 16);
-    uint32_t cnt = 0, job = 0;  // tiles; jobs of this warpgroup
+                  ((lane >> 4) * 4 + part) * S::kMaxRows + (lane & 15);
+    const bool keeps = (lane & 15) < S::kMaxRows &&
+                       (lane < 16 || p.sel == 16);
+    uint32_t cnt = 0;  // tiles
+    [[maybe_unused]] uint32_t test = 0;  // (of test builds: jobs)
     for (uint32_t seg = 0;; ++seg) {
       // (The queries of row tile seg come only once every warp that waits
       // for them, whether it has a tile in seg - 2 or not, has said that it is
@@ -408,41 +423,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(bar(S::kQuery + (seg & 1)), (seg >> 1) & 1, abort))
         goto done;
       const uint32_t weights = base + S::kWeights +
-                               (seg & 1) * kTiles * kColumns * 4 + m * N * 4;
-      const int row0 = walk.i * R + m * per;
-      const int rows = min(per, walk.s.n - row0);  // (may be 0 or less)
+                               (seg & 1) * kTiles * S::kColumns * 4;
       for (int t = walk.t0; t < walk.t1; ++t, ++cnt) {
-        if (kTurns > 1 && cnt % kTurns != static_cast<uint32_t>(a)) continue;
         const int stage = cnt % S::kStages;
-        if (!warp_wait(bar(S::kDone + a), job & 1, abort)) goto done;
-        // (over as well: what orders the scales' copies before their reads)
-        if (!warp_wait(bar(S::kFull + stage), cnt / S::kStages & 1, abort))
-          goto done;
-        fence_after();
-        if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 && job == 2 &&
-            part == 1) {
-          *abort = 1;
-          goto done;
+#pragma unroll
+        for (int j = 0; j < S::kJobs; ++j) {
+          const uint32_t job = cnt * S::kJobs + j;
+          const int a = job % S::kAccs;
+          if (S::kShare < kGroups && a != g / S::kShare) continue;
+          if (!warp_wait(bar(S::kDone + a), job / S::kAccs & 1, abort))
+            goto done;
+          // (over as well: what orders the scales' copies before their reads)
+          if (!warp_wait(bar(S::kFull + stage), cnt / S::kStages & 1, abort))
+            goto done;
+          fence_after();
+          if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 &&
+              test++ == 2 && part == 1) {
+            *abort = 1;
+            goto done;
+          }
+          const float scale = *reinterpret_cast<const float*>(
+              smem + S::kScales + (stage * kTokens + part * 32 + lane) * 4);
+          const int m = j * S::kShare + h;
+          const int row0 = walk.i * R + m * per;
+          const int rows = min(per, walk.s.n - row0);  // (may be 0 or less)
+          // this lane's token is seen by rows from -seen on, counted from 1
+          const int seen = walk.s.L - walk.s.n + row0 + 1 - t * kTokens -
+                           part * 32 - lane;
+          const uint32_t acc = lanes + a * (512 / S::kAccs);
+          __syncwarp();
+          const float mine =
+              Hp % 32 == 0
+                  ? score_rows<32>(acc, weights + m * N * 4, rows, Hp, scale,
+                                   seen, p.sel == 16)
+                  : score_rows<16>(acc, weights + m * N * 4, rows, Hp, scale,
+                                   seen, p.sel == 16);
+          if (keeps)
+            best[stage * S::kBestTile + m * 8 * S::kMaxRows] = mine;
+          fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(S::kFree + a));
+            mbar_arrive(bar(S::kScored + stage));
+          }
         }
-        const float scale = *reinterpret_cast<const float*>(
-            smem + S::kScales + (stage * kTokens + part * 32 + lane) * 4);
-        // tokens of the tile that row 0 sees (one more for each row)
-        const int seen = walk.s.L - walk.s.n + row0 + 1 - t * kTokens;
-        __syncwarp();
-        const float mine =
-            Hp % 32 == 0
-                ? score_rows<32>(acc, weights, rows, Hp, scale,
-                                 seen - part * 32 - lane, p.sel == 16)
-                : score_rows<16>(acc, weights, rows, Hp, scale,
-                                 seen - part * 32 - lane, p.sel == 16);
-        if (keeps) best[stage * S::kBestTile] = mine;
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bar(S::kFree + a));
-          mbar_arrive(bar(S::kScored + stage));
-        }
-        ++job;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(S::kRead + (seg & 1)));
@@ -459,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       const int row0 = ahead.i * R, rows = min(R, ahead.s.n - row0);
       const uint32_t q_to = base + S::kQ + buf * S::kQueries;
-      const uint32_t w_to = base + S::kWeights + buf * kTiles * kColumns * 4;
+      const uint32_t w_to = base + S::kWeights + buf * kTiles * S::kColumns * 4;
       // (heads behind the last one are zeros, and so are their weights; rows
       // behind the sequence's last are not used)
       if (lane == 0)
@@ -518,41 +542,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                             stage * S::kBestTile;
         if (!warp_wait(bar(S::kScored + stage), cnt / S::kStages & 1, abort))
           goto done;
-#pragma unroll 1
-        for (int j = 0; j < S::kJobs; ++j) {
-          const int a = (cnt * S::kJobs + j) % S::kAccs;
-          // the product's rows, a block of each for a lane
-          const int first = j * S::kShare * per;
-          const int n = min(S::kShare * per, rows - first) << shift;
-          for (int i = lane; i < n; i += 32) {
-            const int row = i >> shift, c = i & (in_tile - 1);
-            const int h = row >= per;
-            const float* from = best + (a * S::kShare + h) * 8 * kMaxRows +
-                                row - h * per;
-            float s;
-            if (p.sel == 16) {  // half c % 2 of warp c / 2
-              s = from[((c & 1) * 4 + (c >> 1)) * kMaxRows];
-            } else {
-              from += c * (p.sel >> 5) * kMaxRows;
-              s = from[0];
-              if (p.sel >= 64) s = fmaxf(s, from[kMaxRows]);
-              if (p.sel >= 128)
-                s = fmaxf(s, fmaxf(from[2 * kMaxRows], from[3 * kMaxRows]));
-            }
-            if (t * in_tile + c < p.columns)
-              out[(first + row) * p.scores_stride0 + t * in_tile + c] = s;
+        // a block of a row for each lane
+        for (int i = lane; i < rows << shift; i += 32) {
+          const int row = i >> shift, c = i & (in_tile - 1), m = row / per;
+          const float* from = best + m * 8 * S::kMaxRows + row - m * per;
+          float s;
+          if (p.sel == 16) {  // half c % 2 of warp c / 2
+            s = from[((c & 1) * 4 + (c >> 1)) * S::kMaxRows];
+          } else {
+            from += c * (p.sel >> 5) * S::kMaxRows;
+            s = from[0];
+            if (p.sel >= 64) s = fmaxf(s, from[S::kMaxRows]);
+            if (p.sel >= 128)
+              s = fmaxf(s, fmaxf(from[2 * S::kMaxRows], from[3 * S::kMaxRows]));
           }
+          if (t * in_tile + c < p.columns)
+            out[row * p.scores_stride0 + t * in_tile + c] = s;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::kEmpty + stage));
       }
       if (!walk.next(p, R, false)) break;
     }
-  } else if (any && warp == kTmaWarp) {
+  } else if (any && warp < S::kMmaWarp) {
     // --- the pages' rows and scales ---------------------------------------------
     // A box of 2^box_shift rows for each lane; the pages of as many tiles as
     // there are lanes for are looked up at once.  Tokens whose page is not a
     // page get NaN for their scale: they are left out.
+    // (Two such warps take turns: a tile's copies take one 1300 cycles to
+    // issue.)
+    const uint32_t who = warp - kIssueWarp;
     const bool bulk = box_shift >= 0;
     const int bits = bulk ? 7 - box_shift : 5;  // log2 of a tile's boxes
     const int batch = 32 >> bits;               // tiles of a look-up
@@ -570,6 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_to = base + S::kScales + stage * kTokens * 4;
         const uint32_t full = bar(S::kFull + stage);
         const int turn = (t - walk.t0) & (batch - 1);
+        if (!bulk && issued % S::kTmaWarps != who) continue;
         if (bulk && turn == 0) {
           const int64_t pos = static_cast<int64_t>(t) * kTokens +
                               (lane << box_shift);
@@ -587,9 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                      static_cast<int64_t>(p.B) * p.D + 4 * off;
           oks = __ballot_sync(0xFFFFFFFFu, ok);
           bads = __ballot_sync(0xFFFFFFFFu, seen && !ok);
-          if (bads != 0 && lane == 0)
+          if (bads != 0 && lane == 0 && who == 0)
             flag(p.rows.dev_error, KVQ_DEVERR_BLOCK);
         }
+        if (issued % S::kTmaWarps != who) continue;
         if (issued >= S::kStages &&
             !warp_wait(bar(S::kEmpty + stage),
                        (issued / S::kStages - 1) & 1, abort))
@@ -669,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t hi = desc_hi(p.D);
     const uint32_t idesc =
         kIdesc | (static_cast<uint32_t>(S::kShare * N >> 3) << 17);
-    const uint32_t mine = warp - kMmaWarp;
+    const uint32_t mine = warp - S::kMmaWarp;
     uint32_t cnt = 0, job = 0;
     for (uint32_t seg = 0;; ++seg) {
       const uint32_t q = base + S::kQ + (seg & 1) * S::kQueries;
@@ -679,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int stage = cnt % S::kStages;
 #pragma unroll 1
         for (int j = 0; j < S::kJobs; ++j, ++job) {
-          if (job % kMmaWarps != mine) continue;
+          if (job % S::kMmaWarps != mine) continue;
           // (a tile's stage is not filled again before its products are read:
           // of the tiles that are not its own a warp need not see the phases)
           if (!warp_wait(bar(S::kFull + stage), (cnt / S::kStages) & 1, abort))
@@ -717,11 +738,11 @@ done:
     if (warp == kRowWarp)
       for (uint32_t k = loads > 2 ? loads - 2 : 0; k < loads; ++k)
         mbar_wait(bar(S::kQuery + (k & 1)), k >> 1 & 1);
-    if (warp == kTmaWarp && box_shift >= 0)
+    if (warp >= kIssueWarp && warp < S::kMmaWarp && box_shift >= 0)
       for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0;
            k < issued; ++k)
         mbar_wait(bar(S::kFull + k % S::kStages), k / S::kStages & 1);
-    if (warp >= kMmaWarp) {
+    if (warp >= S::kMmaWarp) {
       if (elect()) {
         mma_commit(bar(S::kLast));
         const uint64_t since = global_ns();
@@ -813,9 +834,10 @@ cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
 
 cudaError_t launch_score_blocks(const ScoreParams& p, cudaStream_t stream) {
   const int Hp = (p.heads + 15) / 16 * 16;
-  const int most = kColumns / Hp, q = std::max(p.max_q_len, 1);
+  const int most = 128 / Hp, q = std::max(p.max_q_len, 1);
   if (q <= most) return launch<1>(p, q, Hp, stream);
   if (q <= 2 * most) return launch<2>(p, 2 * most, Hp, stream);
+  if (Hp <= 64) return launch<8>(p, 8 * (64 / Hp), Hp, stream);
   return launch<4>(p, 4 * most, Hp, stream);
 }
 
