@@ -310,6 +310,15 @@ __device__ __forceinline__ void rescale(uint32_t col, float f) {
 // again).  So the end of a share within kSnap units of an item's end moves
 // there.
 constexpr int kRows = 256;
+// What a row sees: the tokens up to its own; those before the drafts and the
+// drafts of its mask; those of the blocks that its list selects.
+constexpr int kCausal = 0, kTree = 1, kListed = 2;
+
+// Rows of a full item.
+template <int kMode>
+__device__ __forceinline__ int item_rows(const ChunkParams& p) {
+  return kMode == kListed ? p.item_tokens * p.G : kRows;
+}
 constexpr int kItemUnits = 3;
 constexpr int kSnap = 2;
 
@@ -338,7 +347,7 @@ __device__ __forceinline__ Seq seq_of(const ChunkParams& p, int b) {
 // floor((row + G (L - n + 128)) / (128 G)) tiles.  From block to block the
 // row grows by 256, and the quotient is carried along.  (Rows are below 2^29,
 // contexts at most 2^26 tokens, groups at most 16: 32 bits.)
-template <bool kTree>
+template <int kMode>
 struct Blocks {
   int left;   // rows from this block on
   int step;   // 128 G
@@ -349,7 +358,7 @@ struct Blocks {
                                         int i) {
     step = 128 * p.G;
     left = s.n * p.G - i * kRows;
-    if constexpr (kTree) {  // any row may see the last draft
+    if constexpr (kMode == kTree) {  // any row may see the last draft
       tiles = (s.L + kKeys - 1) / kKeys;
       rest = 0;
       return;
@@ -360,7 +369,7 @@ struct Blocks {
   }
   __device__ __forceinline__ void next() {
     left -= kRows;
-    if constexpr (kTree) return;
+    if constexpr (kMode == kTree) return;
     rest += kRows;
     while (rest >= step) {
       rest -= step;
@@ -369,7 +378,7 @@ struct Blocks {
   }
   // Tiles of this block (a last block that is not full ends earlier).
   __device__ __forceinline__ int width() const {
-    if constexpr (kTree) return max(tiles, 1);
+    if constexpr (kMode == kTree) return max(tiles, 1);
     const int short_by = max(kRows - left, 0) - rest;
     return max(tiles - (short_by > 0) - (short_by > step), 1);
   }
@@ -400,20 +409,45 @@ struct Walk {
   int two;        // it has two query tiles (more than 128 rows)
   int seg, tiles;  // segments and tiles of the share before this one
   int there;       // (in the ring) this segment exists
+  int id, len;     // kListed: the item, the tokens of its blocks
 
-  template <bool kTree>
+  // kListed: to the first item from id on that has tiles; false: there is
+  // none.
+  __device__ __forceinline__ bool to_item(const ChunkParams& p) {
+    for (; id < p.num_items; ++id) {
+      const int4 x = __ldg(p.items + id);
+      if (x.x == 0) continue;
+      W = x.x;
+      b = x.y;
+      block = x.z;
+      len = x.w;
+      s = seq_of(p, b);
+      return true;
+    }
+    return false;
+  }
+
+  template <int kMode>
   __device__ __forceinline__ void enter(const ChunkParams& p) {
-    Blocks<kTree> k;
-    k.begin(p, s, block);
-    W = k.width();
-    two = k.left > 128;
-    end = static_cast<int>(min(static_cast<int64_t>(k.units()), rem + left));
+    if constexpr (kMode == kListed) {
+      const int rows = item_rows<kMode>(p);
+      two = min(rows, s.n * p.G - block * rows) > 128;
+      end = static_cast<int>(
+          min(static_cast<int64_t>(kItemUnits + W), rem + left));
+    } else {
+      Blocks<kMode> k;
+      k.begin(p, s, block);
+      W = k.width();
+      two = k.left > 128;
+      end = static_cast<int>(
+          min(static_cast<int64_t>(k.units()), rem + left));
+    }
     kv0 = max(rem - kItemUnits, 0);
     kv1 = max(end - kItemUnits, 0);
   }
   // To the next segment that has a tile (the first one: from a position with
   // rem set and kv0 == kv1); false: there is none.
-  template <bool kTree>
+  template <int kMode>
   __device__ __forceinline__ bool next(const ChunkParams& p, bool first) {
     if (!first) {
       ++seg;
@@ -426,7 +460,10 @@ struct Walk {
         if (left <= 0) return false;
         if (++h == p.Hkv) {
           h = 0;
-          if (++block * kRows >= s.n * p.G) {
+          if constexpr (kMode == kListed) {
+            ++id;
+            if (!to_item(p)) return false;
+          } else if (++block * kRows >= s.n * p.G) {
             block = 0;
             do {
               if (++b >= p.num_seqs) return false;
@@ -436,7 +473,7 @@ struct Walk {
         }
       }
       first = false;
-      enter<kTree>(p);
+      enter<kMode>(p);
     } while (kv0 >= kv1);
     return true;
   }
@@ -447,13 +484,13 @@ struct Walk {
 // each role would be larger than the loops it serves.  True for the whole
 // warp if there is another segment.  (The softmax warps take theirs from the
 // product warp, through a ring: a call would cost them registers.)
-template <bool kTree>
+template <int kMode>
 __device__ __noinline__ bool advance(const ChunkParams& p, Walk* walk) {
   bool more = false;
   __syncwarp();
   if ((threadIdx.x & 31) == 0) {
     Walk w = *walk;
-    more = w.next<kTree>(p, false);
+    more = w.next<kMode>(p, false);
     *walk = w;
   }
   __syncwarp();
@@ -526,6 +563,84 @@ __device__ __noinline__ bool draft_nan(const ChunkParams& p, const Walk& w,
   for (int j = max(-first, 0); j < w.s.n && j < 32 * p.mask_words; ++j) {
     if ((drafts.bits(j) & 1u) == 0u) continue;
     const int page = (first + j) / p.B, off = first + j - page * p.B;
+    const int32_t blk = __ldg(table + page);
+    if (blk < 0 || blk >= p.num_blocks) continue;
+    const uint8_t code =
+        p.side[1][blk * p.page_stride + p.scale_off + w.h * p.shs +
+                  ((off & ~3) + (group >> 1)) * p.sts + (group & 1) * 4 +
+                  (off & 3)];
+    if ((code & 0x7F) == 0x7F) return true;
+  }
+  return false;
+}
+
+// ---------------------------------------------------------------------------
+// Blocks of lists
+// ---------------------------------------------------------------------------
+// The tokens of an item are those of the blocks that any of its rows selects
+// (rising), one after the other, behind a table of their pages.  A row's bit k
+// says whether it selects the k-th of them; `edge` is the one in which the row
+// itself lies, and of which it sees the tokens up to its own (-1: it does not
+// select that one; -2: a row that is none, and sees all).
+struct Listed {
+  const uint32_t* row;
+  int edge;
+
+  // The bits of a tile's blocks, from bit 0 on.
+  __device__ __forceinline__ uint32_t of_tile(const ChunkParams& p,
+                                              int kt) const {
+    if (edge == -2) return ~0u;
+    const int k = kt * kKeys >> p.sel_shift;
+    return __ldg(row + (k >> 5)) >> (k & 31);
+  }
+  // What the row sees of the half tile's 64 tokens.
+  __device__ __forceinline__ void see(const ChunkParams& p, uint32_t blocks,
+                                      int kt, int half, int pos,
+                                      uint32_t* see0, uint32_t* see1) const {
+    const int at = kt * kKeys + 64 * half, k = at >> p.sel_shift;
+    const int first = kt * kKeys >> p.sel_shift;  // block of bit 0
+    if (p.sel_shift >= 6) {
+      // (a half tile lies in one block)
+      const uint32_t all = blocks >> (k - first) & 1u ? ~0u : 0u;
+      int lim = 63;
+      if (k == edge)
+        lim = (pos & ((1 << p.sel_shift) - 1)) -
+              (at & ((1 << p.sel_shift) - 1));
+      *see0 = all & first_bits(lim);
+      *see1 = all & first_bits(lim - 32);
+      return;
+    }
+    const int per = 64 >> p.sel_shift;  // 2 or 4 blocks of 32 or 16 tokens
+    const uint32_t one = p.sel_shift == 5 ? ~0u : 0xFFFFu;
+    uint32_t out[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i >= per || !(blocks >> (k - first + i) & 1u)) continue;
+      uint32_t x = one;
+      if (k + i == edge) x &= first_bits(pos & ((1 << p.sel_shift) - 1));
+      if (p.sel_shift == 5)
+        out[i & 1] |= x;
+      else
+        out[i >> 1] |= x << (16 * (i & 1));
+    }
+    *see0 = out[0];
+    *see1 = out[1];
+  }
+};
+
+// Whether a token that a row sees has NaN for its V scale of a group.
+__device__ __noinline__ bool listed_nan(const ChunkParams& p, const Walk& w,
+                                        Listed listed, int pos, int group) {
+  const int32_t* table = p.item_pages + w.id * p.item_stride;
+  const int sel = 1 << p.sel_shift;
+  for (int at = 0; at < w.len; ++at) {
+    const int k = at >> p.sel_shift;
+    if (!(__ldg(listed.row + (k >> 5)) >> (k & 31) & 1u) ||
+        (k == listed.edge && (at & (sel - 1)) > (pos & (sel - 1)))) {
+      if (!(__ldg(listed.row + (k >> 5)) >> (k & 31) & 1u)) at |= sel - 1;
+      continue;
+    }
+    const int page = at / p.B, off = at - page * p.B;
     const int32_t blk = __ldg(table + page);
     if (blk < 0 || blk >= p.num_blocks) continue;
     const uint8_t code =
@@ -628,7 +743,7 @@ static_assert(kSmemBytes <= 227 * 1024 && kRawBytes % 16 == 0 &&
 // of the two slots.
 constexpr uint32_t kOCol = 256;
 
-template <bool kF16, bool kTree>
+template <bool kF16, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams p) {
   extern __shared__ __align__(16) uint8_t raw_smem[];
@@ -688,18 +803,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   Walk* ring = reinterpret_cast<Walk*>(smem + kRingAt);
   {
     int64_t* scan = reinterpret_cast<int64_t*>(smem + kScanAt);
-    const int rounds = (p.num_seqs + kThreads - 1) / kThreads;
+    const int entries = kMode == kListed ? p.num_items : p.num_seqs;
+    const int rounds = (entries + kThreads - 1) / kThreads;
     int64_t units = 0, incl = 0, U = 0, u0 = 0, u1 = 0;
-    Seq s;
+    [[maybe_unused]] Seq s;
 #pragma unroll 1
     for (int r = 0; r < (rounds > 1 ? 2 * rounds : 1); ++r) {
       if (r == rounds) U = 0;  // (second time over: the totals again)
       const int b = r % rounds * kThreads + tid;
       units = 0;
-      if (b < p.num_seqs) {
+      if constexpr (kMode == kListed) {
+        const int W = b < entries ? __ldg(&p.items[b].x) : 0;
+        if (W > 0) units = static_cast<int64_t>(kItemUnits + W) * p.Hkv;
+      } else if (b < entries) {
         s = seq_of(p, b);
         if (s.n > 0) {
-          Blocks<kTree> k;
+          Blocks<kMode> k;
           k.begin(p, s, 0);
 #pragma unroll 1
           for (; k.left > 0; k.next()) units += k.units();
@@ -709,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1);
           if (c0 < 0 || c1 < c0 || c1 > p.total_q ||
               __ldg(p.lens + b) > p.len_cap ||
-              (kTree && c1 - c0 > 32 * p.mask_words))
+              (kMode == kTree && c1 - c0 > 32 * p.mask_words))
             flag(p.dev_error, KVQ_DEVERR_SEQ);
         }
       }
@@ -747,19 +866,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (u < incl - units || u >= incl) continue;
         int64_t rem = u - (incl - units);
         Walk w = {};
-        Blocks<kTree> k;
-        k.begin(p, s, 0);
+        int size;
+        if constexpr (kMode == kListed) {
+          w.id = b;
+          w.to_item(p);
+          size = kItemUnits + w.W;
+        } else {
+          Blocks<kMode> k;
+          k.begin(p, s, 0);
 #pragma unroll 1
-        for (; rem >= static_cast<int64_t>(k.units()) * p.Hkv; k.next()) {
-          rem -= static_cast<int64_t>(k.units()) * p.Hkv;
-          ++w.block;
+          for (; rem >= static_cast<int64_t>(k.units()) * p.Hkv; k.next()) {
+            rem -= static_cast<int64_t>(k.units()) * p.Hkv;
+            ++w.block;
+          }
+          size = k.units();
+          w.b = b;
+          w.s = s;
         }
-        const int size = k.units();
-        w.b = b;
         w.h = static_cast<int>(rem) / size;
         const int at = static_cast<int>(rem) - w.h * size;
         w.rem = snap(at, size);
-        w.s = s;
         units_kept[2 - end] = u + w.rem - at;
         if (end == 0) ring[0] = w;
       }
@@ -768,7 +894,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && units_kept[2] < units_kept[1]) {
       Walk w = ring[0];
       w.left = units_kept[1] - units_kept[2];
-      w.there = w.next<kTree>(p, true);
+      w.there = w.next<kMode>(p, true);
       ring[0] = w;
       misc[2] = w.there;
     }
@@ -799,24 +925,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       // drafts; then the bits of `drafts`, its row of the mask)
       int kv0, kv1, pos, tiles, rows;
       [[maybe_unused]] Drafts drafts;
+      [[maybe_unused]] Listed listed;
       {
         const Walk& w = ring[seg & 3];
         kv0 = w.kv0;
         kv1 = w.kv1;
-        rows = min(kRows, w.s.n * p.G - w.block * kRows);
+        const int most = item_rows<kMode>(p);
+        rows = min(most, w.s.n * p.G - w.block * most);
         // (tile kt of this segment is the CTA's (tiles + kt)-th)
         tiles = w.tiles - kv0;
         // two query tiles, or one whose KV tiles the slots share out
         const int at = (rows > 128 ? 128 * m : 0) + row;
-        const int r = w.block * kRows + at;  // row of the sequence
+        const int r = w.block * most + at;  // row of the sequence
         const int tok = r / p.G;
         // (a row that is none sees all, so that it does not slow the others)
-        if constexpr (kTree) {
+        if constexpr (kMode == kTree) {
           pos = at < rows ? w.s.L - w.s.n - 1 : INT32_MAX;
           drafts = {p.mask + (w.s.q0 + (at < rows ? tok : 0)) * p.mask_stride,
                     p.mask_words, w.s.n};
         } else {
           pos = at < rows ? w.s.L - w.s.n + tok : INT32_MAX;
+          if constexpr (kMode == kListed) {
+            const int64_t q = w.s.q0 + (at < rows ? tok : 0);
+            listed.row = p.masks + q * p.mask_words;
+            listed.edge = at < rows ? __ldg(&p.tokens[q].x) : -2;
+          }
         }
         if (m == 0 || rows > 128) {
           // the query rows, rounded to fp16, their sign folded with the
@@ -859,6 +992,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int kt0 = two ? kv0 : kv0 + m, step = two ? 1 : 2;
 #pragma unroll 1
       for (int kt = kt0; kt < kv1; kt += step, ++cnt) {
+        [[maybe_unused]] uint32_t blocks = 0;
+        if constexpr (kMode == kListed) blocks = listed.of_tile(p, kt);
         if (!warp_wait(bar(kSFull + m), cnt & 1, abort)) goto done;
         fence_after();
         // Weights are exp2 of the scaled logits minus a reference: kBelow
@@ -888,10 +1023,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the row sees columns 0 .. lim)
             const int lim = pos - kt * kKeys - 64 * half;
             tmem_wait_ld();
-            if (!__all_sync(0xFFFFFFFFu,
-                            lim >= 63 && (valid.x & valid.y) == ~0u)) {
+            if constexpr (kMode == kListed) {
+              uint32_t see0, see1;
+              listed.see(p, blocks, kt, half, pos, &see0, &see1);
+              see0 &= valid.x;
+              see1 &= valid.y;
+              if (!__all_sync(0xFFFFFFFFu, (see0 & see1) == ~0u)) {
+                mask32(s, see0);
+                mask32(s + 32, see1);
+              }
+            } else if (!__all_sync(0xFFFFFFFFu, lim >= 63 &&
+                                   (valid.x & valid.y) == ~0u)) {
               uint32_t see0 = first_bits(lim), see1 = first_bits(lim - 32);
-              if constexpr (kTree) {
+              if constexpr (kMode == kTree) {
                 // (column 0 is draft -1 - lim)
                 if (lim < 63) {
                   see0 |= drafts.bits(-1 - lim);
@@ -995,9 +1139,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = sum > 0.0f ? __ldg(p.v_scale) / sum
                                    : (sum == 0.0f ? 0.0f : sum);
       bool blind = pos < 0;
-      if constexpr (kTree) blind = blind && none_of(drafts, -1 - pos);
+      if constexpr (kMode == kTree) blind = blind && none_of(drafts, -1 - pos);
+      if constexpr (kMode == kListed)
+        blind = listed.edge != -2 &&
+                __ldg(&p.tokens[(listed.row - p.masks) / p.mask_words].y) == 0;
       float* slot = slot_of(p, blockIdx.x, seg > 0);
-      const int r = w.block * kRows + at, tok = r / p.G;
+      const int r = w.block * item_rows<kMode>(p) + at, tok = r / p.G;
       uint16_t* dst = p.out + (w.s.q0 + tok) * p.out_stride0 +
                       (w.h * p.G + (r - tok * p.G)) * kD;
       float* part = slot + at * kD;
@@ -1028,10 +1175,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int4 x = nan_row[col / 16 + g];
           const int first_nan = min(min(x.x, x.y), min(x.z, x.w));
           bool nan = first_nan <= pos;
-          if constexpr (kTree) {
+          if constexpr (kMode == kTree) {
             if (!nan && first_nan != INT32_MAX)
               nan = draft_nan(p, w, drafts, col / 16 + g);
           }
+          if constexpr (kMode == kListed)
+            nan = first_nan != INT32_MAX && at < rows &&
+                  listed_nan(p, w, listed, pos, col / 16 + g);
           if (nan) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[16 * g + j] = 0x7FFFFFFFu;
@@ -1087,8 +1237,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // `kt` and `walk` are at that one).
     int job = warp - kSoftWarps - 2;  // 0..3: K quarters, 4..7: V quarters
     // (this segment: its sequence's length and table row, its head, its end)
-    int kt = walk->kv0, kv1 = walk->kv1, len = walk->s.L, seg = 0;
-    const int32_t* table = p.block_table + walk->b * p.bt_stride;
+    auto length = [&]() { return kMode == kListed ? walk->len : walk->s.L; };
+    auto pages = [&]() {
+      return kMode == kListed ? p.item_pages + walk->id * p.item_stride
+                              : p.block_table + walk->b * p.bt_stride;
+    };
+    int kt = walk->kv0, kv1 = walk->kv1, len = length(), seg = 0;
+    const int32_t* table = pages();
     int64_t data_h = walk->h * p.dhs;
     int64_t scale_h = p.scale_off + walk->h * p.shs;
     uint32_t cnt = 0;      // tile of the share
@@ -1159,13 +1314,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++cnt;
           first = false;
           if (++kt == kv1) {
-            more = advance<kTree>(p, walk);
+            more = advance<kMode>(p, walk);
             first = true;
             ++seg;
             kt = walk->kv0;
             kv1 = walk->kv1;
-            len = walk->s.L;
-            table = p.block_table + walk->b * p.bt_stride;
+            len = length();
+            table = pages();
             data_h = walk->h * p.dhs;
             scale_h = p.scale_off + walk->h * p.shs;
           }
@@ -1344,7 +1499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the softmax warps too)
           if (m == 0 && lane == 0 && walk->kv0 == 0 && walk->kv1 < walk->W)
             note_cut(p, *walk, units_kept[0], units_kept[1]);
-          go = advance<kTree>(p, walk);
+          go = advance<kMode>(p, walk);
           if (lane == 0) {
             if (m == 0) {
               Walk* next = ring + ((segs + 1) & 3);
@@ -1407,7 +1562,7 @@ gone:
 // ---------------------------------------------------------------------------
 constexpr int kMergeRows = 32;  // rows of a CTA, four to a warp
 
-template <bool kF16, bool kTree>
+template <bool kF16, int kMode>
 __global__ void __launch_bounds__(256)
     chunk_merge_kernel(const __grid_constant__ ChunkParams p) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1420,8 +1575,9 @@ __global__ void __launch_bounds__(256)
     lost |= (reinterpret_cast<const Cut*>(p.workspace) + cta + k)->gave_up;
   if (__syncthreads_or(lost)) return;
   const Seq s = seq_of(p, cut.b);
-  const int row0 = cut.block * kRows;
-  const int rows = min(kRows, s.n * p.G - row0);
+  const int most = item_rows<kMode>(p);
+  const int row0 = cut.block * most;
+  const int rows = min(most, s.n * p.G - row0);
   const int lane = threadIdx.x & 31;
   const float vs = __ldg(p.v_scale);
   const int blind = s.n - s.L;  // tokens that see nothing, whose rows are 0
@@ -1453,11 +1609,12 @@ __global__ void __launch_bounds__(256)
                     4 * lane;
     uint2 w = make_uint2(0, 0);
     bool none = tok < blind;
-    if constexpr (kTree) {
+    if constexpr (kMode == kTree) {
       const Drafts drafts = {p.mask + (s.q0 + tok) * p.mask_stride,
                              p.mask_words, s.n};
       none = blind >= 0 && none_of(drafts, blind);
     }
+    if constexpr (kMode == kListed) none = __ldg(&p.tokens[s.q0 + tok].y) == 0;
     if (none) {
       *reinterpret_cast<uint2*>(dst) = w;
       continue;
@@ -1470,19 +1627,19 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-template <bool kF16, bool kTree>
+template <bool kF16, int kMode>
 cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
   const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<kF16, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      chunk_kernel<kF16, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
       kSmemBytes);
   if (set != cudaSuccess) return set;
   const unsigned ctas = static_cast<unsigned>(sm_count());
   if (ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
-  const cudaError_t err = launch_kernel(chunk_kernel<kF16, kTree>,
+  const cudaError_t err = launch_kernel(chunk_kernel<kF16, kMode>,
                                         dim3(ctas), kThreads, kSmemBytes,
                                         stream, p.pdl, p);
   if (err != cudaSuccess) return err;
-  return launch_kernel(chunk_merge_kernel<kF16, kTree>,
+  return launch_kernel(chunk_merge_kernel<kF16, kMode>,
                        dim3(ctas, kRows / kMergeRows), 256, 0, stream, true,
                        p);
 }
@@ -1506,9 +1663,15 @@ static int short_chunk(const ChunkParams& p) {
   return few && p.max_q_len <= 8 ? p.max_q_len : 1;
 }
 
+cudaError_t launch_listed_attention(const ChunkParams& p,
+                                    cudaStream_t stream) {
+  return p.f16 ? launch<true, kListed>(p, stream)
+               : launch<false, kListed>(p, stream);
+}
+
 cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream) {
-  return p.f16 ? launch<true, true>(p, stream)
-               : launch<false, true>(p, stream);
+  return p.f16 ? launch<true, kTree>(p, stream)
+               : launch<false, kTree>(p, stream);
 }
 
 cudaError_t launch_chunk_attention(const ChunkParams& caller,
@@ -1526,8 +1689,8 @@ cudaError_t launch_chunk_attention(const ChunkParams& caller,
   cudaError_t err = cudaSuccess;
   const bool tiles = p.skip == 0 || p.max_q_len > p.skip;
   if (tiles)
-    err = p.f16 ? launch<true, false>(p, stream)
-                : launch<false, false>(p, stream);
+    err = p.f16 ? launch<true, kCausal>(p, stream)
+                : launch<false, kCausal>(p, stream);
   if (err != cudaSuccess || p.skip == 0) return err;
   AttnParams a{};
   a.q = p.q;

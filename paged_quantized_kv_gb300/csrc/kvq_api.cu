@@ -695,8 +695,9 @@ int64_t kvq_sparse_attention_workspace_bytes(
       max_blocks_per_seq < 0 ||
       !selection_ok(max_selected, select_block, block_size))
     return -1;
-  return sparse_workspace_bytes(sm_count(), total_q, num_q_heads,
-                                max_selected, select_block, block_size);
+  return sparse_workspace_bytes(sm_count(), total_q, num_seqs, num_q_heads,
+                                num_kv_heads, max_selected, select_block,
+                                block_size, max_blocks_per_seq);
 }
 
 kvq_status kvq_sparse_attention_nvfp4(
@@ -729,9 +730,10 @@ kvq_status kvq_sparse_attention_nvfp4(
   if (empty) return KVQ_OK;
   if (selected == nullptr) return KVQ_ERR_NULL;
   if (!aligned(selected, 4)) return KVQ_ERR_ALIGN;
-  if (workspace_bytes < sparse_workspace_bytes(sm_count(), total_q,
-                                               num_q_heads, max_selected,
-                                               select_block, block_size))
+  if (workspace_bytes <
+      sparse_workspace_bytes(sm_count(), total_q, num_seqs, num_q_heads,
+                             num_kv_heads, max_selected, select_block,
+                             block_size, max_blocks_per_seq))
     return KVQ_ERR_SCRATCH;
   p.rows = {cu_q_lens, context_lens, total_q,
             num_seqs,  p.chunk.len_cap, dev_error};
@@ -739,6 +741,7 @@ kvq_status kvq_sparse_attention_nvfp4(
   p.selected_stride0 = selected_stride0;
   p.top = max_selected;
   p.sel = select_block;
+  p.max_blocks = max_blocks_per_seq;
   const cudaError_t err =
       launch_sparse_attention(p, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

@@ -204,6 +204,17 @@ struct ChunkParams {
   const uint32_t* mask;
   int64_t mask_stride;
   int32_t mask_words;
+  // Blocks of lists (kvq_sparse_attention_nvfp4): items of item_tokens tokens
+  // of a sequence, {tiles (0: not an item), sequence, number in it, tokens},
+  // each with the pages of its blocks (rows item_stride apart); for each query
+  // token the blocks that it selects among them (mask_words words), the one
+  // in which it lies (-1: not selected) and the tokens that it sees.
+  const int4* items;
+  const int32_t* item_pages;
+  int64_t item_stride;
+  const uint32_t* masks;
+  const int2* tokens;
+  int32_t num_items, item_tokens, sel_shift;
   bool swizzle_k;
   bool f16;
   bool pdl;
@@ -216,6 +227,7 @@ constexpr int kChunkMaxRows = 1 << 25;
 
 cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t stream);
 cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_listed_attention(const ChunkParams& p, cudaStream_t stream);
 // Workspace bytes of a call on a device of `sms` multiprocessors.
 int64_t chunk_workspace_bytes(int sms);
 
@@ -291,7 +303,12 @@ struct SparseParams {
   QueryRows rows;
   const int32_t* selected;  // [total, top]
   int64_t selected_stride0;
-  int32_t top, sel;
+  int32_t top, sel, max_blocks;
+  // items (chunk.items and so on, as the plan writes them; null: none)
+  int4* items;
+  int32_t* item_pages;
+  uint32_t* masks;
+  int2* tokens;
   // a round of rows: the first, how many, their lengths and tables
   int64_t row0;
   int32_t num_rows;
@@ -300,8 +317,9 @@ struct SparseParams {
 };
 cudaError_t launch_sparse_attention(const SparseParams& p,
                                     cudaStream_t stream);
-int64_t sparse_workspace_bytes(int sms, int64_t total, int32_t Hq,
-                               int32_t top, int32_t sel, int32_t B);
+int64_t sparse_workspace_bytes(int sms, int64_t total, int32_t num_seqs,
+                               int32_t Hq, int32_t Hkv, int32_t top,
+                               int32_t sel, int32_t B, int32_t max_blocks);
 
 // ---------------------------------------------------------------------------
 // Page pool: growing, forking, compacting and freeing sequences

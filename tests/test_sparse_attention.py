@@ -112,6 +112,54 @@ def test_many_rows(near, G):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("sel", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (3, 1), (10, 2), (16, 1)])
+def test_block_lengths_with_many_rows(sel, hq, hkv):
+    """Tokens that share their blocks: tiles of several blocks, and blocks of
+    several tiles; heads that do not divide a tile's rows."""
+    c = Sparse([90, 1, 200], [90 + 5 * sel + 3, 700, 200 + 9 * sel], sel=sel,
+               top=7, near=0.8, hq=hq, hkv=hkv, seed=sel + hq)
+    c.check(c.run())
+
+
+def test_tiles_and_rows_in_one_batch():
+    """One sequence whose rows agree, one whose rows do not, single tokens."""
+    c = Sparse([64, 64, 1, 1], [3000, 3000, 2000, 40], sel=16, top=12, hq=8,
+               hkv=1, near=1.0)
+    other = lists(c.rng, c.cu, c.lens, 130, 16, 12, 0.0)
+    c.selected[64:128] = other[64:128]
+    c.check(c.run())
+
+
+def test_tiles_bad_pages_and_nan():
+    """Bad pages and NaN scales under tiles: what a row does not see cannot
+    reach it, what it sees does."""
+    c = Sparse([64], [64 + 600], sel=32, top=8, hq=8, hkv=1, near=1.0)
+    c.table[0, 5] = -1
+    used = np.unique(c.selected[c.selected >= 0])
+    c.selected[:32, 0] = 2 if 2 < c.selected[:32, 1].min() else c.selected[
+        :32, 0]
+    bits = kvq.KVQ_DEVERR_BLOCK if 2 in c.selected else 0
+    e = int(used[len(used) // 2])
+    plain = c.ref()
+    for t in (32 * e + 3, 32 * e + 31):
+        c.pages.set_scale(1, c.table[0, t // 16], t % 16, 0, 6, 0x7F)
+    got = c.run(bits=bits)
+    has = (c.selected == e).any(1)
+    seen = np.array([600 + i + 1 for i in range(64)])
+    has &= seen > 32 * e + 3
+    assert np.isnan(got[has][:, :, 96:112]).all()
+    assert np.isfinite(got[has][:, :, :96]).all()
+    assert np.isfinite(got[~has]).all()
+    got[has] = plain[0][has]
+    c.check(got, plain)
+
+
+def test_long_context_shared_by_many_ctas():
+    c = Sparse([40], [30000], sel=64, top=200, near=0.9, hq=8, hkv=1)
+    c.check(c.run())
+
+
 def test_every_block_is_the_chunk_attention():
     c = Sparse([40, 1], [700, 333], sel=32, top=22, hq=8, hkv=2)
     got = c.run()
