@@ -1629,10 +1629,17 @@ __global__ void __launch_bounds__(256)
 
 template <bool kF16, int kMode>
 cudaError_t launch(const ChunkParams& p, cudaStream_t stream) {
-  const cudaError_t set = cudaFuncSetAttribute(
-      chunk_kernel<kF16, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      kSmemBytes);
-  if (set != cudaSuccess) return set;
+  static bool configured[64] = {false};  // per instantiation and device
+  int dev = 0;
+  const cudaError_t got = cudaGetDevice(&dev);
+  if (got != cudaSuccess) return got;
+  if (!configured[dev & 63]) {
+    const cudaError_t set = cudaFuncSetAttribute(
+        chunk_kernel<kF16, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        kSmemBytes);
+    if (set != cudaSuccess) return set;
+    configured[dev & 63] = true;
+  }
   const unsigned ctas = static_cast<unsigned>(sm_count());
   if (ctas > kMaxCtas) return cudaErrorInvalidConfiguration;
   const cudaError_t err = launch_kernel(chunk_kernel<kF16, kMode>,

@@ -784,6 +784,9 @@ kvq_status kvq_quantize_indexer_q(
   p.total = total_q;
   p.heads = num_heads;
   p.D = head_dim;
+  p.dense = q_stride0 == static_cast<int64_t>(num_heads) * head_dim &&
+            weights_stride0 == num_heads;
+  p.vec32 = aligned(q, 32) && q_stride0 % 16 == 0;
   p.f16 = dtype == KVQ_DTYPE_FP16;
   p.pdl = (flags & KVQ_F_PDL) != 0u;
   const cudaError_t err =
@@ -895,6 +898,7 @@ kvq_status kvq_select_blocks(const float* scores, int64_t scores_stride0,
   p.scores_stride0 = scores_stride0;
   p.selected = selected;
   p.selected_stride0 = selected_stride0;
+  p.columns = num_columns;
   p.sel = select_block;
   p.top = max_selected;
   p.first = num_first;

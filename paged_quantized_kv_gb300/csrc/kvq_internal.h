@@ -256,6 +256,8 @@ struct QuantizeQParams {
   float* w_out;            // [total, heads]
   int64_t total;
   int32_t heads, D;
+  bool dense;              // no gaps between rows, of q or of weights
+  bool vec32;              // rows start 32-byte aligned (256-bit loads)
   bool f16, pdl;
 };
 cudaError_t launch_quantize_q(const QuantizeQParams& p, cudaStream_t stream);
@@ -289,7 +291,7 @@ struct SelectParams {
   int64_t scores_stride0;
   int32_t* selected;       // [total, top]
   int64_t selected_stride0;
-  int32_t sel, top, first, last;
+  int32_t columns, sel, top, first, last;
   bool pdl;
 };
 cudaError_t launch_select_blocks(const SelectParams& p, cudaStream_t stream);

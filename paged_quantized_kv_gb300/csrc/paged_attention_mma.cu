@@ -1328,6 +1328,9 @@ cudaError_t launch_form_of(const AttnParams& caller, cudaStream_t stream) {
       while (p.part > 512 &&
              rows * ((p.len_cap + p.part - 1) / p.part) < want)
         p.part = p.part > 1024 ? 1024 : 512;
+#ifdef LPART
+      if (p.listed) p.part = LPART;
+#endif
     }
   }
   const int parts =

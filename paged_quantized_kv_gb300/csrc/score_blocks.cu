@@ -800,10 +800,17 @@ cudaError_t tensor_of(const uint8_t* at, int D, int64_t rows, int64_t outer,
 template <int kTiles>
 cudaError_t launch(const ScoreParams& p, int R, int Hp, cudaStream_t stream) {
   auto kernel = score_kernel<kTiles>;
-  cudaError_t err = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      Smem<kTiles>::kBytes);
+  static bool configured[64] = {false};  // per instantiation and device
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  if (!configured[dev & 63]) {
+    err = cudaFuncSetAttribute(kernel,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               Smem<kTiles>::kBytes);
+    if (err != cudaSuccess) return err;
+    configured[dev & 63] = true;
+  }
   // (a power of two; the copies' places and sizes are multiples of 128 and 16
   // bytes)
   const int box = std::gcd(p.B, kTokens);

@@ -29,12 +29,16 @@ namespace {
 constexpr int kPlanThreads = 128;  // rows: a warp for each
 constexpr int kPart = 512;         // partition of the decode scratch
 constexpr int kD = 128;
-constexpr int kUnionThreads = 256;
+constexpr int kUnionThreads = 1024;
+constexpr int kUnionWarps = kUnionThreads / 32;
 constexpr int kMaxUnion = 8192;    // blocks of an item
 // An item goes by tiles if its rows' tokens add up to more than kTileCost for
 // each of its tiles and kTileItem more: a tile of 128 tokens takes the SM as
 // long as that many tokens of rows in the decode kernel (2.1 us at 4.2 ns).
 constexpr int kTileCost = 500, kTileItem = 3;
+
+// Tokens of all rows and KV heads from which on items are looked at.
+constexpr int64_t kItemsFrom = 2500000;
 
 // The entries of a row's list that count: those that lie above all before
 // them and hold something that the row sees.  fn(entry, their number so far),
@@ -76,8 +80,8 @@ __device__ __forceinline__ int tokens_of(int2 list, int sel, int seen) {
 __global__ void __launch_bounds__(kUnionThreads)
     plan_items_kernel(const SparseParams p) {
   pdl_prologue();
-  __shared__ uint32_t bits[kMaxUnion / 32], buffer[8][kMaxUnion / 32];
-  __shared__ int rank[kMaxUnion / 32 + 1], scan[8], sum;
+  __shared__ uint32_t bits[kMaxUnion / 32], buffer[kUnionWarps][kMaxUnion / 32];
+  __shared__ int rank[kMaxUnion / 32], scan[8], sum;
   const ChunkParams& c = p.chunk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = c.item_tokens, x = blockIdx.x;
@@ -115,7 +119,7 @@ __global__ void __launch_bounds__(kUnionThreads)
     return p.selected + (q0 + tok0 + j) * p.selected_stride0;
   };
   auto blocks_of = [&](int j) { return (seen_of(j) + p.sel - 1) / p.sel; };
-  for (int j = warp; j < nt; j += 8) {
+  for (int j = warp; j < nt; j += kUnionWarps) {
     const int2 list = walk_list(list_of(j), p.top, blocks_of(j), &bad,
                                 [&](int e, int) {
                                   atomicOr(&bits[e >> 5], 1u << (e & 31));
@@ -125,7 +129,7 @@ __global__ void __launch_bounds__(kUnionThreads)
   if (__any_sync(~0u, bad) && lane == 0 && c.dev_error != nullptr)
     atomicOr(c.dev_error, KVQ_DEVERR_SEQ);
   __syncthreads();
-  // (a word for each thread)
+  // (a word for each of the first threads)
   const uint32_t mine = tid < words ? bits[tid] : 0u;
   int incl = __popc(mine);
 #pragma unroll
@@ -133,14 +137,14 @@ __global__ void __launch_bounds__(kUnionThreads)
     const int y = __shfl_up_sync(~0u, incl, d);
     if (lane >= d) incl += y;
   }
-  if (lane == 31) scan[warp] = incl;
+  if (lane == 31 && warp < 8) scan[warp] = incl;
   __syncthreads();
   int U = 0;
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < kMaxUnion / 1024; ++w) {
     if (w < warp) incl += scan[w];
     U += scan[w];
   }
-  rank[tid] = incl - __popc(mine);
+  if (tid < kMaxUnion / 32) rank[tid] = incl - __popc(mine);
   const int W = static_cast<int>(
       (static_cast<int64_t>(U) * p.sel + 127) / 128);
   if (sum <= kTileCost * (kTileItem + W)) {  // (nothing is selected: by rows)
@@ -164,7 +168,7 @@ __global__ void __launch_bounds__(kUnionThreads)
   }
   __syncthreads();
   // each token's blocks among them
-  for (int j = warp; j < nt; j += 8) {
+  for (int j = warp; j < nt; j += kUnionWarps) {
     uint32_t* own = buffer[warp];
     for (int w = lane; w < words; w += 32) own[w] = 0;
     __syncwarp();
@@ -293,7 +297,11 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
                     p.sel, c.B, p.max_blocks);
   p.row_lens = reinterpret_cast<int32_t*>(c.workspace + space.row_lens);
   p.row_table = reinterpret_cast<int32_t*>(c.workspace + space.row_table);
-  const bool items = space.num_items > 0 && c.max_q_len > Space::kFewRows;
+  // (and where there is enough to do: else the decode kernel spreads its rows
+  // over the SMs at once, 82 rows of 640 tokens in 10 us, by tiles in 45)
+  const bool items = space.num_items > 0 && c.max_q_len > Space::kFewRows &&
+                     c.total_q * c.Hkv * std::min<int64_t>(tokens, c.len_cap) >
+                         kItemsFrom;
   bool pdl = c.pdl;
   if (items) {
     p.items = reinterpret_cast<int4*>(c.workspace + space.items);

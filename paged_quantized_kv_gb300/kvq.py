@@ -75,6 +75,9 @@ KVQ_DEVERR_TIMEOUT = 8
 KVQ_DEVERR_REF = 16
 KVQ_DEVERR_FULL = 32
 
+_HALF_TYPES = {torch.bfloat16: KVQ_DTYPE_BF16,
+               torch.float16: KVQ_DTYPE_FP16}
+
 _lock = threading.Lock()
 _lib = None
 
@@ -482,16 +485,15 @@ def _dev_error_ok(fn: str, t) -> None:
 
 def _page_views(fn: str, key_cache, value_cache) -> int:
     """Checks the store's 4-D page views; returns their layout."""
-    for t in (key_cache, value_cache):
-        if t.dtype != torch.uint8:
-            raise KvqError(fn, KVQ_ERR_DTYPE)
-        if t.dim() != 4 or t.stride(3) != 1:
-            raise KvqError(fn, KVQ_ERR_SHAPE)
-    n, B, H, full = key_cache.shape
-    if (tuple(value_cache.shape) != (n, B, H, full)
-            or value_cache.stride() != key_cache.stride()):
+    if (key_cache.dtype is not torch.uint8
+            or value_cache.dtype is not torch.uint8):
+        raise KvqError(fn, KVQ_ERR_DTYPE)
+    shape, strides = key_cache.shape, key_cache.stride()
+    if (len(shape) != 4 or strides[3] != 1 or value_cache.shape != shape
+            or value_cache.stride() != strides):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    _, sb, sh, _ = key_cache.stride()
+    _, B, H, full = shape
+    _, sb, sh, _ = strides
     if sb == full and (sh == B * full or H == 1):
         return KVQ_LAYOUT_HND  # (with one head both layouts are the same)
     if sh == full and sb == H * full:
@@ -507,14 +509,17 @@ def chunk_attention_workspace(device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _rows_of(fn: str, t: torch.Tensor, dtype: torch.dtype, total: int) -> int:
-    """The row stride of a matrix [total, width] with contiguous rows."""
+def _rows_of(fn: str, t: torch.Tensor, dtype: torch.dtype, total: int):
+    """(row stride, width) of a matrix [total, width] with contiguous rows."""
     if t.dtype is not dtype:
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if (t.dim() != 2 or t.size(0) != total
-            or (t.size(1) > 1 and t.stride(1) != 1 and t.numel() > 0)):
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != total:
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    return t.stride(0) if total > 1 else t.size(1)
+    stride, step = t.stride()
+    if shape[1] > 1 and step != 1 and total > 0:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
+    return stride if total > 1 else shape[1], shape[1]
 
 
 def _record(t: torch.Tensor, here: int, stream: int | None) -> None:
@@ -533,27 +538,31 @@ def _attend(fn: str, query, key_cache, value_cache, block_table, cu_q_lens,
     """What the attentions of many query tokens per sequence share: checks
     and the call, with the arguments `extra` (of `tensors`) behind the
     contexts'."""
-    dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
-    if query.dtype not in dtypes or out.dtype != query.dtype:
+    # (shapes and strides are asked for once: a call of torch for each would
+    # be most of a small call's time)
+    dtype = _HALF_TYPES.get(query.dtype)
+    if dtype is None or out.dtype is not query.dtype:
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if query.dim() != 3 or out.shape != query.shape:
+    shape, strides, out_strides = query.shape, query.stride(), out.stride()
+    if len(shape) != 3 or out.shape != shape:
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    total, Hq, D = query.shape
-    if (query.stride(2) != 1 or query.stride(1) != D or out.stride(2) != 1
-            or out.stride(1) != D):
+    total, Hq, D = shape
+    if (strides[2] != 1 or strides[1] != D or out_strides[2] != 1
+            or out_strides[1] != D):
         raise KvqError(fn, KVQ_ERR_SHAPE)
     layout = _page_views(fn, key_cache, value_cache)
+    blocks, B, Hkv, full = key_cache.shape
     _vector(fn, torch.int32, cu_q_lens, context_lens)
     n = context_lens.numel()
-    if block_table.dtype != torch.int32:
+    if block_table.dtype is not torch.int32:
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if (cu_q_lens.numel() != n + 1 or block_table.dim() != 2
-            or block_table.size(0) < n
-            or (block_table.numel() > 1 and block_table.size(1) > 1
-                and block_table.stride(1) != 1)
-            or key_cache.size(3) != D // 2 + D // 16):
+    table, table_strides = block_table.shape, block_table.stride()
+    if (cu_q_lens.numel() != n + 1 or len(table) != 2 or table[0] < n
+            or (table[1] > 1 and table[0] > 0 and table_strides[1] != 1)
+            or full != D // 2 + D // 16):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+    if (k_scale.dtype is not torch.float32
+            or v_scale.dtype is not torch.float32):
         raise KvqError(fn, KVQ_ERR_DTYPE)
     _dev_error_ok(fn, dev_error)
     here = _here(fn, query, out, key_cache, value_cache, block_table,
@@ -566,16 +575,15 @@ def _attend(fn: str, query, key_cache, value_cache, block_table, cu_q_lens,
     if not workspace.is_contiguous():
         raise KvqError(fn, KVQ_ERR_SHAPE)
     st = getattr(lib(), fn)(
-        query.data_ptr(), query.stride(0) if total > 1 else Hq * D,
-        dtypes[query.dtype], total, n, cu_q_lens.data_ptr(), int(max_q_len),
-        Hq, key_cache.size(2), D, key_cache.data_ptr(),
-        value_cache.data_ptr(), key_cache.stride(0), key_cache.size(1),
-        key_cache.size(0), layout, block_table.data_ptr(),
-        block_table.stride(0) if n > 1 else block_table.size(1),
-        block_table.size(1), context_lens.data_ptr(), int(max_context_len),
-        *extra, k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
+        query.data_ptr(), strides[0] if total > 1 else Hq * D, dtype, total,
+        n, cu_q_lens.data_ptr(), int(max_q_len), Hq, Hkv, D,
+        key_cache.data_ptr(), value_cache.data_ptr(), key_cache.stride(0), B,
+        blocks, layout, block_table.data_ptr(),
+        table_strides[0] if n > 1 else table[1], table[1],
+        context_lens.data_ptr(), int(max_context_len), *extra,
+        k_scale.data_ptr(), v_scale.data_ptr(), float(scale),
         workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        out.data_ptr(), out.stride(0) if total > 1 else Hq * D, int(flags),
+        out.data_ptr(), out_strides[0] if total > 1 else Hq * D, int(flags),
         _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
@@ -628,10 +636,10 @@ def kvq_tree_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     see its sequence's draft j.  Everything else as for
     ``kvq_chunk_attention_nvfp4``."""
     fn = "kvq_tree_attention_nvfp4"
-    stride = _rows_of(fn, tree_mask, torch.int32, query.size(0))
+    stride, words = _rows_of(fn, tree_mask, torch.int32, query.size(0))
     _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
             context_lens, (tree_mask,),
-            (tree_mask.data_ptr(), stride, tree_mask.size(1)), k_scale,
+            (tree_mask.data_ptr(), stride, words), k_scale,
             v_scale, scale, out, max_q_len, workspace, None, max_context_len,
             flags, dev_error, stream)
 
@@ -645,24 +653,24 @@ def kvq_quantize_indexer_q(q: torch.Tensor, weights: torch.Tensor,
     contiguous), weights fp32 [total_q, heads] times scale and each head's
     scale into weights_out (contiguous)."""
     fn = "kvq_quantize_indexer_q"
-    dtypes = {torch.bfloat16: KVQ_DTYPE_BF16, torch.float16: KVQ_DTYPE_FP16}
-    if q.dtype not in dtypes or q_fp8.element_size() != 1:
+    dtype = _HALF_TYPES.get(q.dtype)
+    if (dtype is None or q_fp8.element_size() != 1
+            or weights_out.dtype is not torch.float32):
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if weights_out.dtype is not torch.float32:
-        raise KvqError(fn, KVQ_ERR_DTYPE)
-    if q.dim() != 3 or q_fp8.shape != q.shape:
+    shape, strides = q.shape, q.stride()
+    if len(shape) != 3 or q_fp8.shape != shape:
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    total, heads, D = q.shape
-    stride = _rows_of(fn, weights, torch.float32, total)
-    if (q.stride(2) != 1 or q.stride(1) != D or weights.size(1) != heads
-            or tuple(weights_out.shape) != (total, heads)
+    total, heads, D = shape
+    stride, width = _rows_of(fn, weights, torch.float32, total)
+    if (strides[2] != 1 or strides[1] != D or width != heads
+            or weights_out.shape != weights.shape
             or not q_fp8.is_contiguous() or not weights_out.is_contiguous()):
         raise KvqError(fn, KVQ_ERR_SHAPE)
     here = _here(fn, q, weights, q_fp8, weights_out)
     st = lib().kvq_quantize_indexer_q(
-        q.data_ptr(), q.stride(0) if total > 1 else heads * D,
-        dtypes[q.dtype], weights.data_ptr(), stride, float(scale), total,
-        heads, D, q_fp8.data_ptr(), weights_out.data_ptr(), int(flags),
+        q.data_ptr(), strides[0] if total > 1 else heads * D, dtype,
+        weights.data_ptr(), stride, float(scale), total, heads, D,
+        q_fp8.data_ptr(), weights_out.data_ptr(), int(flags),
         here if stream is None else stream)
     _check(fn, st)
 
@@ -685,46 +693,45 @@ def kvq_score_blocks_indexer_k(q_fp8: torch.Tensor, weights: torch.Tensor,
     block_table, cu_q_lens, context_lens, max_q_len as for
     ``kvq_chunk_attention_nvfp4``."""
     fn = "kvq_score_blocks_indexer_k"
-    if kv_cache.element_size() != 1 or q_fp8.element_size() != 1:
+    if (kv_cache.element_size() != 1 or q_fp8.element_size() != 1
+            or block_table.dtype is not torch.int32):
         raise KvqError(fn, KVQ_ERR_DTYPE)
-    if block_table.dtype is not torch.int32:
-        raise KvqError(fn, KVQ_ERR_DTYPE)
-    if q_fp8.dim() != 3 or kv_cache.dim() not in (2, 3):
+    shape, strides = q_fp8.shape, q_fp8.stride()
+    cache, cache_strides = kv_cache.shape, kv_cache.stride()
+    if len(shape) != 3 or len(cache) not in (2, 3):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    total, heads, D = q_fp8.shape
+    total, heads, D = shape
     if block_size is None:
-        if kv_cache.dim() != 3:
+        if len(cache) != 3:
             raise KvqError(fn, KVQ_ERR_SHAPE)
-        block_size = kv_cache.size(1)
+        block_size = cache[1]
     # (a block's bytes lie together)
-    held = kv_cache.size(1) * (kv_cache.size(2) if kv_cache.dim() == 3 else 1)
-    if (kv_cache.stride(-1) != 1 or held < block_size * (D + 4)
-            or (kv_cache.dim() == 3
-                and kv_cache.stride(1) != kv_cache.size(2))):
+    held = cache[1] * (cache[2] if len(cache) == 3 else 1)
+    if (cache_strides[-1] != 1 or held < block_size * (D + 4)
+            or (len(cache) == 3 and cache_strides[1] != cache[2])):
         raise KvqError(fn, KVQ_ERR_SHAPE)
-    w_stride = _rows_of(fn, weights, torch.float32, total)
-    s_stride = _rows_of(fn, scores, torch.float32, total)
+    w_stride, width = _rows_of(fn, weights, torch.float32, total)
+    s_stride, columns = _rows_of(fn, scores, torch.float32, total)
     _vector(fn, torch.int32, cu_q_lens, context_lens)
     n = context_lens.numel()
-    if (q_fp8.stride(2) != 1 or q_fp8.stride(1) != D
-            or weights.size(1) != heads or cu_q_lens.numel() != n + 1
-            or block_table.dim() != 2 or block_table.size(0) < n
-            or (block_table.numel() > 1 and block_table.size(1) > 1
-                and block_table.stride(1) != 1)):
+    table, table_strides = block_table.shape, block_table.stride()
+    if (strides[2] != 1 or strides[1] != D or width != heads
+            or cu_q_lens.numel() != n + 1 or len(table) != 2 or table[0] < n
+            or (table[1] > 1 and table[0] > 0 and table_strides[1] != 1)):
         raise KvqError(fn, KVQ_ERR_SHAPE)
     _dev_error_ok(fn, dev_error)
     here = _here(fn, q_fp8, weights, kv_cache, block_table, cu_q_lens,
                  context_lens, scores, dev_error)
     st = lib().kvq_score_blocks_indexer_k(
-        q_fp8.data_ptr(), q_fp8.stride(0) if total > 1 else heads * D,
+        q_fp8.data_ptr(), strides[0] if total > 1 else heads * D,
         weights.data_ptr(), w_stride, total, n, cu_q_lens.data_ptr(),
         int(max_q_len), heads, D, kv_cache.data_ptr(),
-        kv_cache.stride(0) if kv_cache.size(0) > 1 else held,
-        kv_cache.size(0), int(block_size), block_table.data_ptr(),
-        block_table.stride(0) if n > 1 else block_table.size(1),
-        block_table.size(1), context_lens.data_ptr(), int(select_block),
-        scores.data_ptr(), s_stride, scores.size(1), int(flags),
-        _ptr(dev_error), here if stream is None else stream)
+        cache_strides[0] if cache[0] > 1 else held, cache[0],
+        int(block_size), block_table.data_ptr(),
+        table_strides[0] if n > 1 else table[1], table[1],
+        context_lens.data_ptr(), int(select_block), scores.data_ptr(),
+        s_stride, columns, int(flags), _ptr(dev_error),
+        here if stream is None else stream)
     _check(fn, st)
 
 
@@ -742,8 +749,8 @@ def kvq_select_blocks(scores: torch.Tensor, cu_q_lens: torch.Tensor,
     if scores.dim() != 2:
         raise KvqError(fn, KVQ_ERR_SHAPE)
     total = scores.size(0)
-    s_stride = _rows_of(fn, scores, torch.float32, total)
-    l_stride = _rows_of(fn, selected, torch.int32, total)
+    s_stride, columns = _rows_of(fn, scores, torch.float32, total)
+    l_stride, top = _rows_of(fn, selected, torch.int32, total)
     _vector(fn, torch.int32, cu_q_lens, context_lens)
     n = context_lens.numel()
     if cu_q_lens.numel() != n + 1:
@@ -751,11 +758,10 @@ def kvq_select_blocks(scores: torch.Tensor, cu_q_lens: torch.Tensor,
     _dev_error_ok(fn, dev_error)
     here = _here(fn, scores, cu_q_lens, context_lens, selected, dev_error)
     st = lib().kvq_select_blocks(
-        scores.data_ptr(), s_stride, scores.size(1), total, n,
+        scores.data_ptr(), s_stride, columns, total, n,
         cu_q_lens.data_ptr(), context_lens.data_ptr(), int(select_block),
-        int(num_first), int(num_last), selected.data_ptr(), l_stride,
-        selected.size(1), int(flags), _ptr(dev_error),
-        here if stream is None else stream)
+        int(num_first), int(num_last), selected.data_ptr(), l_stride, top,
+        int(flags), _ptr(dev_error), here if stream is None else stream)
     _check(fn, st)
 
 
@@ -796,11 +802,10 @@ def kvq_sparse_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     (``sparse_attention_workspace``) is allocated here when it is not
     given."""
     fn = "kvq_sparse_attention_nvfp4"
-    stride = _rows_of(fn, selected, torch.int32, query.size(0))
+    stride, top = _rows_of(fn, selected, torch.int32, query.size(0))
     _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
             context_lens, (selected,),
-            (selected.data_ptr(), stride, selected.size(1),
-             int(select_block)), k_scale, v_scale, scale, out, max_q_len,
+            (selected.data_ptr(), stride, top, int(select_block)), k_scale, v_scale, scale, out, max_q_len,
             workspace, lambda: sparse_attention_workspace(
                 query, selected, key_cache, block_table, select_block),
             max_context_len, flags, dev_error, stream)

@@ -405,3 +405,13 @@ def test_select_many_rows_and_long_rows():
     x = np.round(rng.standard_normal((64, 9000)) * 50).astype(
         np.float32) / 50
     check_select(x, [0, 64], [9000 * 16], 16, 128, 2, 3)
+
+
+@pytest.mark.parametrize("nb", [16384, 16385, 20000])
+@pytest.mark.parametrize("top,first,last", [(1, 0, 0), (100, 3, 5),
+                                            (16000, 0, 1)])
+def test_select_longest_rows(nb, top, first, last):
+    rng = np.random.default_rng(nb + top)
+    x = np.round(rng.standard_normal((3, nb)) * 200).astype(np.float32) / 200
+    x[1] = 0.25
+    check_select(x, [0, 2, 3], [16 * nb, 16 * nb], 16, top, first, last)
