@@ -56,8 +56,9 @@ constexpr int kIssueWarps = 3;          // of copies and of products
 // (20 warps: 96 registers each)
 constexpr int kThreads = 32 * (kIssueWarp + kIssueWarps);
 
-// Test builds only: in every other thread block an epilogue warp gives up at
-// its third tile as if its wait there had run out (0 in the library).
+// Test builds only: in every other thread block a warp of each warpgroup gives
+// up at its first or second product as if its wait there had run out (0 in
+// the library).
 #ifndef KVQ_TEST_SCORE_GIVE_UP
 #define KVQ_TEST_SCORE_GIVE_UP 0
 #endif
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             goto done;
           fence_after();
           if (KVQ_TEST_SCORE_GIVE_UP != 0 && blockIdx.x % 2 == 1 &&
-              test++ == 2 && part == 1) {
+              test++ == blockIdx.x / 2 % 2 && part == 1) {
             *abort = 1;
             goto done;
           }

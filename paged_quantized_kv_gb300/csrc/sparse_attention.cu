@@ -37,8 +37,12 @@ constexpr int kMaxUnion = 8192;    // blocks of an item
 // long as that many tokens of rows in the decode kernel (2.1 us at 4.2 ns).
 constexpr int kTileCost = 500, kTileItem = 3;
 
-// Tokens of all rows and KV heads from which on items are looked at.
-constexpr int64_t kItemsFrom = 2500000;
+// Tokens of all rows and KV heads from which on items are looked at (test
+// builds: always).
+#ifndef KVQ_SPARSE_ITEMS_FROM
+#define KVQ_SPARSE_ITEMS_FROM 2500000
+#endif
+constexpr int64_t kItemsFrom = KVQ_SPARSE_ITEMS_FROM;
 
 // The entries of a row's list that count: those that lie above all before
 // them and hold something that the row sees.  fn(entry, their number so far),

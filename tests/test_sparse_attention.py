@@ -8,8 +8,26 @@ import torch
 from paged_quantized_kv_gb300 import kvq
 from tests.sparse_models import listed_tokens, masked_attention, rows_of
 from tests.test_chunk_attention import KS, VS, Case
+from tests.variant_build import build_variant
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tiles_library(tmp_path_factory):
+    return build_variant(tmp_path_factory.mktemp("kvq_tiles"), {
+        "sparse_attention.cu": {"KVQ_SPARSE_ITEMS_FROM": 0}})
+
+
+@pytest.fixture(params=["regular", "tiles"], autouse=True)
+def library(request, monkeypatch):
+    """The regular library, whose small batches go by rows alone, and a build
+    that always asks whether tiles pay."""
+    if request.param == "tiles":
+        monkeypatch.setattr(kvq, "LIB_PATH",
+                            request.getfixturevalue("tiles_library"))
+        monkeypatch.setattr(kvq, "_lib", None)
+    yield
 
 
 def lists(rng, cu, lens, total, sel, top, near=0.0):
@@ -153,6 +171,13 @@ def test_tiles_bad_pages_and_nan():
     assert np.isfinite(got[~has]).all()
     got[has] = plain[0][has]
     c.check(got, plain)
+
+
+def test_tiles_of_the_regular_library():
+    """Enough for tiles to be asked for: 300 rows of 2304 tokens, 4 heads."""
+    c = Sparse([300, 1, 2], [6000, 500, 9], sel=64, top=36, near=0.9, hq=8,
+               hkv=4)
+    c.check(c.run())
 
 
 def test_long_context_shared_by_many_ctas():
