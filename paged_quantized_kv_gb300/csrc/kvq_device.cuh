@@ -196,7 +196,7 @@ __device__ __forceinline__ QueryRow query_row(const QueryRows& q, int row) {
     if (n > 0) lo += (n - 1) * step + 1;
   }
   if (lo == 0) return {-1, 0, 0};
-  const int b = lo - 1, c0 = __ldg(q.cu + b);
+  const int b = lo - 1, c0 = max(__ldg(q.cu + b), 0);
   const int c1 = static_cast<int>(
       min(static_cast<int64_t>(__ldg(q.cu + b + 1)), q.total));
   const int L = min(max(__ldg(q.lens + b), 0), q.len_cap);

@@ -273,6 +273,21 @@ def test_score_offsets_out_of_order():
     c.run(bits=kvq.KVQ_DEVERR_SEQ)
 
 
+@pytest.mark.parametrize("first", [-3, -2 ** 31])
+def test_first_offset_below_zero(first):
+    """Taken as 0, and flagged, by the scores and the selection."""
+    c = Scores([40, 3], [900, 77], sel=16)
+    cu, c.cu = c.cu, c.cu.copy()
+    c.cu[0] = first
+    got = c.run(bits=kvq.KVQ_DEVERR_SEQ)
+    x = np.where(np.isneginf(got), 0, got).astype(np.float32)
+    taken = run_select(x, c.cu, c.lens, 16, 9, 1, 1,
+                       bits=kvq.KVQ_DEVERR_SEQ)
+    c.cu = cu
+    c.check(got)
+    assert (taken == select_blocks(x, cu, c.lens, 16, 9, 1, 1)).all()
+
+
 def test_score_repeats_to_the_bit():
     c = Scores([40, 1, 9], [900, 2000, 77], heads=64, sel=32)
     a = c.run()

@@ -296,6 +296,26 @@ def test_context_lens_too_long():
             c.ref(lens=[256]))
 
 
+@pytest.mark.parametrize("first", [-3, -40, -2 ** 31])
+def test_first_offset_below_zero(first):
+    """Taken as 0, and flagged."""
+    c = Sparse([70, 40], [900, 300], hq=8, hkv=1, top=9, near=0.9)
+    cu, c.cu = c.cu, c.cu.copy()
+    c.cu[0] = first
+    got = c.run(bits=kvq.KVQ_DEVERR_SEQ)
+    c.cu = cu
+    c.check(got)
+
+
+def test_last_offset_behind_the_rows():
+    c = Sparse([70, 40], [900, 300], hq=8, hkv=1, top=9, near=0.9)
+    cu, c.cu = c.cu, c.cu.copy()
+    c.cu[2] = 2 ** 31 - 1
+    got = c.run(bits=kvq.KVQ_DEVERR_SEQ)
+    c.cu = cu
+    c.check(got)
+
+
 def test_negative_and_zero_scale():
     for scale in (-0.2, 0.0):
         c = Sparse([2, 20], [300, 500], hq=8, hkv=2, scale=scale)
