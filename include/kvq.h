@@ -726,7 +726,8 @@ kvq_status kvq_sparse_attention_nvfp4(
     int32_t* dev_error, void* stream);
 
 /* Workspace of a kvq_sparse_attention_nvfp4 call on the current device (-1:
-   sizes that the call refuses). */
+   sizes that the call refuses).  It does not shrink with total_q or num_seqs:
+   a workspace for the largest call is one for all. */
 int64_t kvq_sparse_attention_workspace_bytes(
     int64_t total_q, int32_t num_seqs, int32_t num_q_heads,
     int32_t num_kv_heads, int32_t max_selected, int32_t select_block,

@@ -692,7 +692,7 @@ int64_t kvq_sparse_attention_workspace_bytes(
   if (total_q < 0 || total_q > kChunkMaxRows || num_seqs < 0 ||
       num_seqs > kChunkMaxSeqs || num_kv_heads <= 0 || num_q_heads <= 0 ||
       num_q_heads > 1024 || num_q_heads % num_kv_heads != 0 ||
-      max_blocks_per_seq < 0 ||
+      num_q_heads / num_kv_heads > 16 || max_blocks_per_seq < 0 ||
       !selection_ok(max_selected, select_block, block_size))
     return -1;
   return sparse_workspace_bytes(sm_count(), total_q, num_seqs, num_q_heads,

@@ -265,15 +265,20 @@ struct Space {
         item_tokens * top);
     item_stride = blocks * (sel / B);
     words = ((static_cast<int64_t>(max_blocks) * B + sel - 1) / sel + 31) / 32;
-    const bool fits = sel >= 16 && (sel & (sel - 1)) == 0 &&
-                      words <= kMaxUnion / 32 && total > kFewRows &&
-                      num_items * (item_stride * 4 + 16) +
-                              total * (words * 4 + 8) <= kItems;
-    if (!fits) {
+    if (sel < 16 || (sel & (sel - 1)) != 0 || words > kMaxUnion / 32 ||
+        total <= kFewRows) {
       num_items = 0;
       return;
     }
     items = bytes;
+    if (num_items * (item_stride * 4 + 16) + total * (words * 4 + 8) >
+        kItems) {
+      // (what a call of fewer rows or sequences can need: a workspace for the
+      // largest call is one for all)
+      num_items = 0;
+      bytes = items + kItems + 4 * 32;
+      return;
+    }
     item_pages = items + up(num_items * 16);
     tokens = item_pages + up(num_items * item_stride * 4);
     masks = tokens + up(total * 8);

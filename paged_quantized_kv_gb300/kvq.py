@@ -768,12 +768,17 @@ def kvq_select_blocks(scores: torch.Tensor, cu_q_lens: torch.Tensor,
 def sparse_attention_workspace(query: torch.Tensor, selected: torch.Tensor,
                                key_cache: torch.Tensor,
                                block_table: torch.Tensor,
-                               select_block: int) -> torch.Tensor:
-    """Workspace of kvq_sparse_attention_nvfp4 for calls with these sizes
-    (calls that may overlap each need their own)."""
+                               select_block: int,
+                               num_seqs: int | None = None) -> torch.Tensor:
+    """Workspace of kvq_sparse_attention_nvfp4 for calls with these sizes, or
+    with fewer rows or sequences (calls that may overlap each need their own).
+    num_seqs: the sequences of a call (None: as many as the block table has
+    rows)."""
     with torch.cuda.device(query.device):
         n = lib().kvq_sparse_attention_workspace_bytes(
-            query.size(0), block_table.size(0), query.size(1),
+            query.size(0),
+            block_table.size(0) if num_seqs is None else num_seqs,
+            query.size(1),
             key_cache.size(2), selected.size(1), int(select_block),
             key_cache.size(1), block_table.size(1))
     if n < 0:
@@ -805,9 +810,11 @@ def kvq_sparse_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     stride, top = _rows_of(fn, selected, torch.int32, query.size(0))
     _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
             context_lens, (selected,),
-            (selected.data_ptr(), stride, top, int(select_block)), k_scale, v_scale, scale, out, max_q_len,
-            workspace, lambda: sparse_attention_workspace(
-                query, selected, key_cache, block_table, select_block),
+            (selected.data_ptr(), stride, top, int(select_block)), k_scale,
+            v_scale, scale, out, max_q_len, workspace,
+            lambda: sparse_attention_workspace(
+                query, selected, key_cache, block_table, select_block,
+                context_lens.numel()),
             max_context_len, flags, dev_error, stream)
 
 

@@ -82,8 +82,26 @@ def test_sparse_workspace(lib):
                 (1, 1, 0, 2, 8, 32, 16, 64), (1, 1, 7, 2, 8, 32, 16, 64),
                 (1, 1, 8, 0, 8, 32, 16, 64), (1, 1, 8, 2, 0, 32, 16, 64),
                 (1, 1, 8, 2, 8, 24, 16, 64), (1, 1, 8, 2, 8, 32, 0, 64),
-                (1, 1, 8, 2, 8, 32, 16, -1)]:
+                (1, 1, 8, 2, 8, 32, 16, -1), (1, 1, 17, 1, 8, 32, 16, 64),
+                (1, 1, 1024, 1, 8, 32, 16, 64)]:
         assert f(*bad) == -1
+
+
+@pytest.mark.parametrize("sel,top,blocks", [(64, 32, 2048), (16, 8, 512),
+                                            (128, 4, 8192), (48, 8, 100)])
+def test_sparse_workspace_does_not_shrink(lib, sel, top, blocks):
+    """Neither with the rows nor with the sequences, also where its parts
+    reach their limits."""
+    f = lib.kvq_sparse_attention_workspace_bytes
+    sizes = [0, 1, 4, 5, 64, 1000, 4096, 5000, 100000, 1 << 20, 1 << 25]
+    for Hq, Hkv in [(8, 8), (64, 8), (16, 1)]:
+        for n in [0, 1, 7, 1000, 65536]:
+            at = [f(t, n, Hq, Hkv, top, sel, 16, blocks) for t in sizes]
+            assert at == sorted(at) and at[0] > 0
+        for t in sizes:
+            at = [f(t, n, Hq, Hkv, top, sel, 16, blocks)
+                  for n in [0, 1, 7, 1000, 30000, 65536]]
+            assert at == sorted(at)
 
 
 @pytest.mark.parametrize("kw,code", [
