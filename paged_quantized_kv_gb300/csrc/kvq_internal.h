@@ -152,8 +152,11 @@ struct AttnParams {
   int32_t per_seq;
   bool only_short;         // a longer chunk is an error
   // Rows of block lists (kvq_sparse_attention_nvfp4; cu set too): row b has
-  // block-table row b and length lens[b], below 0 for a row that is none.
+  // block-table row b and length lens[b], below 0 for a row that is none.  With
+  // live set there are *live of them, row b for query row row_ids[b].
   bool listed;
+  const int32_t* live;
+  const int32_t* row_ids;
 };
 
 cudaError_t launch_paged_attention_mma(const AttnParams& p,
@@ -311,9 +314,13 @@ struct SparseParams {
   int32_t* item_pages;
   uint32_t* masks;
   int2* tokens;
-  // a round of rows: the first, how many, their lengths and tables
+  // a round of rows (of `rounds`): the first, how many, their lengths and
+  // tables; with items: how many of them no item has (for each round), and
+  // which (only theirs are the lengths and tables then)
   int64_t row0;
-  int32_t num_rows;
+  int32_t round, rounds, num_rows;
+  int32_t* live;
+  int32_t* row_ids;
   int32_t* row_lens;
   int32_t* row_table;
 };

@@ -90,6 +90,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "kvq_internal.h"
@@ -122,6 +123,9 @@ constexpr int kLastShare = KVQ_ATTN_MMA_LAST_SHARE;
 // 300 to 2300 tokens beside longer chunks 90 us at 1792, 84 at 1024; one
 // token over 131000 (592 CTAs) 46 us at 1792, 61 at 1024, 101 at 512.
 constexpr int kChunkCtas = 3;
+// Thread blocks an SM of a launch for rows that a list on the device names
+// (AttnParams::live), in the attention and in the merge.
+constexpr int kListedCtas = 16;
 // the longest stretch (the first of two, 2 kLastShare S / (kLastShare + 1)
 // tokens) leaves each warp at most 1024 tokens: 64 blocks of 16
 static_assert(2 * kLastShare * KVQ_ATTN_MMA_PART / (kLastShare + 1) <=
@@ -191,9 +195,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 // ---------------------------------------------------------------------------
 // Row b of a launch: its query and output row, its sequence (block-table
 // row) and its context length.  A decode step's row b is sequence b.  In a
-// launch for chunks (kChunk) that is not one of block lists it is new token b % per_seq of sequence b / per_seq, which sees the
-// context up to itself; a token that the sequence does not have, or whose
-// sequence has more than per_seq of them, is none (live false).
+// launch for block lists it is query row b, or row_ids[b], with a block-table
+// row of its own.  In another launch for chunks (kChunk) it is new token
+// b % per_seq of sequence b / per_seq, which sees the context up to itself; a
+// token that the sequence does not have, or whose sequence has more than
+// per_seq of them, is none (live false).
 struct Row {
   int64_t q;
   int seq, L;
@@ -210,6 +216,7 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
     return r;
   }
   if (p.listed) {
+    if (p.live != nullptr) r.q = __ldg(p.row_ids + b);
     r.L = __ldg(p.lens + b);
     r.live = r.L >= 0;
     return r;
@@ -447,9 +454,10 @@ constexpr float kChunkBelow = 7.0f;
 // that a warp's range spans at most 64 blocks.
 // Chunks of a few new tokens run here too (kChunk), each token as a row of
 // its own: see row_of.
+// cta: one of (stretch, row, KV head), rows of them a stretch.
 template <int NG, bool kF16, int kPages, bool kChunk>
-__global__ void __launch_bounds__(kThreads, NG == 8 ? 4 : 3)
-paged_attention_mma_kernel(const AttnParams p) {
+__device__ __forceinline__ void attend(const AttnParams& p, int cta,
+                                       int rows) {
   constexpr bool kB8 = kPages >= 9;
   constexpr bool kSwzK = kPages >= 5 && !kB8;
   constexpr int kForm = kB8 ? (kPages == 9 ? 1 : 3) : kSwzK ? kPages - 4
@@ -463,9 +471,9 @@ paged_attention_mma_kernel(const AttnParams p) {
   const int g = lane >> 2, t = lane & 3;
   // stretch-major launch order: (stretch, sequence, KV head), KV head
   // fastest
-  const int kh = static_cast<int>(blockIdx.x % p.Hkv);
-  const int sb = static_cast<int>(blockIdx.x / p.Hkv);
-  const int b = sb % p.num_seqs, part = sb / p.num_seqs;
+  const int kh = cta % p.Hkv;
+  const int sb = cta / p.Hkv;
+  const int b = sb % rows, part = sb / rows;
   // PDL: wait for the kernel before here, or -- when the caller promised
   // that it writes none of the query, block table, context lengths and
   // scales (KVQ_F_PDL_EARLY_META) -- only before the first read of the
@@ -1226,6 +1234,29 @@ paged_attention_mma_kernel(const AttnParams p) {
   }
 }
 
+template <int NG, bool kF16, int kPages, bool kChunk>
+__global__ void __launch_bounds__(kThreads, NG == 8 ? 4 : 3)
+paged_attention_mma_kernel(const AttnParams p) {
+  if constexpr (!kChunk) {
+    attend<NG, kF16, kPages, kChunk>(p, blockIdx.x, p.num_seqs);
+    return;
+  }
+  // Rows that a list names may be fewer than the host knows of: a grid of a
+  // few thread blocks an SM takes them in turn (16384 thread blocks, one for
+  // each row that might be, took 21 us to find that there is none).
+  int rows = p.num_seqs, end = gridDim.x;
+  if (p.live != nullptr) {
+    pdl_prologue();
+    rows = *p.live;
+    end = rows * p.Hkv * max((p.len_cap + p.part - 1) / p.part, 1);
+  }
+#pragma unroll 1
+  for (int cta = blockIdx.x; cta < end; cta += gridDim.x) {
+    attend<NG, kF16, kPages, kChunk>(p, cta, rows);
+    if (p.live != nullptr) __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Merge of the partitions of contexts longer than one partition
 // ---------------------------------------------------------------------------
@@ -1239,74 +1270,83 @@ constexpr int kMergeRows = kMergeThreads / 16;
 // Rows of at most this many partitions issue all their loads at once.
 constexpr int kMergeFew = 4;
 
-template <bool kF16, bool kChunk>
+// kLive: rows that a list on the device names (AttnParams::live), the grid's
+// in turn.
+template <bool kF16, bool kChunk, bool kLive>
 __global__ void __launch_bounds__(kMergeThreads)
 attention_merge_kernel(const AttnParams p) {
   const int sub = threadIdx.x & 15;  // dims 8 sub .. 8 sub + 7
-  const int64_t row =
+  int64_t row =
       static_cast<int64_t>(blockIdx.x) * kMergeRows + (threadIdx.x >> 4);
-  const bool live = row < static_cast<int64_t>(p.num_seqs) * p.Hq;
-  const int b = live ? static_cast<int>(row / p.Hq) : 0;
-  const int h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.Hq)
-                     : 0;
-  const Row me = live ? row_of<kChunk>(p, b) : Row{0, 0, 0, false, false};
-  pdl_prologue();
-  const int L = me.live ? me.L : 0;
-  const int nparts = (L + p.part - 1) / p.part;
-  if (!live || nparts <= 1) return;
-  const int64_t row0 = row * p.max_parts;
-  float M = -INFINITY;
-  float den = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  auto add = [&](float w, const float4& x, const float4& y) {
-    den += w;
-    acc[0] += w * x.x; acc[1] += w * x.y; acc[2] += w * x.z; acc[3] += w * x.w;
-    acc[4] += w * y.x; acc[5] += w * y.y; acc[6] += w * y.z; acc[7] += w * y.w;
-  };
-  if (nparts <= kMergeFew) {
-    // every load of the row in one round trip, then the same sums in order
-    float ml[kMergeFew], es[kMergeFew];
-    float4 xs[kMergeFew], ys[kMergeFew];
+  const int rows = kLive ? __ldg(p.live) : p.num_seqs;
+  do {
+    const bool live = row < static_cast<int64_t>(rows) * p.Hq;
+    const int b = live ? static_cast<int>(row / p.Hq) : 0;
+    const int h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.Hq)
+                       : 0;
+    const Row me = live ? row_of<kChunk>(p, b) : Row{0, 0, 0, false, false};
+    pdl_prologue();
+    const int L = me.live ? me.L : 0;
+    const int nparts = (L + p.part - 1) / p.part;
+    if (!live || (!kLive && nparts <= 1)) return;
+    if (kLive && nparts <= 1) continue;
+    const int64_t row0 = row * p.max_parts;
+    float M = -INFINITY;
+    float den = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float w, const float4& x, const float4& y) {
+      den += w;
+      acc[0] += w * x.x; acc[1] += w * x.y;
+      acc[2] += w * x.z; acc[3] += w * x.w;
+      acc[4] += w * y.x; acc[5] += w * y.y;
+      acc[6] += w * y.z; acc[7] += w * y.w;
+    };
+    if (nparts <= kMergeFew) {
+      // every load of the row in one round trip, then the same sums in order
+      float ml[kMergeFew], es[kMergeFew];
+      float4 xs[kMergeFew], ys[kMergeFew];
 #pragma unroll
-    for (int i = 0; i < kMergeFew; ++i) {
-      if (i < nparts) {
-        ml[i] = p.max_logits[row0 + i];
-        es[i] = p.exp_sums[row0 + i];
+      for (int i = 0; i < kMergeFew; ++i) {
+        if (i < nparts) {
+          ml[i] = p.max_logits[row0 + i];
+          es[i] = p.exp_sums[row0 + i];
+          const float4* src = reinterpret_cast<const float4*>(
+              p.tmp_out + (row0 + i) * kD + 8 * sub);
+          xs[i] = src[0];
+          ys[i] = src[1];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i)
+        if (i < nparts) M = fmaxf(M, ml[i]);
+#pragma unroll
+      for (int i = 0; i < kMergeFew; ++i)
+        if (i < nparts) add(es[i] * ex2(ml[i] - M), xs[i], ys[i]);
+    } else {
+#pragma unroll 4
+      for (int i = 0; i < nparts; ++i) M = fmaxf(M, p.max_logits[row0 + i]);
+#pragma unroll 2
+      for (int i = 0; i < nparts; ++i) {
         const float4* src = reinterpret_cast<const float4*>(
             p.tmp_out + (row0 + i) * kD + 8 * sub);
-        xs[i] = src[0];
-        ys[i] = src[1];
+        add(p.exp_sums[row0 + i] * ex2(p.max_logits[row0 + i] - M), src[0],
+            src[1]);
       }
     }
+    const bool some = has_weights<kChunk>(den);
+    const float f = some ? 1.0f / den : 0.f;
+    const float vs = __ldg(p.v_scale);
+    uint32_t packed[4];
 #pragma unroll
-    for (int i = 0; i < kMergeFew; ++i)
-      if (i < nparts) M = fmaxf(M, ml[i]);
-#pragma unroll
-    for (int i = 0; i < kMergeFew; ++i)
-      if (i < nparts) add(es[i] * ex2(ml[i] - M), xs[i], ys[i]);
-  } else {
-#pragma unroll 4
-    for (int i = 0; i < nparts; ++i) M = fmaxf(M, p.max_logits[row0 + i]);
-#pragma unroll 2
-    for (int i = 0; i < nparts; ++i) {
-      const float4* src = reinterpret_cast<const float4*>(
-          p.tmp_out + (row0 + i) * kD + 8 * sub);
-      add(p.exp_sums[row0 + i] * ex2(p.max_logits[row0 + i] - M), src[0],
-          src[1]);
+    for (int k = 0; k < 4; ++k) {
+      const float y0 = some ? acc[2 * k] * f * vs : 0.f;
+      const float y1 = some ? acc[2 * k + 1] * f * vs : 0.f;
+      packed[k] = static_cast<uint32_t>(float_to_out<kF16>(y0)) |
+                  (static_cast<uint32_t>(float_to_out<kF16>(y1)) << 16);
     }
-  }
-  const bool some = has_weights<kChunk>(den);
-  const float f = some ? 1.0f / den : 0.f;
-  const float vs = __ldg(p.v_scale);
-  uint32_t packed[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float y0 = some ? acc[2 * k] * f * vs : 0.f;
-    const float y1 = some ? acc[2 * k + 1] * f * vs : 0.f;
-    packed[k] = static_cast<uint32_t>(float_to_out<kF16>(y0)) |
-                (static_cast<uint32_t>(float_to_out<kF16>(y1)) << 16);
-  }
-  *reinterpret_cast<uint4*>(p.out + me.q * p.out_stride0 + h * kD + 8 * sub) =
-      make_uint4(packed[0], packed[1], packed[2], packed[3]);
+    *reinterpret_cast<uint4*>(p.out + me.q * p.out_stride0 + h * kD + 8 * sub) =
+        make_uint4(packed[0], packed[1], packed[2], packed[3]);
+  } while (kLive &&
+           (row += static_cast<int64_t>(gridDim.x) * kMergeRows) > 0);
 }
 
 template <int NG, bool kF16, int kPages, bool kChunk>
@@ -1328,9 +1368,6 @@ cudaError_t launch_form_of(const AttnParams& caller, cudaStream_t stream) {
       while (p.part > 512 &&
              rows * ((p.len_cap + p.part - 1) / p.part) < want)
         p.part = p.part > 1024 ? 1024 : 512;
-#ifdef LPART
-      if (p.listed) p.part = LPART;
-#endif
     }
   }
   const int parts =
@@ -1348,8 +1385,11 @@ cudaError_t launch_form_of(const AttnParams& caller, cudaStream_t stream) {
   }
   // one CTA per (stretch, sequence, KV head), stretch-major (the checks
   // keep the count below 2^31)
-  const int64_t ctas =
+  int64_t ctas =
       static_cast<int64_t>(parts > 0 ? parts : 1) * p.num_seqs * p.Hkv;
+  if (kChunk && p.live != nullptr)
+    ctas = std::min<int64_t>(ctas, static_cast<int64_t>(kListedCtas) *
+                                       sm_count());
   const dim3 grid(static_cast<unsigned>(ctas));
   err = launch_kernel(kernel, grid, kThreads,
                       Slots<kContig>::template smem<NG / 8>(), stream, p.pdl,
@@ -1401,13 +1441,20 @@ cudaError_t launch_layout(const AttnParams& p, cudaStream_t stream) {
 
 cudaError_t launch_attention_merge(const AttnParams& p, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.Hq;
-  const dim3 grid(static_cast<unsigned>((rows + kMergeRows - 1) / kMergeRows));
+  int64_t ctas = (rows + kMergeRows - 1) / kMergeRows;
+  if (p.live != nullptr)
+    ctas = std::min<int64_t>(ctas,
+                             static_cast<int64_t>(kListedCtas) * sm_count());
+  const dim3 grid(static_cast<unsigned>(ctas));
   auto kernel =
-      p.cu != nullptr
-          ? (p.f16 ? attention_merge_kernel<true, true>
-                   : attention_merge_kernel<false, true>)
-          : (p.f16 ? attention_merge_kernel<true, false>
-                   : attention_merge_kernel<false, false>);
+      p.live != nullptr
+          ? (p.f16 ? attention_merge_kernel<true, true, true>
+                   : attention_merge_kernel<false, true, true>)
+      : p.cu != nullptr
+          ? (p.f16 ? attention_merge_kernel<true, true, false>
+                   : attention_merge_kernel<false, true, false>)
+          : (p.f16 ? attention_merge_kernel<true, false, false>
+                   : attention_merge_kernel<false, false, false>);
   return launch_kernel(kernel, grid, kMergeThreads, 0, stream, true, p);
 }
 

@@ -89,7 +89,10 @@ __global__ void __launch_bounds__(kUnionThreads)
   const ChunkParams& c = p.chunk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = c.item_tokens, x = blockIdx.x;
-  if (x == 0) dev::check_rows(p.rows, tid, kUnionThreads);
+  if (x == 0) {
+    dev::check_rows(p.rows, tid, kUnionThreads);
+    for (int k = tid; k < p.rounds; k += kUnionThreads) p.live[k] = 0;
+  }
   // the last sequence that begins at x or before
   int lo = 0, hi = c.num_seqs;
   while (lo < hi) {
@@ -195,12 +198,13 @@ __global__ void __launch_bounds__(kUnionThreads)
   }
 }
 
-// The rows from p.row0 on: their tables and lengths (-1: not a row, or an
-// item's).
+// The rows from p.row0 on: their tables and lengths (-1: not a row).  Where
+// items are looked at, only those that no item has, in any order, with their
+// numbers (a row's result does not depend on its place).
 __global__ void __launch_bounds__(kPlanThreads)
     plan_rows_kernel(const SparseParams p) {
   pdl_prologue();
-  const int i = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
+  int i = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (p.row0 == 0 && blockIdx.x == 0)
     dev::check_rows(p.rows, threadIdx.x, kPlanThreads);
@@ -214,8 +218,16 @@ __global__ void __launch_bounds__(kPlanThreads)
     left = p.items[q0 / T + r.seq + r.i / T].x == 0;
   }
   if (!left) {
-    if (lane == 0) p.row_lens[i] = -1;
+    if (lane == 0 && p.items == nullptr) p.row_lens[i] = -1;
     return;
+  }
+  if (p.items != nullptr) {
+    const int id = i;
+    if (lane == 0) {
+      i = atomicAdd(p.live + p.round, 1);
+      p.row_ids[i] = id;
+    }
+    i = __shfl_sync(~0u, i, 0);
   }
   const int per = p.sel / c.B;  // pages of a block
   const int32_t* table = c.block_table + r.seq * c.bt_stride;
@@ -239,9 +251,10 @@ __global__ void __launch_bounds__(kPlanThreads)
 // The workspace
 // ---------------------------------------------------------------------------
 // First the partial results, of the decode kernel's rows (a round of them) or
-// of the tiles' kernel; then the rows' lengths and tables; then the items.
+// of the tiles' kernel; then how many rows each round has, their numbers,
+// lengths and tables; then the items.
 struct Space {
-  int64_t parts, rows, row_lens, row_table;
+  int64_t parts, rows, rounds, live, row_ids, row_lens, row_table;
   int64_t item_tokens, num_items, item_stride, words;  // (num_items 0: none)
   int64_t items, item_pages, masks, tokens, bytes;
 
@@ -254,7 +267,10 @@ struct Space {
     const int64_t row = parts > 1 ? Hq * parts * (kD + 2) * 4 : 4;
     rows = std::max<int64_t>(
         1, std::min(total, std::min<int64_t>(kScratch / row, 4096)));
-    row_lens = up(std::max(chunk_workspace_bytes(sms), rows * row));
+    rounds = (total + rows - 1) / rows;
+    live = up(std::max(chunk_workspace_bytes(sms), rows * row));
+    row_ids = live + up(rounds * 4);
+    row_lens = row_ids + up(rows * 4);
     row_table = row_lens + up(rows * 4);
     bytes = row_table + up(rows * (span / B) * 4);
     // items: blocks of 16, 32, 64 .. tokens, as the masks of a tile need them
@@ -317,6 +333,9 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
     p.item_pages = reinterpret_cast<int32_t*>(c.workspace + space.item_pages);
     p.masks = reinterpret_cast<uint32_t*>(c.workspace + space.masks);
     p.tokens = reinterpret_cast<int2*>(c.workspace + space.tokens);
+    p.live = reinterpret_cast<int32_t*>(c.workspace + space.live);
+    p.row_ids = reinterpret_cast<int32_t*>(c.workspace + space.row_ids);
+    p.rounds = static_cast<int32_t>(space.rounds);
     c.items = p.items;
     c.item_pages = p.item_pages;
     c.masks = p.masks;
@@ -365,8 +384,9 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
   a.pdl = true;
   a.cu = c.cu;
   a.listed = true;
+  a.row_ids = p.row_ids;
   a.tmp_out = reinterpret_cast<float*>(c.workspace);
-  for (p.row0 = 0; p.row0 < c.total_q; p.row0 += space.rows) {
+  for (; p.row0 < c.total_q; p.row0 += space.rows, ++p.round) {
     p.num_rows =
         static_cast<int32_t>(std::min(space.rows, c.total_q - p.row0));
     const unsigned ctas =
@@ -378,6 +398,7 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
     a.q = c.q + p.row0 * c.q_stride0;
     a.out = c.out + p.row0 * c.out_stride0;
     a.num_seqs = p.num_rows;
+    a.live = items ? p.live + p.round : nullptr;
     a.exp_sums = a.tmp_out + p.num_rows * c.Hq * space.parts * kD;
     a.max_logits = a.exp_sums + p.num_rows * c.Hq * space.parts;
     err = launch_paged_attention_mma(a, stream);

@@ -173,6 +173,17 @@ def test_tiles_bad_pages_and_nan():
     c.check(got, plain)
 
 
+def test_tiles_and_rows_in_many_rounds():
+    """Rows that no tile takes, in several rounds, beside rows of tiles."""
+    c = Sparse([600, 100, 33], [640, 700, 600], sel=16, top=2, hq=16, hkv=1,
+               near=0.0)
+    wide = np.full((733, 128), -1, dtype=np.int32)
+    wide[:, :2] = c.selected
+    wide[600:700, :30] = lists(c.rng, c.cu, c.lens, 733, 16, 30, 1.0)[600:700]
+    c.selected = wide
+    c.check(c.run())
+
+
 def test_tiles_of_the_regular_library():
     """Enough for tiles to be asked for: 300 rows of 2304 tokens, 4 heads."""
     c = Sparse([300, 1, 2], [6000, 500, 9], sel=64, top=36, near=0.9, hq=8,
