@@ -542,7 +542,8 @@ int64_t kvq_chunk_attention_workspace_bytes(void);
  * ancestors and its own, the rows are what kvq_chunk_attention_nvfp4 gives on
  * each path of the tree; accepted drafts stay by kvq_compact_sequences and
  * kvq_move_tokens_nvfp4.
- * Arithmetic: as for the longer chunks of kvq_chunk_attention_nvfp4.
+ * Arithmetic: as for kvq_chunk_attention_nvfp4, for small trees and large ones
+ * as for its short chunks and long ones.
  *
  * tree_mask       int32 [total_q, mask_words], device, 4-byte aligned, rows
  *                 tree_mask_stride0 (>= mask_words) words apart; 0 <

@@ -38,8 +38,14 @@
 // exponentials' unit takes one warp's in 4 cycles), and each hand-over some
 // 340 for both ways.
 // Sixteen softmax warps of half a row each were slower, 2.02 ms against 1.65.
-// 16 tokens of 32 sequences over 2000 to 4000: 0.117 to 0.124 ms for 0.13 GB.  Chunks
-// of a few tokens go through the decode kernel instead (short_chunk).
+// 16 tokens of 32 sequences over 2000 to 4000: 0.117 to 0.124 ms for 0.13 GB.
+// Chunks of a few tokens go through the decode kernel instead (short_chunk).
+//
+// The same kernel, as instantiations of their own (kMode), for trees of drafts
+// (a row's mask among the newest tokens: 32 trees of 33 to 64 drafts over 2000
+// to 8000 tokens, 244 GFLOP, 299 us, 815 TFLOP/s: 264 to 512 rows in tiles of
+// 128, two to an item) and for blocks of lists (a row's mask of the blocks that
+// its item selects; see sparse_attention.cu).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -1708,10 +1714,20 @@ int64_t chunk_workspace_bytes(int sms) {
 // five tokens of 8 sequences 25 us against 34 us.  Up to four tokens always,
 // up to eight where there are no more than one (sequence, KV head) per SM;
 // single tokens beside longer chunks too.
-static int short_chunk(const ChunkParams& p) {
+// Trees the same (100 of one draft over 512 to 2560 tokens 43 us against 197, 6
+// of 4 drafts 14 against 28, of 8 drafts 22 against 29), but 5 to 8 drafts only
+// over short contexts: a row's token takes an SM 4.2 ns, a tile's 16.4 and all
+// tiles 26 us more (8 drafts over 60000 tokens of 8 heads 101 us by rows, 75 by
+// tiles), and without a launch for single drafts where there are few trees.
+constexpr int64_t kTreeRowTokens = 2400;  // of an SM, by the longest context
+static int short_chunk(const ChunkParams& p, bool tree) {
   if (p.max_q_len <= 4) return p.max_q_len > 1 ? p.max_q_len : 1;
-  const bool few = static_cast<int64_t>(p.num_seqs) * p.Hkv <= sm_count();
-  return few && p.max_q_len <= 8 ? p.max_q_len : 1;
+  const int64_t each = static_cast<int64_t>(p.num_seqs) * p.Hkv;
+  const bool few = each <= sm_count();
+  if (few && p.max_q_len <= 8 &&
+      (!tree || each * p.len_cap <= kTreeRowTokens * sm_count()))
+    return p.max_q_len;
+  return few && tree ? 0 : 1;
 }
 
 cudaError_t launch_listed_attention(const ChunkParams& p,
@@ -1720,15 +1736,12 @@ cudaError_t launch_listed_attention(const ChunkParams& p,
                : launch<false, kListed>(p, stream);
 }
 
-cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream) {
-  return p.f16 ? launch<true, kTree>(p, stream)
-               : launch<false, kTree>(p, stream);
-}
-
-cudaError_t launch_chunk_attention(const ChunkParams& caller,
-                                   cudaStream_t stream) {
+// Short chunks, or trees, by rows, the others by tiles.
+template <int kMode>
+static cudaError_t launch_rows_and_tiles(const ChunkParams& caller,
+                                         cudaStream_t stream) {
   ChunkParams p = caller;
-  p.skip = short_chunk(p);
+  p.skip = short_chunk(p, kMode == kTree);
   // the decode kernel's scratch: output, sum and maximum of each stretch
   constexpr int kPart = 512;
   const int64_t rows = static_cast<int64_t>(p.num_seqs) * p.skip;
@@ -1740,8 +1753,8 @@ cudaError_t launch_chunk_attention(const ChunkParams& caller,
   cudaError_t err = cudaSuccess;
   const bool tiles = p.skip == 0 || p.max_q_len > p.skip;
   if (tiles)
-    err = p.f16 ? launch<true, kCausal>(p, stream)
-                : launch<false, kCausal>(p, stream);
+    err = p.f16 ? launch<true, kMode>(p, stream)
+                : launch<false, kMode>(p, stream);
   if (err != cudaSuccess || p.skip == 0) return err;
   AttnParams a{};
   a.q = p.q;
@@ -1783,7 +1796,17 @@ cudaError_t launch_chunk_attention(const ChunkParams& caller,
   a.total_q = p.total_q;
   a.per_seq = p.skip;
   a.only_short = !tiles;
+  a.mask = p.mask;
+  a.mask_stride = p.mask_stride;
   return launch_paged_attention_mma(a, stream);
+}
+
+cudaError_t launch_chunk_attention(const ChunkParams& p, cudaStream_t stream) {
+  return launch_rows_and_tiles<kCausal>(p, stream);
+}
+
+cudaError_t launch_tree_attention(const ChunkParams& p, cudaStream_t stream) {
+  return launch_rows_and_tiles<kTree>(p, stream);
 }
 
 }  // namespace kvq

@@ -151,6 +151,11 @@ struct AttnParams {
   int64_t total_q;
   int32_t per_seq;
   bool only_short;         // a longer chunk is an error
+  // Trees of drafts (kvq_tree_attention_nvfp4; cu set too): a row sees what is
+  // before the drafts, and those of the first word of its mask, of which it
+  // has no more than 32.  Null: chunks.
+  const uint32_t* mask;
+  int64_t mask_stride;
   // Rows of block lists (kvq_sparse_attention_nvfp4; cu set too): row b has
   // block-table row b and length lens[b], below 0 for a row that is none.  With
   // live set there are *live of them, row b for query row row_ids[b].

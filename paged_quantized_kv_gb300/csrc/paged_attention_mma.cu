@@ -199,16 +199,21 @@ constexpr float kLog2e = 1.4426950408889634f;
 // row of its own.  In another launch for chunks (kChunk) it is new token
 // b % per_seq of sequence b / per_seq, which sees the context up to itself; a
 // token that the sequence does not have, or whose sequence has more than
-// per_seq of them, is none (live false).
+// per_seq of them, is none (live false).  A tree's draft sees the context before
+// the drafts and, in the steps from there on, those of its mask.
 struct Row {
   int64_t q;
   int seq, L;
   bool live, bad;  // bad: lengths or offsets out of range
+  // a tree's row: the first draft's position (else far behind all), and which
+  // of the drafts it sees
+  int first;
+  uint32_t drafts;
 };
 
 template <bool kChunk>
 __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
-  Row r = {b, b, 0, true, false};
+  Row r = {b, b, 0, true, false, INT32_MAX, 0u};
   if constexpr (!kChunk) {
     r.L = __ldg(p.lens + b);
     r.bad = r.L < 0 || r.L > p.len_cap;
@@ -232,7 +237,13 @@ __device__ __forceinline__ Row row_of(const AttnParams& p, int b) {
                      (p.only_short && n > p.per_seq));
   r.live = i < n && n <= p.per_seq;
   r.q = q0 + i;
-  r.L = max(0, max(0, min(len, p.len_cap)) - n + i + 1);
+  r.L = max(0, min(len, p.len_cap)) - n + i + 1;
+  if (p.mask != nullptr && r.live) {
+    r.first = r.L - i - 1;
+    r.drafts = __ldg(p.mask + r.q * p.mask_stride) & (~0u >> (32 - n));
+    r.L = r.first + 32 - __clz(r.drafts);  // (up to the last one seen)
+  }
+  r.L = max(0, r.L);
   return r;
 }
 
@@ -452,8 +463,8 @@ constexpr float kChunkBelow = 7.0f;
 // bands); 9, 10 = 1, 3 with block_size 8 (linear K scales): 8-token piece
 // j of step i is block 4i + j, and a stretch is kPartB8 tokens long, so
 // that a warp's range spans at most 64 blocks.
-// Chunks of a few new tokens run here too (kChunk), each token as a row of
-// its own: see row_of.
+// Chunks of a few new tokens, small trees of drafts and rows of block lists
+// run here too (kChunk), each token as a row of its own: see row_of.
 // cta: one of (stretch, row, KV head), rows of them a stretch.
 template <int NG, bool kF16, int kPages, bool kChunk>
 __device__ __forceinline__ void attend(const AttnParams& p, int cta,
@@ -880,6 +891,16 @@ __device__ __forceinline__ void attend(const AttnParams& p, int cta,
     // registers live at a time
     float sacc[2][NB][4];
     uint32_t kvalid = 0xFu;  // bit j: K token T0 + g + 8j is usable
+    // rows of trees: bit j: token T0 + j is before the drafts or one that the
+    // row sees
+    [[maybe_unused]] uint32_t see = ~0u;
+    if constexpr (kMasked && kChunk) {
+      const int d = me.first - T0;
+      if (d <= 0)
+        see = d > -32 ? me.drafts >> -d : 0u;
+      else if (d < 32)
+        see = me.drafts << d | ((1u << d) - 1u);
+    }
     if constexpr (kMasked && kB8) {
       // 8-token piece j of the step is the warp's block 4i + j
       const uint32_t vb = static_cast<uint32_t>(bmask64 >> (4 * i)) & 0xFu;
@@ -965,6 +986,11 @@ __device__ __forceinline__ void attend(const AttnParams& p, int cta,
     // every accumulator of the warp is rescaled at once); in between the
     // weights stay below 2^kLazy.  v holds the unscaled logits; c2 > 0 is
     // applied to their maxima and inside each weight's exponent (one FMA).
+    if constexpr (kMasked && kChunk) {
+      const uint32_t own = see >> g;
+      kvalid &= (own & 1u) | (own >> 7 & 2u) | (own >> 14 & 4u) |
+                (own >> 21 & 8u);
+    }
     float v[NB][2][4];
     float bmu[NB][2];  // this lane's maximum unscaled logit of head 8n+2t+c
     bool grow = false;
@@ -1067,6 +1093,10 @@ __device__ __forceinline__ void attend(const AttnParams& p, int cta,
           // left = tokens of the range from this pair's first one on
           const int left = vleft - 16 * h - 8 * q;
           if (left < 2) pair &= left == 1 ? 0x00FF : 0;
+          if constexpr (kChunk) {  // nor one of a draft that is not seen
+            const uint32_t two = see >> (16 * h + 8 * q + 2 * t);
+            pair &= (two & 1u ? 0x00FF : 0) | (two & 2u ? 0xFF00 : 0);
+          }
         }
         const uint32_t sfp = e4m3x2_f16x2(pair);  // {sf(2t), sf(2t+1)}
         uint32_t bw[NB][4];  // even: {P(2t), 0}, {P(2t+1), 0}; odd: swapped
@@ -1123,9 +1153,11 @@ __device__ __forceinline__ void attend(const AttnParams& p, int cta,
     *reinterpret_cast<float*>(smem + SL::kVsc(NB)) = v_scale_in;
   __syncthreads();  // the query is staged
   // the steps with no token to leave out come first; the warp's last
-  // (partial) step, and every step when a block of its range has a bad id,
-  // take the masked form
-  const int nfast = bad_block ? 0 : (w1 - w0) / kStep;
+  // (partial) step, those with drafts of a tree, and every step when a block
+  // of its range has a bad id, take the masked form
+  const int nfast =
+      bad_block ? 0
+                : max((kChunk ? min(w1, me.first) : w1) - w0, 0) / kStep;
   int i = 0;
   for (; i < nfast; ++i) step(i, std::false_type{});
   for (; i < nsteps; ++i) step(i, std::true_type{});
@@ -1284,7 +1316,7 @@ attention_merge_kernel(const AttnParams p) {
     const int b = live ? static_cast<int>(row / p.Hq) : 0;
     const int h = live ? static_cast<int>(row - static_cast<int64_t>(b) * p.Hq)
                        : 0;
-    const Row me = live ? row_of<kChunk>(p, b) : Row{0, 0, 0, false, false};
+    const Row me = live ? row_of<kChunk>(p, b) : Row{0, 0, 0, false, false, 0, 0u};
     pdl_prologue();
     const int L = me.live ? me.L : 0;
     const int nparts = (L + p.part - 1) / p.part;

@@ -14,6 +14,14 @@
 //     of them, and the products are those of 256 rows.
 // A plan kernel unites the lists, counts and decides; another one writes the
 // tables of the rows that are left.
+//
+// Measured, blocks of 64 tokens, 32 a row, 64 query and 8 KV heads: 64 single
+// tokens (153 MB) 40 us, 3.8 TB/s, of which 5 us are the rows' tables and 4 the
+// join of a row's two stretches (the decode kernel's own 32 us: 0.71 of the
+// measured copy rate).  1024 rows over 32768 tokens 254 to 263 us: of the 69
+// GFLOP that the rows ask for the tiles do 2.8 times as many, for the 90 blocks
+// that 32 rows select together, at 860 TFLOP/s; by rows alone 441 us.  Items of
+// 16 rows would select 78 blocks together for half the rows.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -230,3 +230,84 @@ def test_random(seed):
              seed=seed, pad_rows=int(seed % 3))
     if c.q.shape[0]:
         c.check(c.run())
+
+
+# Trees of up to 8 drafts go by rows where they are few over short contexts, of
+# up to 4 always; single drafts too beside larger trees of many sequences.
+@pytest.mark.parametrize("n", [1, 3, 4, 5, 8])
+@pytest.mark.parametrize("first", [0, 1, 24, 27, 28, 31, 32, 60, 93, 120, 127,
+                                   500])
+def test_small_trees_anywhere_in_a_step(n, first):
+    c = Tree([n, n], [first + n, first + n + 3], hq=8, hkv=2, seed=first + n)
+    c.mask[n:] = c.rng.integers(0, 1 << 32, c.mask[n:].shape)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("block", [4, 8, 12, 16, 32, 64, 128])
+@pytest.mark.parametrize("nhd", [False, True])
+@pytest.mark.parametrize("swz", [False, True])
+@pytest.mark.parametrize("G", [4, 16])
+def test_small_trees_of_all_layouts(block, nhd, swz, G):
+    c = Tree([6, 1, 8], [100, 200, 333], hq=2 * G, hkv=2, block=block, nhd=nhd,
+             swz=swz, f16=nhd)
+    c.check(c.run())
+
+
+def test_small_trees_of_no_mask_and_short_contexts():
+    c = Tree([8, 8, 3, 2], [60, 8, 2, 0], hq=8, hkv=2)
+    c.mask[:4] = 0
+    c.mask[8:12] = 0xFFFFFF00     # (bits behind the last draft)
+    c.mask[16:19, 0] = [1, 2, 7]  # (the first draft has no place)
+    c.check(c.run())
+
+
+def test_many_small_trees():
+    rng = np.random.default_rng(5)
+    q = rng.integers(0, 5, 100)
+    c = Tree(list(q), list(q + rng.integers(0, 300, 100)), hq=8, hkv=2)
+    c.check(c.run())
+
+
+def test_single_drafts_beside_large_trees():
+    rng = np.random.default_rng(6)
+    q = np.where(rng.random(100) < 0.7, 1, rng.integers(0, 40, 100))
+    c = Tree(list(q), list(q + rng.integers(0, 300, 100)), hq=8, hkv=2)
+    c.mask[:5] = 0
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("q_lens,lens,hkv", [
+    ([3, 7], [9000, 4100], 1), ([4, 2], [5, 20000], 8),
+    ([8], [60000], 8)])
+def test_small_trees_of_several_stretches(q_lens, lens, hkv):
+    c = Tree(q_lens, lens, hq=8, hkv=hkv)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("first", [64, 61, 90])
+def test_masked_drafts_of_small_trees_reach_nothing(first):
+    """NaN scales of drafts: rows that see one are NaN (in its group, for V),
+    the others as without it."""
+    c = Tree([6], [first + 6], hq=4, hkv=1)
+    c.mask[:, 0] = [0b1, 0b11, 0b101, 0b1001, 0b10001, 0b110101]
+    plain = [a.copy() for a in c.ref()]
+    tok = first + 4     # V: rows 4 and 5
+    c.pages.set_scale(1, c.table[0, tok // 16], tok % 16, 0, 3, 0x7F)
+    tok = first + 3     # K: row 3
+    c.pages.set_scale(0, c.table[0, tok // 16], tok % 16, 0, 1, 0x7F)
+    got = c.run()
+    assert np.isnan(got[3]).all()
+    for r in (4, 5):
+        assert np.isnan(got[r, :, 48:64]).all()
+        assert np.isfinite(got[r, :, :48]).all()
+        assert np.isfinite(got[r, :, 64:]).all()
+    plain[0][3:] = got[3:] = 0
+    c.check(got, tuple(plain))
+
+
+def test_small_trees_bad_pages():
+    c = Tree([6, 4], [400, 300], hq=8, hkv=2)
+    c.table[0, 3] = -1
+    c.table[0, 24] = 1 << 29     # (the drafts' page)
+    c.table[1, 0] = c.pages.nb
+    c.check(c.run(bits=kvq.KVQ_DEVERR_BLOCK))
