@@ -11,9 +11,10 @@ Two memory-bound CUDA kernels for sm_103a behind a C-ABI library
   ``block_table`` and ``cu_seq_lens``.
 
 Beside them: the NVFP4 read, the indexer-K store, decode attention, attention
-of chunks of new tokens over the NVFP4 pages, and the state of a paged cache
-on the device (extend, fork, compact, free) with the page copies and token
-moves that go with it.
+of chunks of new tokens and of trees of drafts over the NVFP4 pages, sparse
+attention over the blocks that an indexer's scores select, and the state of a
+paged cache on the device (extend, fork, compact, free) with the page copies
+and token moves that go with it.
 
 ``paged_quantized_kv_gb300.kvq`` is the thin Python binding (ctypes; torch
 tensors only supply device pointers and the current stream).  Importing the
