@@ -20,7 +20,7 @@
 // join of a row's two stretches (the decode kernel's own 32 us: 0.71 of the
 // measured copy rate).  1024 rows over 32768 tokens 254 to 263 us: of the 69
 // GFLOP that the rows ask for the tiles do 2.8 times as many, for the 90 blocks
-// that 32 rows select together, at 860 TFLOP/s; by rows alone 441 us.  Items of
+// that 32 rows select together, at 853 TFLOP/s; by rows alone 441 us.  Items of
 // 16 rows would select 78 blocks together for half the rows.
 #include <cuda_runtime.h>
 #include <stdint.h>
