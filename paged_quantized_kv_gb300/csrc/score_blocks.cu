@@ -104,6 +104,8 @@ struct Smem {
   static constexpr int kStart = kScan + 32 * 8;  // total, place, sequence
   static constexpr int kBytes = kStart + 32 + 1024;
   static_assert(kBytes <= 227 * 1024, "");
+  // (a stage is always filled by the same warp)
+  static_assert(kStages % kTmaWarps == 0, "");
 };
 
 // kind::f8f6f4, e4m3 operands, fp32 accumulator, M = 128, K-major; N to add.
@@ -739,10 +741,12 @@ done:
     if (warp == kRowWarp)
       for (uint32_t k = loads > 2 ? loads - 2 : 0; k < loads; ++k)
         mbar_wait(bar(S::kQuery + (k & 1)), k >> 1 & 1);
+    // (its own copies: what the other such warp has not begun never lands)
     if (warp >= kIssueWarp && warp < S::kMmaWarp && box_shift >= 0)
       for (uint32_t k = issued > S::kStages ? issued - S::kStages : 0;
            k < issued; ++k)
-        mbar_wait(bar(S::kFull + k % S::kStages), k / S::kStages & 1);
+        if (k % S::kTmaWarps == static_cast<uint32_t>(warp - kIssueWarp))
+          mbar_wait(bar(S::kFull + k % S::kStages), k / S::kStages & 1);
     if (warp >= S::kMmaWarp) {
       if (elect()) {
         mma_commit(bar(S::kLast));
