@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libkvq.so")
 
 SOURCES = ["kvq_api.cu", "store_nvfp4.cu", "gather_indexer_k.cu",
            "load_nvfp4.cu", "store_indexer_k.cu", "attention_noalloc.cu",
-           "paged_attention_mma.cu", "chunk_attention.cu", "page_pool.cu",
+           "paged_attention_mma.cu", "attention_chunk_rows.cu",
+           "attention_marked_rows.cu", "chunk_attention.cu", "page_pool.cu",
            "page_move.cu", "quantize_indexer_q.cu", "score_blocks.cu",
            "select_blocks.cu", "sparse_attention.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -68,16 +69,18 @@ def build(force: bool = False, ptxas_verbose: bool = False,
 
 def _build_locked(lib, bdir, ptxas_verbose, defines):
     nvcc = _nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
-    extra += [f"-D{k}={v}" for k, v in (defines or {}).items()]
+    extra = [f"-D{k}={v}" for k, v in (defines or {}).items()]
 
     def compile_one(src):
         obj = os.path.join(bdir, src.replace(".cu", ".o"))
-        cmd = [nvcc, *ARCH, *NVCC_FLAGS, *extra, "-c",
+        cmd = [nvcc, *ARCH, *NVCC_FLAGS, "-Xptxas", "-v", *extra, "-c",
                os.path.join(CSRC, src), "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed for {src}:\n{r.stdout}\n{r.stderr}")
+        # (registers, spills and shared memory of each kernel)
+        with open(os.path.join(bdir, src + ".ptxas"), "w") as log:
+            log.write(r.stderr)
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(len(SOURCES)) as ex:

@@ -166,6 +166,9 @@ struct AttnParams {
 
 cudaError_t launch_paged_attention_mma(const AttnParams& p,
                                        cudaStream_t stream);
+// The same for rows of chunks, and of trees and block lists.
+cudaError_t launch_chunk_rows(const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_marked_rows(const AttnParams& p, cudaStream_t stream);
 // The argument checks of kvq_paged_attention_nvfp4 other than those of its
 // scratch pointers (KVQ_OK when they pass); kvq_paged_attention_nvfp4_noalloc
 // runs them before it checks its scratch capacity.
