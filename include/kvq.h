@@ -701,14 +701,24 @@ kvq_status kvq_select_blocks(const float* scores, int64_t scores_stride0,
  * before it, or whose block holds nothing that the row could see, is skipped
  * and flagged (KVQ_DEVERR_SEQ).
  * Arithmetic: as for kvq_chunk_attention_nvfp4.
+ * Chunks of more than four tokens whose rows select much the same blocks are
+ * computed together, as tiles (decided on the device, for each group of rows),
+ * where select_block is a power of two from 16 on and the longest context that
+ * the call allows -- max_context_len, else the width of block_table -- has at
+ * most 8192 blocks of select_block tokens.  Elsewhere every row is computed by
+ * itself, which takes a prompt up to two and a half times as long (1024 rows,
+ * 2048 of 32768 tokens of 64 query and 8 KV heads: 421 us for 174): give
+ * max_context_len with a wide block_table.
  *
  * selected       int32 [total_q, max_selected], rows selected_stride0 apart
  *                (those of kvq_select_blocks).
  * select_block   a multiple of block_size; max_selected * select_block <=
  *                2^20.
  * workspace      at least kvq_sparse_attention_workspace_bytes(...) of the
- *                call's sizes (else KVQ_ERR_SCRATCH), 32-byte aligned;
- *                otherwise as for kvq_chunk_attention_nvfp4.
+ *                call's sizes (else KVQ_ERR_SCRATCH), with max_blocks_per_seq
+ *                the width of block_table, or less where max_context_len fits
+ *                into fewer blocks; 32-byte aligned; otherwise as for
+ *                kvq_chunk_attention_nvfp4.
  * All other arguments, flags, errors and limits as for
  * kvq_chunk_attention_nvfp4.
  */
@@ -727,8 +737,10 @@ kvq_status kvq_sparse_attention_nvfp4(
     int32_t* dev_error, void* stream);
 
 /* Workspace of a kvq_sparse_attention_nvfp4 call on the current device (-1:
-   sizes that the call refuses).  It does not shrink with total_q or num_seqs:
-   a workspace for the largest call is one for all. */
+   sizes that the call refuses).  It does not shrink with total_q, num_seqs or
+   max_blocks_per_seq: a workspace for the largest call is one for all.  64
+   query and 8 KV heads, 32 blocks of 64 tokens a row: 137 MB for 1024 rows, 282
+   MB for 8192 rows over a million tokens. */
 int64_t kvq_sparse_attention_workspace_bytes(
     int64_t total_q, int32_t num_seqs, int32_t num_q_heads,
     int32_t num_kv_heads, int32_t max_selected, int32_t select_block,

@@ -248,7 +248,6 @@ kvq_status kvq_gather_indexer_k(const uint8_t* kv_cache, int64_t block_stride,
   p.total = total_tokens;
   p.B = block_size;
   p.D = head_dim;
-  p.max_blocks = max_blocks_per_seq;
   p.num_seqs = num_seqs;
   p.early_read = (flags & KVQ_F_PDL_EARLY_READ) != 0u;
   p.early_meta = p.early_read || (flags & KVQ_F_PDL_EARLY_META) != 0u;
@@ -351,7 +350,6 @@ kvq_status kvq_load_nvfp4(const uint8_t* key_cache, const uint8_t* value_cache,
   if (passes >= (int64_t{1} << 31)) return KVQ_ERR_SHAPE;
   p.num_passes = static_cast<int32_t>(passes);
   p.num_seqs = num_seqs;
-  p.max_blocks = max_blocks_per_seq;
   p.swizzle_sides = 2u | ((flags & KVQ_F_SWIZZLE_K_SCALE) ? 1u : 0u);
   p.early_meta = (flags & KVQ_F_PDL_EARLY_META) != 0u;
   p.pdl = p.early_meta || (flags & KVQ_F_PDL) != 0u;
@@ -730,10 +728,13 @@ kvq_status kvq_sparse_attention_nvfp4(
   if (empty) return KVQ_OK;
   if (selected == nullptr) return KVQ_ERR_NULL;
   if (!aligned(selected, 4)) return KVQ_ERR_ALIGN;
+  // (pages of the longest context that the call allows)
+  const int32_t pages = static_cast<int32_t>(
+      (static_cast<int64_t>(p.chunk.len_cap) + block_size - 1) / block_size);
   if (workspace_bytes <
       sparse_workspace_bytes(sm_count(), total_q, num_seqs, num_q_heads,
                              num_kv_heads, max_selected, select_block,
-                             block_size, max_blocks_per_seq))
+                             block_size, pages))
     return KVQ_ERR_SCRATCH;
   p.rows = {cu_q_lens, context_lens, total_q,
             num_seqs,  p.chunk.len_cap, dev_error};
@@ -741,7 +742,6 @@ kvq_status kvq_sparse_attention_nvfp4(
   p.selected_stride0 = selected_stride0;
   p.top = max_selected;
   p.sel = select_block;
-  p.max_blocks = max_blocks_per_seq;
   const cudaError_t err =
       launch_sparse_attention(p, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? KVQ_OK : KVQ_ERR_CUDA;

@@ -316,7 +316,7 @@ struct SparseParams {
   QueryRows rows;
   const int32_t* selected;  // [total, top]
   int64_t selected_stride0;
-  int32_t top, sel, max_blocks;
+  int32_t top, sel;
   // items (chunk.items and so on, as the plan writes them; null: none)
   int4* items;
   int32_t* item_pages;

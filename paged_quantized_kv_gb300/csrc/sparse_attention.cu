@@ -39,7 +39,7 @@ constexpr int kPart = 512;         // partition of the decode scratch
 constexpr int kD = 128;
 constexpr int kUnionThreads = 1024;
 constexpr int kUnionWarps = kUnionThreads / 32;
-constexpr int kMaxUnion = 8192;    // blocks of an item
+constexpr int kMaxUnion = 8192;    // blocks of a context that items can name
 // An item goes by tiles if its rows' tokens add up to more than kTileCost for
 // each of its tiles and kTileItem more: a tile of 128 tokens takes the SM as
 // long as that many tokens of rows in the decode kernel (2.1 us at 4.2 ns).
@@ -260,14 +260,14 @@ __global__ void __launch_bounds__(kPlanThreads)
 // ---------------------------------------------------------------------------
 // First the partial results, of the decode kernel's rows (a round of them) or
 // of the tiles' kernel; then how many rows each round has, their numbers,
-// lengths and tables; then the items.
+// lengths and tables; then the items, for contexts of up to `context` tokens.
 struct Space {
   int64_t parts, rows, rounds, live, row_ids, row_lens, row_table;
   int64_t item_tokens, num_items, item_stride, words;  // (num_items 0: none)
   int64_t items, item_pages, masks, tokens, bytes;
 
   Space(int sms, int64_t total, int32_t num_seqs, int32_t Hq, int32_t Hkv,
-        int32_t top, int32_t sel, int32_t B, int32_t max_blocks) {
+        int32_t top, int32_t sel, int32_t B, int64_t context) {
     constexpr int64_t kScratch = int64_t{256} << 20, kItems = kScratch;
     const int64_t span = static_cast<int64_t>(top) * sel;
     auto up = [](int64_t x) { return (x + 31) / 32 * 32; };
@@ -284,12 +284,10 @@ struct Space {
     // items: blocks of 16, 32, 64 .. tokens, as the masks of a tile need them
     item_tokens = 256 / (Hq / Hkv);
     num_items = total / item_tokens + num_seqs;
-    const int64_t blocks = std::min<int64_t>(
-        (static_cast<int64_t>(max_blocks) * B + sel - 1) / sel,
-        item_tokens * top);
-    item_stride = blocks * (sel / B);
-    words = ((static_cast<int64_t>(max_blocks) * B + sel - 1) / sel + 31) / 32;
-    if (sel < 16 || (sel & (sel - 1)) != 0 || words > kMaxUnion / 32 ||
+    const int64_t blocks = (context + sel - 1) / sel;
+    item_stride = std::min(blocks, item_tokens * top) * (sel / B);
+    words = (blocks + 31) / 32;
+    if (sel < 16 || (sel & (sel - 1)) != 0 || blocks > kMaxUnion ||
         total <= kFewRows) {
       num_items = 0;
       return;
@@ -318,7 +316,12 @@ struct Space {
 int64_t sparse_workspace_bytes(int sms, int64_t total, int32_t num_seqs,
                                int32_t Hq, int32_t Hkv, int32_t top,
                                int32_t sel, int32_t B, int32_t max_blocks) {
-  return Space(sms, total, num_seqs, Hq, Hkv, top, sel, B, max_blocks).bytes;
+  // (calls over longer contexts have no items: what those up to there need is
+  // enough for them)
+  const int64_t context =
+      std::min(static_cast<int64_t>(max_blocks) * B,
+               static_cast<int64_t>(kMaxUnion) * sel);
+  return Space(sms, total, num_seqs, Hq, Hkv, top, sel, B, context).bytes;
 }
 
 cudaError_t launch_sparse_attention(const SparseParams& caller,
@@ -327,7 +330,7 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
   ChunkParams& c = p.chunk;
   const int64_t tokens = static_cast<int64_t>(p.top) * p.sel;
   const Space space(sm_count(), c.total_q, c.num_seqs, c.Hq, c.Hkv, p.top,
-                    p.sel, c.B, p.max_blocks);
+                    p.sel, c.B, c.len_cap);
   p.row_lens = reinterpret_cast<int32_t*>(c.workspace + space.row_lens);
   p.row_table = reinterpret_cast<int32_t*>(c.workspace + space.row_table);
   // (and where there is enough to do: else the decode kernel spreads its rows

@@ -769,18 +769,22 @@ def sparse_attention_workspace(query: torch.Tensor, selected: torch.Tensor,
                                key_cache: torch.Tensor,
                                block_table: torch.Tensor,
                                select_block: int,
-                               num_seqs: int | None = None) -> torch.Tensor:
+                               num_seqs: int | None = None,
+                               max_context_len: int = 0) -> torch.Tensor:
     """Workspace of kvq_sparse_attention_nvfp4 for calls with these sizes, or
     with fewer rows or sequences (calls that may overlap each need their own).
     num_seqs: the sequences of a call (None: as many as the block table has
-    rows)."""
+    rows); max_context_len: the longest context (0: the block table's
+    width)."""
+    B, blocks = key_cache.size(1), block_table.size(1)
+    if max_context_len > 0 and B > 0:
+        blocks = min(blocks, -(-max_context_len // B))
     with torch.cuda.device(query.device):
         n = lib().kvq_sparse_attention_workspace_bytes(
             query.size(0),
             block_table.size(0) if num_seqs is None else num_seqs,
             query.size(1),
-            key_cache.size(2), selected.size(1), int(select_block),
-            key_cache.size(1), block_table.size(1))
+            key_cache.size(2), selected.size(1), int(select_block), B, blocks)
     if n < 0:
         raise KvqError("sparse_attention_workspace", KVQ_ERR_SHAPE)
     return torch.empty(n, dtype=torch.uint8, device=query.device)
@@ -814,7 +818,7 @@ def kvq_sparse_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
             v_scale, scale, out, max_q_len, workspace,
             lambda: sparse_attention_workspace(
                 query, selected, key_cache, block_table, select_block,
-                context_lens.numel()),
+                context_lens.numel(), max_context_len),
             max_context_len, flags, dev_error, stream)
 
 

@@ -251,3 +251,16 @@ def test_binding_indexer(lib):
     refused(SHAPE, f, s, i32(3), i32(2), i32(3, 2), 64)
     refused(SHAPE, f, s, i32(2), i32(2), i32(4, 2), 64)
     refused(kvq.KVQ_ERR_DTYPE, f, s, i32(3), i32(2), i32(4, 2).long(), 64)
+
+
+@pytest.mark.parametrize("sel,top", [(16, 8), (64, 32), (128, 4)])
+def test_sparse_workspace_does_not_shrink_with_the_table(lib, sel, top):
+    """Also beyond the contexts that tiles can name: a call on a wide table
+    whose longest context is shorter has them."""
+    f = lib.kvq_sparse_attention_workspace_bytes
+    edge = 8192 * sel // 16
+    widths = [0, 1, 64, 2048, edge - 1, edge, edge + 1, 2 * edge, 1 << 22]
+    for total, n in [(1, 1), (100, 3), (1024, 1), (5000, 70)]:
+        at = [f(total, n, 64, 8, top, sel, 16, w) for w in widths]
+        assert at == sorted(at)
+        assert at[-1] == at[5]
