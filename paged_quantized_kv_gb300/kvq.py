@@ -636,6 +636,8 @@ def kvq_tree_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     see its sequence's draft j.  Everything else as for
     ``kvq_chunk_attention_nvfp4``."""
     fn = "kvq_tree_attention_nvfp4"
+    if query.dim() != 3:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
     stride, words = _rows_of(fn, tree_mask, torch.int32, query.size(0))
     _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
             context_lens, (tree_mask,),
@@ -776,6 +778,9 @@ def sparse_attention_workspace(query: torch.Tensor, selected: torch.Tensor,
     num_seqs: the sequences of a call (None: as many as the block table has
     rows); max_context_len: the longest context (0: the block table's
     width)."""
+    if (query.dim() != 3 or selected.dim() != 2 or key_cache.dim() != 4
+            or block_table.dim() != 2):
+        raise KvqError("sparse_attention_workspace", KVQ_ERR_SHAPE)
     B, blocks = key_cache.size(1), block_table.size(1)
     if max_context_len > 0 and B > 0:
         blocks = min(blocks, -(-max_context_len // B))
@@ -811,6 +816,8 @@ def kvq_sparse_attention_nvfp4(query: torch.Tensor, key_cache: torch.Tensor,
     (``sparse_attention_workspace``) is allocated here when it is not
     given."""
     fn = "kvq_sparse_attention_nvfp4"
+    if query.dim() != 3:
+        raise KvqError(fn, KVQ_ERR_SHAPE)
     stride, top = _rows_of(fn, selected, torch.int32, query.size(0))
     _attend(fn, query, key_cache, value_cache, block_table, cu_q_lens,
             context_lens, (selected,),

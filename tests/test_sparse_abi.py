@@ -264,3 +264,24 @@ def test_sparse_workspace_does_not_shrink_with_the_table(lib, sel, top):
         at = [f(total, n, 64, 8, top, sel, 16, w) for w in widths]
         assert at == sorted(at)
         assert at[-1] == at[5]
+
+
+def test_binding_dimensions(lib):
+    """Tensors of fewer or more dimensions are refused as such."""
+    a, z = attention_args()
+    for bad in (torch.zeros((), dtype=torch.bfloat16),
+                torch.zeros(5, dtype=torch.bfloat16), a[0][0], a[0][None]):
+        refused(SHAPE, kvq.kvq_tree_attention_nvfp4, bad, *a[1:], i32(5, 1),
+                *z)
+        refused(SHAPE, kvq.kvq_sparse_attention_nvfp4, bad, *a[1:], i32(5, 3),
+                32, *z)
+        refused(SHAPE, kvq.sparse_attention_workspace, bad, i32(5, 3), a[1],
+                a[3], 32)
+    f = kvq.sparse_attention_workspace
+    refused(SHAPE, f, a[0], i32(5), a[1], a[3], 32)
+    refused(SHAPE, f, a[0], i32(5, 3), a[1][0], a[3], 32)
+    refused(SHAPE, f, a[0], i32(5, 3), a[1], a[3][0], 32)
+    s = torch.zeros(4, 5)
+    for bad in (s[0], s[None], torch.zeros(())):
+        refused(SHAPE, kvq.kvq_select_blocks, bad, i32(3), i32(2), i32(4, 2),
+                64)
