@@ -1714,19 +1714,28 @@ int64_t chunk_workspace_bytes(int sms) {
 // five tokens of 8 sequences 25 us against 34 us.  Up to four tokens always,
 // up to eight where there are no more than one (sequence, KV head) per SM;
 // single tokens beside longer chunks too.
-// Trees the same (100 of one draft over 512 to 2560 tokens 43 us against 197, 6
-// of 4 drafts 14 against 28, of 8 drafts 22 against 29), but 5 to 8 drafts only
-// over short contexts: a row's token takes an SM 4.2 ns, a tile's 16.4 and all
-// tiles 26 us more (8 drafts over 60000 tokens of 8 heads 101 us by rows, 75 by
-// tiles), and without a launch for single drafts where there are few trees.
-constexpr int64_t kTreeRowTokens = 2400;  // of an SM, by the longest context
+// Trees the same (100 of one draft over 512 to 2560 tokens 44 us against 195, 6
+// of 4 drafts over 300 to 2000 14 against 28, of 8 drafts 22 against 29), but 5
+// to 8 drafts only over short contexts (by_rows), and without a launch for
+// single drafts where there are few trees.
+//
+// Rows take an SM as long as its share of the contexts' tokens times the
+// drafts, tiles the same for all of them.  Both are even (64 query heads on 8
+// KV heads, 1 to 18 trees) at 3200 to 3800 tokens of an SM for 5 drafts, 2000
+// to 2300 for 6, 1200 to 1800 for 7 and 800 to 1500 for 8: about 4000 / (drafts
+// - 4).  At 600, 8 drafts take 24 to 28 us by rows and 27 to 38 by tiles; at
+// 2300, 73 to 79 and 52 to 63.  With 16 heads to a KV head they are even at 1000
+// to 1300 for 5 drafts and below 600 for 8.
+static bool by_rows(const ChunkParams& p) {
+  const int64_t tokens = static_cast<int64_t>(p.num_seqs) * p.Hkv * p.len_cap;
+  const int64_t sms = sm_count();
+  return p.G <= 8 ? tokens * (p.max_q_len - 4) <= 4000 * sms
+                  : tokens * (p.max_q_len - 2) <= 3000 * sms;
+}
 static int short_chunk(const ChunkParams& p, bool tree) {
   if (p.max_q_len <= 4) return p.max_q_len > 1 ? p.max_q_len : 1;
-  const int64_t each = static_cast<int64_t>(p.num_seqs) * p.Hkv;
-  const bool few = each <= sm_count();
-  if (few && p.max_q_len <= 8 &&
-      (!tree || each * p.len_cap <= kTreeRowTokens * sm_count()))
-    return p.max_q_len;
+  const bool few = static_cast<int64_t>(p.num_seqs) * p.Hkv <= sm_count();
+  if (few && p.max_q_len <= 8 && (!tree || by_rows(p))) return p.max_q_len;
   return few && tree ? 0 : 1;
 }
 

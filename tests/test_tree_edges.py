@@ -1,12 +1,13 @@
 """kvq_tree_attention_nvfp4 on the GPU: chunks longer than max_q_len, and NaN
 scales of several drafts, by rows and by tiles."""
-import numpy as np
 import pytest
+import torch
 
 from paged_quantized_kv_gb300 import kvq
 from tests.sparse_models import tree_tokens
 from tests.test_sparse_edges import check_v_nan
 from tests.test_tree_attention import Tree
+from tests.variant_build import build_variant
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,36 @@ def test_nan_of_two_drafts_by_rows(n, ctx):
     c.mask[2, 0] |= 0b10
     hit = check_v_nan(c, 0, tree_tokens(c.mask), [(ctx, 0), (ctx + 1, 0)])
     assert hit[:3].all() and not hit[3:].any()
+
+
+# ---------------------------------------------------------------------------
+# by rows or by tiles
+# ---------------------------------------------------------------------------
+@pytest.fixture(scope="module")
+def telling_library(tmp_path_factory):
+    """A softmax warp of the tiles' kernel gives up: a call says
+    KVQ_DEVERR_TIMEOUT if it has tiles."""
+    return build_variant(tmp_path_factory.mktemp("kvq_tell"), {
+        "chunk_attention.cu": {"KVQ_TEST_GIVE_UP": 1,
+                               "KVQ_WAIT_LIMIT_NS": 20000000}})
+
+
+# per: tokens of the contexts for each multiprocessor and KV head.  Measured
+# well away from where both are even: 8 drafts at 2300 took 73 to 79 us by rows
+# and 52 to 63 by tiles, at 600 24 to 28 and 27 to 38.
+@pytest.mark.parametrize("drafts,per,G,tiles", [
+    (4, 6000, 8, False), (5, 2300, 8, False), (5, 6000, 8, True),
+    (6, 1500, 8, False), (6, 4000, 8, True), (7, 1000, 8, False),
+    (7, 2300, 8, True), (8, 600, 8, False), (8, 2300, 8, True),
+    (8, 600, 1, False), (8, 2300, 1, True), (5, 600, 16, False),
+    (5, 2300, 16, True), (8, 300, 16, False), (8, 1000, 16, True),
+    (9, 100, 8, True)])
+def test_rows_or_tiles(telling_library, monkeypatch, drafts, per, G, tiles):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    c = Tree([drafts] * 4, [per * sms // 8] * 4, hq=2 * G, hkv=2)
+    monkeypatch.setattr(kvq, "LIB_PATH", telling_library)
+    monkeypatch.setattr(kvq, "_lib", None)
+    c.upload()
+    c.call(max_context_len=per * sms // 8)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == (kvq.KVQ_DEVERR_TIMEOUT if tiles else 0)
