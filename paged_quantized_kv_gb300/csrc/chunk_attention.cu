@@ -43,7 +43,7 @@
 //
 // The same kernel, as instantiations of their own (kMode), for trees of drafts
 // (a row's mask among the newest tokens: 32 trees of 33 to 64 drafts over 2000
-// to 8000 tokens, 244 GFLOP, 299 us, 815 TFLOP/s: 264 to 512 rows in tiles of
+// to 8000 tokens, 244 GFLOP, 301 us, 810 TFLOP/s: 264 to 512 rows in tiles of
 // 128, two to an item) and for blocks of lists (a row's mask of the blocks that
 // its item selects; see sparse_attention.cu).
 #include <cuda_runtime.h>

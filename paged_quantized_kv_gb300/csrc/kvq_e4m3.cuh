@@ -48,9 +48,11 @@ __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
 }
 
 // Four elements (two packed pairs) -> their four e4m3 codes, element 0 in
-// the low byte: q0 = k y, r = k + q0 (-scale), q1 = q0 + r y as packed IEEE
+// the low byte: q0 = k y, r = k + q0 (-scale), q1 = q0 + r y (P. Markstein's
+// quotient correction, IBM J. Res. Dev. 34(1), 1990) as packed IEEE
 // products and fused multiply-adds (two elements per f32x2 instruction),
-// then cvt.rn.satfinite.e4m3x2.f32.  y2 = {y, y}, ns2 = {-scale, -scale}.
+// then cvt.rn.satfinite.e4m3x2.f32.  The codes are those of the IEEE quotients,
+// which tests/quotient_exhaustive.c shows for every pair of inputs.  y2 = {y, y}, ns2 = {-scale, -scale}.
 __device__ __forceinline__ uint32_t codes4(uint64_t x01, uint64_t x23,
                                            uint64_t y2, uint64_t ns2) {
   uint32_t out;

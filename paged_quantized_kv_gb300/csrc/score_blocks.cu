@@ -21,14 +21,18 @@
 // Rows of one sequence share a tile: up to 512 columns for longer chunks, so
 // that a tile is read once for 8 rows of 64 heads.
 //
-// Measured: 1024 rows of 64 heads over 24576 tokens (404 GFLOP) 285 us, 1.42
-// PFLOP/s; 77 rows of 48 sequences over 9001 to 33333 tokens (130 MB) 37 us,
-// 3.5 TB/s, 53 % of the measured copy rate.  The first is bound by the
-// warpgroups' arithmetic: 3.5 cycles for a column of 32 tokens on each quarter
-// of the SM with four warps at work (2 of them the maximum with 0, whose unit
-// takes a warp's in 2 cycles), against 256 cycles of products for 128 x 128 x
-// 128.  The second by the hand-overs of a tile between the roles, some 700
-// cycles, in which a tile's 16.9 KB would come in 735 at the copy rate.
+// Measured: 1024 rows of 64 heads over 24576 tokens (404 GFLOP) 284 us, 1.42
+// PFLOP/s; 77 rows of 48 sequences over 9001 to 33333 tokens (130 MB) 35 us,
+// 3.7 TB/s, 55 % of the measured copy rate.  In copies with wrong results the
+// first took 114 us without the sums over the heads and 84 without the products
+// as well: the sums bound it.  No unit of theirs is full (57 % of the ALU's
+// cycles, 20 % of the FMA's, 68 % of the issue slots): it took 248 us without
+// the maximum with 0 and 269 without the weights' loads, and the rest is what a
+// warp waits for from one load of 32 columns to the next, which the three others
+// of its quarter cover in part.  The second took 29 us without the sums and 28
+// without the products too, and takes 8 over contexts of two tokens: 7 us to
+// start and to end, 21 for the copies (6.2 TB/s), 7 for sums that the copies do
+// not cover.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>

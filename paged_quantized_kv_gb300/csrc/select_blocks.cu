@@ -17,7 +17,10 @@
 // 4096 rows of 1563 to 2048 blocks, 32 of each (32 MB): 34 us, 0.94 TB/s.
 // Bound by a row's chain of latencies (its sequence, its scores, the counts) at
 // 12 warps an SM, whose registers hold the keys; with the same keys searched
-// whole, without the bound that leaves a few of them, 40 us.
+// whole, without the bound that leaves a few of them, 40 us.  Longer rows are
+// far slower: 4096 of 2049 blocks 398 us, of 4096 and 8192 blocks 383.  Of their
+// thread blocks (243 registers, 256 threads) an SM takes one at a time, and all
+// of its keys are searched bit by bit, with a barrier each.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -16,11 +16,11 @@
 // tables of the rows that are left.
 //
 // Measured, blocks of 64 tokens, 32 a row, 64 query and 8 KV heads: 64 single
-// tokens (153 MB) 40 us, 3.8 TB/s, of which 5 us are the rows' tables and 4 the
+// tokens (153 MB) 37 us, 4.1 TB/s, of which 5 us are the rows' tables and 4 the
 // join of a row's two stretches (the decode kernel's own 32 us: 0.71 of the
-// measured copy rate).  1024 rows over 32768 tokens 254 to 263 us: of the 69
+// measured copy rate).  1024 rows over 32768 tokens 254 us: of the 69
 // GFLOP that the rows ask for the tiles do 2.8 times as many, for the 90 blocks
-// that 32 rows select together, at 853 TFLOP/s; by rows alone 441 us.  Items of
+// that 32 rows select together, at 853 TFLOP/s; by rows alone 422 us.  Items of
 // 16 rows would select 78 blocks together for half the rows.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -46,7 +46,10 @@ constexpr int kMaxUnion = 8192;    // blocks of a context that items can name
 constexpr int kTileCost = 500, kTileItem = 3;
 
 // Tokens of all rows and KV heads from which on items are looked at (test
-// builds: always).
+// builds: always).  Measured by rows and by tiles, 1 and 8 sequences, 1 to 8
+// query heads to a KV head, 512 and 2048 tokens a row: at 2.5 million 66 to 75 us
+// and 71 to 100, at 3.3 85 to 96 and 73 to 119, at 4.2 106 to 120 and 75 to 122,
+// at 16.8 422 and 201 to 254.
 #ifndef KVQ_SPARSE_ITEMS_FROM
 #define KVQ_SPARSE_ITEMS_FROM 2500000
 #endif
@@ -335,7 +338,8 @@ cudaError_t launch_sparse_attention(const SparseParams& caller,
   p.row_lens = reinterpret_cast<int32_t*>(c.workspace + space.row_lens);
   p.row_table = reinterpret_cast<int32_t*>(c.workspace + space.row_table);
   // (and where there is enough to do: else the decode kernel spreads its rows
-  // over the SMs at once, 82 rows of 640 tokens in 10 us, by tiles in 45)
+  // over the SMs at once, 82 rows of 640 tokens of 8 KV heads in a call of 21 us,
+  // by tiles of 50)
   const bool items = space.num_items > 0 && c.max_q_len > Space::kFewRows &&
                      c.total_q * c.Hkv * std::min<int64_t>(tokens, c.len_cap) >
                          kItemsFrom;
