@@ -248,6 +248,7 @@ kvq_status kvq_gather_indexer_k(const uint8_t* kv_cache, int64_t block_stride,
   p.total = total_tokens;
   p.B = block_size;
   p.D = head_dim;
+  p.max_blocks = max_blocks_per_seq;
   p.num_seqs = num_seqs;
   p.early_read = (flags & KVQ_F_PDL_EARLY_READ) != 0u;
   p.early_meta = p.early_read || (flags & KVQ_F_PDL_EARLY_META) != 0u;
@@ -350,6 +351,7 @@ kvq_status kvq_load_nvfp4(const uint8_t* key_cache, const uint8_t* value_cache,
   if (passes >= (int64_t{1} << 31)) return KVQ_ERR_SHAPE;
   p.num_passes = static_cast<int32_t>(passes);
   p.num_seqs = num_seqs;
+  p.max_blocks = max_blocks_per_seq;
   p.swizzle_sides = 2u | ((flags & KVQ_F_SWIZZLE_K_SCALE) ? 1u : 0u);
   p.early_meta = (flags & KVQ_F_PDL_EARLY_META) != 0u;
   p.pdl = p.early_meta || (flags & KVQ_F_PDL) != 0u;
