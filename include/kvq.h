@@ -701,14 +701,14 @@ kvq_status kvq_select_blocks(const float* scores, int64_t scores_stride0,
  * before it, or whose block holds nothing that the row could see, is skipped
  * and flagged (KVQ_DEVERR_SEQ).
  * Arithmetic: as for kvq_chunk_attention_nvfp4.
- * Chunks of more than four tokens whose rows select much the same blocks are
- * computed together, as tiles (decided on the device, for each group of rows),
- * where select_block is a power of two from 16 on and the longest context that
- * the call allows -- max_context_len, else the width of block_table -- has at
- * most 8192 blocks of select_block tokens.  Elsewhere every row is computed by
- * itself, which takes a prompt up to two and a half times as long (1024 rows,
- * 2048 of 32768 tokens of 64 query and 8 KV heads: 421 us for 174): give
- * max_context_len with a wide block_table.
+ * In batches with enough to do, chunks of more than four tokens whose rows
+ * select much the same blocks are computed together, as tiles (decided on the
+ * device, for each group of rows), where select_block is a power of two from 16
+ * on and the longest context that the call allows -- max_context_len, else the
+ * width of block_table -- has at most 8192 blocks of select_block tokens.
+ * Elsewhere every row is computed by itself, which takes a prompt up to two and
+ * a half times as long (1024 rows, 2048 of 32768 tokens of 64 query and 8 KV
+ * heads: 421 us for 174): give max_context_len with a wide block_table.
  *
  * selected       int32 [total_q, max_selected], rows selected_stride0 apart
  *                (those of kvq_select_blocks).
